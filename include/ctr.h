@@ -508,6 +508,153 @@ ctr_status ctr_istft_describe(ctr_istft_t plan, char *buf, size_t len);
 ctr_status ctr_istft_set_timing_events(ctr_istft_t plan, void *before, void *after);
 void ctr_istft_destroy(ctr_istft_t plan);
 
+/* ------------------------------------------------------------------------------------
+ * Attention of one new token over a paged key-value cache.
+ *
+ * The decode step of an autoregressive model that feeds the streaming upsamplers above with
+ * frames: for each of B sequences, one query per head reads the keys and values of all
+ * tokens so far, which lie in fixed-size pages that a table lists:
+ *
+ *     n    = lens[b] + (k_new ? 1 : 0)            tokens, slots 0 .. n - 1
+ *     lo   = window > 0 ? max(0, n - window) : 0   first slot that is attended to
+ *     p[j] = softmax over lo <= j < n of  scale * (q[b, h] . K[j, h / (H_q / H_kv)])
+ *     out[b, h] = sum over j of p[j] * V[j, h / (H_q / H_kv)]          (0 when n = 0)
+ *
+ * Slot j of sequence b is row j % page_size of page tables[b][j / page_size].  With k_new and
+ * v_new the call first puts them at slot lens[b] (in the same launch); the caller advances
+ * lens afterwards.  lens[b] < 0 marks an idle row: nothing is written to the cache, out = 0.
+ * With weights enabled the call also accumulates the attention weight of every slot,
+ *
+ *     weights_out[b, hk, j] = (j < lens[b] ? weights_in[b, hk, j] : 0)
+ *                             + sum over the heads h of hk's group of p[j]      (0 <= j < n)
+ *
+ * which ctr_attn_evict uses to choose what a full cache gives up.
+ *
+ * Buffers (device, contiguous unless a stride is given; q, k_new, v_new, the pages, out and
+ * their strides in bytes on 16-byte boundaries, the int32 and fp32 arrays on their elements'):
+ *   q             [B][H_q][D] in the plan's dtype, q_stride elements from row b to b + 1
+ *   k_new, v_new  [B][H_kv][D], kv_stride elements between rows; both or neither NULL
+ *   k_pages, v_pages  [num_pages][H_kv][page_size][D] (CTR_CACHE_HEAD_MAJOR) or
+ *                 [num_pages][page_size][H_kv][D] (CTR_CACHE_TOKEN_MAJOR), bound to the plan
+ *   tables        [B][max_pages] int32 page numbers; entries past a sequence's last page are
+ *                 not read
+ *   lens          [B] int32
+ *   weights_in, weights_out  [B][H_kv][max_pages * page_size] fp32; may be the same buffer;
+ *                 weights_in NULL reads as zeros; slots >= n are left alone
+ *   out           [B][H_q][D]
+ * Rows of stale pages past a sequence's end may hold anything, NaN included.
+ *
+ * Sums, softmax statistics and weights are fp32; out is rounded once to the dtype.  The
+ * result does not depend on timing: partial results join in a fixed order.
+ * A page number outside [0, num_pages) hides its slots, and a length past the table's capacity
+ * is cut to it (without room for the new row, which is then not put); ctr_attn_check reports
+ * either as CTR_ERR_INVALID_ARG.  Two sequences may share pages that neither appends to.
+ * ------------------------------------------------------------------------------------ */
+typedef struct ctr_attn_s *ctr_attn_t;
+
+typedef enum {
+    CTR_CACHE_HEAD_MAJOR = 0,   /* pages [H_kv][page_size][D] (default) */
+    CTR_CACHE_TOKEN_MAJOR = 1   /* pages [page_size][H_kv][D] */
+} ctr_cache_layout;
+
+/*
+ * Create an attention plan (host only).  1 <= B <= 4096; 1 <= H_kv, H_q a multiple of it,
+ * H_q / H_kv <= 128; D a multiple of 16 up to 256; page_size >= 1; max_pages >= 1;
+ * B * H_kv <= 2^20, max_pages * page_size <= 2^28.  dtype: CTR_F32, CTR_BF16 or CTR_F16.
+ * CTR_ERR_INVALID_ARG for sizes < 1 or H_q no multiple of H_kv, CTR_ERR_UNSUPPORTED
+ * beyond the limits.
+ */
+ctr_status ctr_attn_create(ctr_attn_t *out, int64_t B, int64_t H_q, int64_t H_kv, int64_t D,
+                           int64_t page_size, int64_t max_pages, int dtype);
+/* Page layout (default CTR_CACHE_HEAD_MAJOR).  Host only, as the next three calls. */
+ctr_status ctr_attn_set_layout(ctr_attn_t plan, int layout);
+/* Score scale (default 1 / sqrt(D)); must be finite. */
+ctr_status ctr_attn_set_scale(ctr_attn_t plan, float scale);
+/* Attend to the last `window` slots only (default 0 = all). */
+ctr_status ctr_attn_set_window(ctr_attn_t plan, int64_t window);
+/* Accumulate weights (default 0): the workspace then also holds one fp32 score per query head
+ * and slot.  Unbinds the workspace. */
+ctr_status ctr_attn_set_weights(ctr_attn_t plan, int enable);
+size_t ctr_attn_workspace_bytes(ctr_attn_t plan);
+/* Bind a caller-owned workspace (256-byte aligned), as ctr_plan_bind_workspace. */
+ctr_status ctr_attn_bind_workspace(ctr_attn_t plan, void *dev_ptr, size_t bytes);
+/* Clear the workspace's counters and status word (asynchronous on stream): once after each
+ * ctr_attn_bind_workspace, before the first ctr_attn_forward (CTR_ERR_NOT_PREPARED
+ * otherwise).  The calls themselves leave the counters cleared. */
+ctr_status ctr_attn_reset(ctr_attn_t plan, void *stream);
+/* Bind the caller-owned cache pages; they must stay allocated while bound. */
+ctr_status ctr_attn_bind_cache(ctr_attn_t plan, void *k_pages, void *v_pages, int64_t num_pages);
+/* One decode step.  Asynchronous on stream; never allocates or synchronises.  weights_out is
+ * required when weights are enabled and must be NULL (as weights_in) otherwise. */
+ctr_status ctr_attn_forward(ctr_attn_t plan, const void *q, int64_t q_stride, const void *k_new,
+                            const void *v_new, int64_t kv_stride, const int32_t *tables,
+                            const int32_t *lens, const float *weights_in, float *weights_out,
+                            void *out, void *stream);
+/*
+ * Evict from the cache by accumulated attention weight: of the lens[b] slots of every
+ * (sequence, KV head) keep n = min(lens[b], budget) -- the first `sinks`, the last `recent`,
+ * and of the others those with the largest weight (ties: the lowest slot; NaN counts as
+ * lowest) -- and copy their K and V rows, in slot order, to slots 0 .. n - 1 of the pages in
+ * dst_tables.  Each head keeps slots of its own.  The source pages are not changed, so pages
+ * shared with other sequences stay valid; no destination page may be a source page or occur
+ * twice.
+ *   weights      [B][H_kv][max_pages * page_size] fp32
+ *   dst_tables   [B][dst_pitch] int32, dst_pitch >= ceil(budget / page_size)
+ *   slots        [B][H_kv][budget] int32: the kept slots, ascending, then -1
+ *   lens_out     [B] int32: n (lens[b] itself for an idle row); may not be lens
+ *   weights_out  [B][H_kv][weights_pitch] fp32, weights_pitch >= budget: the kept weights,
+ *                entries from n on left alone; NULL or != weights
+ * Requires budget >= 1 and sinks + recent <= budget (CTR_ERR_INVALID_ARG).  Page numbers out
+ * of range are skipped and reported by ctr_attn_check, as above.  Needs the bound cache and,
+ * for the status word, the workspace.
+ */
+ctr_status ctr_attn_evict(ctr_attn_t plan, const int32_t *tables, const int32_t *lens,
+                          const float *weights, const int32_t *dst_tables, int64_t dst_pitch,
+                          int64_t budget, int64_t sinks, int64_t recent, int32_t *slots,
+                          int32_t *lens_out, float *weights_out, int64_t weights_pitch,
+                          void *stream);
+/* Synchronise stream, then read and clear the status word: CTR_OK, CTR_ERR_INVALID_ARG when a
+ * call since the last check met a page number or length out of range, or CTR_ERR_CUDA. */
+ctr_status ctr_attn_check(ctr_attn_t plan, void *stream);
+ctr_status ctr_attn_describe(ctr_attn_t plan, char *buf, size_t len);
+void ctr_attn_destroy(ctr_attn_t plan);
+
+/* ------------------------------------------------------------------------------------
+ * Sampling the next token (a code of the codec) from logits and given random numbers.
+ *
+ * Per row, with l the logits as fp32 (NaN reads as -inf), m their maximum, the order (l
+ * descending, index ascending) and w_i = exp((l_i - m) / T), 1 where l_i = m, kept is the
+ * shortest of these prefixes of the order, but at least its first token:
+ *     T <= 0        the first token (greedy)
+ *     top_k > 0     the first top_k tokens
+ *     top_p < 1     the tokens with (mass of the tokens before them) < top_p * (mass of the
+ *                   top_k tokens)
+ *     min_p > 0     the tokens with w_i >= min_p
+ * and the token is the kept one with the largest w_i / max(noise_i, FLT_MIN) (ties: the lowest
+ * index).  With independent Exp(1) numbers as noise this is a draw from the kept tokens in
+ * proportion to w (the exponential race).  A token with l_i = -inf is never drawn; a row
+ * of nothing else gives -1.  Masses are summed in 64-bit fixed point, so the kept set does
+ * not depend on the order of summation.
+ *
+ *   logits   [rows][vocab] in the plan's dtype, row stride in elements (any, >= vocab)
+ *   noise    [rows][vocab] fp32, row stride in elements
+ *   temperature, top_p, min_p  [rows] fp32 or NULL (1, 1 and 0);  top_k  [rows] int32 or NULL
+ *   tokens   [rows] int64
+ * Every buffer is aligned to its elements (CTR_ERR_MISALIGNED otherwise), so a slice of a
+ * larger tensor will do.  1 <= vocab <= 2^20, 0 <= rows <= 2^20.  No workspace;
+ * ctr_sampler_forward is asynchronous on stream and never allocates or synchronises.
+ * ------------------------------------------------------------------------------------ */
+typedef struct ctr_sampler_s *ctr_sampler_t;
+
+ctr_status ctr_sampler_create(ctr_sampler_t *out, int64_t rows, int64_t vocab, int dtype);
+ctr_status ctr_sampler_forward(ctr_sampler_t plan, const void *logits, int64_t logits_stride,
+                               const float *noise, int64_t noise_stride,
+                               const float *temperature, const int32_t *top_k,
+                               const float *top_p, const float *min_p, int64_t *tokens,
+                               void *stream);
+ctr_status ctr_sampler_describe(ctr_sampler_t plan, char *buf, size_t len);
+void ctr_sampler_destroy(ctr_sampler_t plan);
+
 #ifdef __cplusplus
 }
 #endif

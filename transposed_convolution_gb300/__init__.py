@@ -21,8 +21,16 @@ Inverse STFT (same names as the C ABI): ``ctr_istft_create``, ``ctr_istft_output
 ``ctr_istft_forward``, ``ctr_istft_describe``, ``ctr_istft_set_timing_events``,
 ``ctr_istft_destroy``.
 
+Decode step of the model that writes a codec's frames (same names as the C ABI):
+``ctr_attn_create``, ``ctr_attn_set_layout``, ``ctr_attn_set_scale``, ``ctr_attn_set_window``,
+``ctr_attn_set_weights``, ``ctr_attn_workspace_bytes``, ``ctr_attn_bind_workspace``,
+``ctr_attn_reset``, ``ctr_attn_bind_cache``, ``ctr_attn_forward``, ``ctr_attn_evict``,
+``ctr_attn_check``, ``ctr_attn_describe``, ``ctr_attn_destroy``, ``ctr_sampler_create``,
+``ctr_sampler_forward``, ``ctr_sampler_describe``, ``ctr_sampler_destroy``.
+
 High level: ``Plan`` (a plan with its packed weight and workspace held as torch tensors),
-``Istft`` (an inverse-STFT plan with its workspace), and
+``Istft`` (an inverse-STFT plan with its workspace), ``PagedAttention`` (attention of one new
+token over a paged cache, and eviction from it), ``Sampler`` (next-token sampling), and
 ``conv_transpose(x, w, bias, stride, padding, output_padding, negative_slope, groups)``.
 """
 from __future__ import annotations
@@ -60,6 +68,8 @@ CTR_AUTO_PAD_VALID = 3
 CTR_PHASE_AUTO = 0
 CTR_PHASE_UNPADDED = 1
 CTR_PHASE_OUTPUT = 2
+CTR_CACHE_HEAD_MAJOR = 0
+CTR_CACHE_TOKEN_MAJOR = 1
 PATH_NAMES = {CTR_PATH_POLYPHASE: "polyphase", CTR_PATH_COL2IM: "col2im", CTR_PATH_GATHER: "gather",
               CTR_PATH_DEPTHWISE: "depthwise"}
 
@@ -110,6 +120,28 @@ SIGNATURES = {
     "ctr_istft_describe": (ctypes.c_int, [_vp, ctypes.c_char_p, ctypes.c_size_t]),
     "ctr_istft_set_timing_events": (ctypes.c_int, [_vp, _vp, _vp]),
     "ctr_istft_destroy": (None, [_vp]),
+    "ctr_attn_create": (ctypes.c_int, [ctypes.POINTER(_vp)] + [ctypes.c_int64] * 6 + [ctypes.c_int]),
+    "ctr_attn_set_layout": (ctypes.c_int, [_vp, ctypes.c_int]),
+    "ctr_attn_set_scale": (ctypes.c_int, [_vp, ctypes.c_float]),
+    "ctr_attn_set_window": (ctypes.c_int, [_vp, ctypes.c_int64]),
+    "ctr_attn_set_weights": (ctypes.c_int, [_vp, ctypes.c_int]),
+    "ctr_attn_workspace_bytes": (ctypes.c_size_t, [_vp]),
+    "ctr_attn_bind_workspace": (ctypes.c_int, [_vp, _vp, ctypes.c_size_t]),
+    "ctr_attn_reset": (ctypes.c_int, [_vp, _vp]),
+    "ctr_attn_bind_cache": (ctypes.c_int, [_vp, _vp, _vp, ctypes.c_int64]),
+    "ctr_attn_forward": (ctypes.c_int, [_vp, _vp, ctypes.c_int64, _vp, _vp, ctypes.c_int64, _vp, _vp,
+                                        _vp, _vp, _vp, _vp]),
+    "ctr_attn_evict": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp] + [ctypes.c_int64] * 4
+                       + [_vp, _vp, _vp, ctypes.c_int64, _vp]),
+    "ctr_attn_check": (ctypes.c_int, [_vp, _vp]),
+    "ctr_attn_describe": (ctypes.c_int, [_vp, ctypes.c_char_p, ctypes.c_size_t]),
+    "ctr_attn_destroy": (None, [_vp]),
+    "ctr_sampler_create": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.c_int64, ctypes.c_int64,
+                                          ctypes.c_int]),
+    "ctr_sampler_forward": (ctypes.c_int, [_vp, _vp, ctypes.c_int64, _vp, ctypes.c_int64, _vp, _vp, _vp,
+                                           _vp, _vp, _vp]),
+    "ctr_sampler_describe": (ctypes.c_int, [_vp, ctypes.c_char_p, ctypes.c_size_t]),
+    "ctr_sampler_destroy": (None, [_vp]),
 }
 
 
@@ -346,6 +378,100 @@ def ctr_istft_set_timing_events(plan, before, after):
 
 def ctr_istft_destroy(plan):
     lib.ctr_istft_destroy(plan)
+
+
+def ctr_attn_create(B, H_q, H_kv, D, page_size, max_pages, dtype=CTR_F32):
+    """Returns an attention plan handle (int).  Raises CtrError on a non-OK status."""
+    h = _vp()
+    _check(lib.ctr_attn_create(ctypes.byref(h), int(B), int(H_q), int(H_kv), int(D), int(page_size),
+                               int(max_pages), int(dtype)), "ctr_attn_create")
+    return h.value
+
+
+def ctr_attn_set_layout(plan, layout):
+    _check(lib.ctr_attn_set_layout(plan, int(layout)), "ctr_attn_set_layout")
+
+
+def ctr_attn_set_scale(plan, scale):
+    _check(lib.ctr_attn_set_scale(plan, float(scale)), "ctr_attn_set_scale")
+
+
+def ctr_attn_set_window(plan, window):
+    _check(lib.ctr_attn_set_window(plan, int(window)), "ctr_attn_set_window")
+
+
+def ctr_attn_set_weights(plan, enable):
+    _check(lib.ctr_attn_set_weights(plan, int(enable)), "ctr_attn_set_weights")
+
+
+def ctr_attn_workspace_bytes(plan) -> int:
+    return int(lib.ctr_attn_workspace_bytes(plan))
+
+
+def ctr_attn_bind_workspace(plan, ptr, nbytes):
+    _check(lib.ctr_attn_bind_workspace(plan, ptr, int(nbytes)), "ctr_attn_bind_workspace")
+
+
+def ctr_attn_reset(plan, stream):
+    _check(lib.ctr_attn_reset(plan, stream), "ctr_attn_reset")
+
+
+def ctr_attn_bind_cache(plan, k_pages_ptr, v_pages_ptr, num_pages):
+    _check(lib.ctr_attn_bind_cache(plan, k_pages_ptr, v_pages_ptr, int(num_pages)),
+           "ctr_attn_bind_cache")
+
+
+def ctr_attn_forward(plan, q_ptr, q_stride, k_new_ptr, v_new_ptr, kv_stride, tables_ptr, lens_ptr,
+                     weights_in_ptr, weights_out_ptr, out_ptr, stream):
+    _check(lib.ctr_attn_forward(plan, q_ptr, q_stride, k_new_ptr, v_new_ptr, kv_stride, tables_ptr,
+                                lens_ptr, weights_in_ptr, weights_out_ptr, out_ptr, stream),
+           "ctr_attn_forward")
+
+
+def ctr_attn_evict(plan, tables_ptr, lens_ptr, weights_ptr, dst_tables_ptr, dst_pitch, budget, sinks,
+                   recent, slots_ptr, lens_out_ptr, weights_out_ptr, weights_pitch, stream):
+    _check(lib.ctr_attn_evict(plan, tables_ptr, lens_ptr, weights_ptr, dst_tables_ptr, dst_pitch,
+                              budget, sinks, recent, slots_ptr, lens_out_ptr, weights_out_ptr,
+                              weights_pitch, stream), "ctr_attn_evict")
+
+
+def ctr_attn_check(plan, stream):
+    _check(lib.ctr_attn_check(plan, stream), "ctr_attn_check")
+
+
+def ctr_attn_describe(plan) -> str:
+    buf = ctypes.create_string_buffer(256)
+    _check(lib.ctr_attn_describe(plan, buf, 256), "ctr_attn_describe")
+    return buf.value.decode()
+
+
+def ctr_attn_destroy(plan):
+    lib.ctr_attn_destroy(plan)
+
+
+def ctr_sampler_create(rows, vocab, dtype=CTR_F32):
+    """Returns a sampler plan handle (int).  Raises CtrError on a non-OK status."""
+    h = _vp()
+    _check(lib.ctr_sampler_create(ctypes.byref(h), int(rows), int(vocab), int(dtype)),
+           "ctr_sampler_create")
+    return h.value
+
+
+def ctr_sampler_forward(plan, logits_ptr, logits_stride, noise_ptr, noise_stride, temperature_ptr,
+                        top_k_ptr, top_p_ptr, min_p_ptr, tokens_ptr, stream):
+    _check(lib.ctr_sampler_forward(plan, logits_ptr, logits_stride, noise_ptr, noise_stride,
+                                   temperature_ptr, top_k_ptr, top_p_ptr, min_p_ptr, tokens_ptr,
+                                   stream), "ctr_sampler_forward")
+
+
+def ctr_sampler_describe(plan) -> str:
+    buf = ctypes.create_string_buffer(256)
+    _check(lib.ctr_sampler_describe(plan, buf, 256), "ctr_sampler_describe")
+    return buf.value.decode()
+
+
+def ctr_sampler_destroy(plan):
+    lib.ctr_sampler_destroy(plan)
 
 
 # ------------------------------------------------------------------ torch-level helpers
@@ -678,3 +804,11 @@ def conv_transpose(x, w, bias=None, stride=1, padding=0, output_padding=0, negat
         plan.prepack(w.contiguous())
         _plan_cache[key] = plan
     return plan.forward(x.contiguous(), None if bias is None else bias.contiguous())
+
+
+def __getattr__(name):
+    """PagedAttention and Sampler, imported when first used (their module imports torch)."""
+    if name in ("PagedAttention", "Sampler"):
+        from . import decode
+        return getattr(decode, name)
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))

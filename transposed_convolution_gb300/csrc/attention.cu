@@ -1,0 +1,132 @@
+// attention.cu -- attention of one new token over the paged cache.
+#include <algorithm>
+
+#include "decode_device.cuh"
+
+namespace ctr {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr float kNegInf = -__builtin_inff();
+
+__device__ float block_reduce(float v, bool is_max, float *red) {
+    for (int o = 16; o; o >>= 1) {
+        const float u = __shfl_xor_sync(0xffffffffu, v, o);
+        v = is_max ? fmaxf(v, u) : v + u;
+    }
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = red[0];
+    for (int i = 1; i < kThreads / 32; ++i) v = is_max ? fmaxf(v, red[i]) : v + red[i];
+    return v;
+}
+
+template <typename T>
+__global__ void append_kernel(AttnParams p) {
+    const int h = blockIdx.x, b = blockIdx.y;
+    int len;
+    const int n = tokens_of(p.cache, b, true, &len);
+    if (n <= len || len < 0) return;
+    const int64_t at = slot_offset(p.cache, b, h, len);
+    if (at < 0) return;
+    const int64_t src = b * p.kv_stride + (int64_t)h * p.D;
+    for (int d = threadIdx.x; d < p.D; d += blockDim.x) {
+        static_cast<T *>(p.k)[at + d] = static_cast<const T *>(p.k_new)[src + d];
+        static_cast<T *>(p.v)[at + d] = static_cast<const T *>(p.v_new)[src + d];
+    }
+}
+
+// One block per (query head, sequence): chunks of 128 slots with the running maximum and sum of
+// the softmax; a thread per slot for the scores, a thread per column for the products with V.
+template <typename T>
+__global__ void attention_kernel(AttnParams p) {
+    __shared__ float qs[256], ps[kThreads], red[kThreads / 32];
+    __shared__ int64_t offs[kThreads];
+    const int h = blockIdx.x, b = blockIdx.y, t = threadIdx.x, hk = h / p.G;
+    int len;
+    const int n = tokens_of(p.cache, b, p.k_new != nullptr, &len);
+    const int lo = p.window > 0 && n > p.window ? n - (int)p.window : 0;
+    for (int d = t; d < p.D; d += kThreads)
+        qs[d] = to_f(static_cast<const T *>(p.q)[b * p.q_stride + (int64_t)h * p.D + d]);
+    float m = kNegInf, l = 0.0f, acc[2] = {0.0f, 0.0f};
+    float *scores = p.scores ? p.scores + ((int64_t)b * p.Hq + h) * p.cache.cap : nullptr;
+    for (int base = lo; base < n; base += kThreads) {
+        __syncthreads();
+        const int j = base + t;
+        float s = kNegInf;
+        offs[t] = j < n ? slot_offset(p.cache, b, hk, j) : -1;
+        if (offs[t] >= 0) {
+            const T *k = static_cast<const T *>(p.k) + offs[t];
+            float dot = 0.0f;
+            for (int d = 0; d < p.D; ++d) dot = fmaf(qs[d], to_f(k[d]), dot);
+            s = dot * p.scale_log2;
+        }
+        if (scores && j < n) scores[j] = s;
+        const float m2 = fmaxf(m, block_reduce(s, true, red));
+        const float base_m = m2 == kNegInf ? 0.0f : m2;
+        const float e = exp2f(s - base_m), shrink = exp2f(m - base_m);
+        ps[t] = e;
+        l = l * shrink + block_reduce(e, false, red);
+        m = m2;
+        for (int i = 0; i < 2; ++i) {
+            const int d = t + i * kThreads;
+            if (d >= p.D) continue;
+            float a = acc[i] * shrink;
+            for (int r = 0; r < kThreads && base + r < n; ++r)
+                if (offs[r] >= 0) a = fmaf(ps[r], to_f(static_cast<const T *>(p.v)[offs[r] + d]), a);
+            acc[i] = a;
+        }
+    }
+    for (int i = 0; i < 2; ++i) {
+        const int d = t + i * kThreads;
+        if (d < p.D)
+            static_cast<T *>(p.out)[((int64_t)b * p.Hq + h) * p.D + d] =
+                from_f<T>(l > 0.0f ? acc[i] / l : 0.0f);
+    }
+    if (scores) {
+        const float lse = l > 0.0f ? m + log2f(l) : 0.0f;
+        for (int j = lo + t; j < n; j += kThreads) scores[j] = exp2f(scores[j] - lse);
+    }
+}
+
+__global__ void weights_kernel(AttnParams p, int chunks) {
+    const int unit = blockIdx.x / chunks, hk = unit % p.Hkv, b = unit / p.Hkv;
+    int len;
+    const int n = tokens_of(p.cache, b, p.k_new != nullptr, &len);
+    const int lo = p.window > 0 && n > p.window ? n - (int)p.window : 0;
+    const int64_t base = ((int64_t)b * p.Hkv + hk) * p.cache.cap;
+    const float *s = p.scores + ((int64_t)b * p.Hq + (int64_t)hk * p.G) * p.cache.cap;
+    for (int j = blockIdx.x % chunks * blockDim.x + threadIdx.x; j < n; j += chunks * blockDim.x) {
+        float w = 0.0f;
+        if (j >= lo)
+            for (int g = 0; g < p.G; ++g) w += s[(int64_t)g * p.cache.cap + j];
+        p.w_out[base + j] = (p.w_in && j < len ? p.w_in[base + j] : 0.0f) + w;
+    }
+}
+
+template <typename T>
+cudaError_t launch(const AttnParams &p, cudaStream_t st) {
+    if (p.k_new) {
+        append_kernel<T><<<dim3(p.Hkv, p.B), kThreads, 0, st>>>(p);
+        count_launches(1);
+    }
+    attention_kernel<T><<<dim3(p.Hq, p.B), kThreads, 0, st>>>(p);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attention(const ctr_attn_s *pl, const AttnParams &p, cudaStream_t st) {
+    cudaError_t e = pl->dtype == CTR_F32    ? launch<float>(p, st)
+                    : pl->dtype == CTR_BF16 ? launch<__nv_bfloat16>(p, st)
+                                            : launch<__half>(p, st);
+    if (e != cudaSuccess || !p.w_out) return e;
+    const int chunks = std::min((p.cache.cap + 1023) / 1024, 64);
+    weights_kernel<<<(unsigned)(p.B * p.Hkv) * chunks, 256, 0, st>>>(p, chunks);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace ctr

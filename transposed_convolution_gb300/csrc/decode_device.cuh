@@ -1,0 +1,45 @@
+// decode_device.cuh -- device helpers shared by the decode-step kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "decode_internal.h"
+
+namespace ctr {
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+template <typename T> __device__ __forceinline__ T from_f(float v);
+template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
+    return __float2bfloat16_rn(v);
+}
+template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+
+// Tokens of sequence b (slots 0 .. n - 1), with the new one if there is one and room for it.
+// Reports a length past the table's capacity.
+__device__ __forceinline__ int tokens_of(const CacheView &c, int b, bool with_new, int *len) {
+    int n = c.lens[b];
+    *len = n;
+    if (n < 0) return 0;
+    if (n > c.cap - (with_new ? 1 : 0)) {
+        if (threadIdx.x == 0) atomicOr(c.status, kStatusBadLength);
+        *len = min(n, c.cap);
+        return *len;
+    }
+    return n + (with_new ? 1 : 0);
+}
+
+// First element of slot j of sequence b, or -1 when the table names no page of the cache.
+__device__ __forceinline__ int64_t slot_offset(const CacheView &c, int b, int h, int j) {
+    const int pg = c.tables[(int64_t)b * c.table_pitch + j / c.page];
+    if ((unsigned)pg >= (unsigned)c.num_pages) {
+        atomicOr(c.status, kStatusBadPage);
+        return -1;
+    }
+    return pg * c.page_stride + h * c.head_stride + (j % c.page) * c.row_stride;
+}
+
+}  // namespace ctr
