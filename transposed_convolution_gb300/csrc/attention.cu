@@ -1,7 +1,7 @@
 // attention.cu -- attention of one new token over the paged cache.
 #include <algorithm>
 
-#include "decode_device.cuh"
+#include "attention16.cuh"
 
 namespace ctr {
 namespace {
@@ -50,7 +50,7 @@ __global__ void attention_kernel(AttnParams p) {
     for (int d = t; d < p.D; d += kThreads)
         qs[d] = to_f(static_cast<const T *>(p.q)[b * p.q_stride + (int64_t)h * p.D + d]);
     float m = kNegInf, l = 0.0f, acc[2] = {0.0f, 0.0f};
-    float *scores = p.scores ? p.scores + ((int64_t)b * p.Hq + h) * p.cache.cap : nullptr;
+    float *scores = p.scores ? p.scores + ((int64_t)b * p.Hq + h) * p.score_pitch : nullptr;
     for (int base = lo; base < n; base += kThreads) {
         __syncthreads();
         const int j = base + t;
@@ -84,10 +84,7 @@ __global__ void attention_kernel(AttnParams p) {
             static_cast<T *>(p.out)[((int64_t)b * p.Hq + h) * p.D + d] =
                 from_f<T>(l > 0.0f ? acc[i] / l : 0.0f);
     }
-    if (scores) {
-        const float lse = l > 0.0f ? m + log2f(l) : 0.0f;
-        for (int j = lo + t; j < n; j += kThreads) scores[j] = exp2f(scores[j] - lse);
-    }
+    if (scores && t == 0) p.stats[(int64_t)b * p.Hq + h] = make_float2(m, l);
 }
 
 __global__ void weights_kernel(AttnParams p, int chunks) {
@@ -95,14 +92,39 @@ __global__ void weights_kernel(AttnParams p, int chunks) {
     int len;
     const int n = tokens_of(p.cache, b, p.k_new != nullptr, &len);
     const int lo = p.window > 0 && n > p.window ? n - (int)p.window : 0;
-    const int64_t base = ((int64_t)b * p.Hkv + hk) * p.cache.cap;
-    const float *s = p.scores + ((int64_t)b * p.Hq + (int64_t)hk * p.G) * p.cache.cap;
+    const int64_t base = ((int64_t)b * p.Hkv + hk) * p.cache.cap, h0 = (int64_t)b * p.Hq + hk * p.G;
     for (int j = blockIdx.x % chunks * blockDim.x + threadIdx.x; j < n; j += chunks * blockDim.x) {
         float w = 0.0f;
         if (j >= lo)
-            for (int g = 0; g < p.G; ++g) w += s[(int64_t)g * p.cache.cap + j];
+            for (int g = 0; g < p.G; ++g) {
+                const float2 st = p.stats[h0 + g];
+                if (st.y > 0.0f)
+                    w += exp2f(p.scores[(h0 + g) * p.score_pitch + j] - st.x) / st.y;
+            }
         p.w_out[base + j] = (p.w_in && j < len ? p.w_in[base + j] : 0.0f) + w;
     }
+}
+
+template <typename T, int DP>
+cudaError_t launch16(const ctr_attn_s *pl, const AttnParams &p, cudaStream_t st) {
+    static PerDeviceOnce once;
+    const auto kernel = attn16::attention16_kernel<T, DP>;
+    const cudaError_t e = once.run(current_device(), cudaSuccess, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)attn16::smem_bytes<DP>(DP, 2048));
+    });
+    if (e != cudaSuccess) return e;
+    const int per_sm = DP == 256 ? 1 : kMaxPerSm;
+    count_launches(1);
+    return launch_pdl(kernel, dim3((unsigned)(pl->num_sms * per_sm)), dim3(attn16::kThreads),
+                      attn16::smem_bytes<DP>(p.D, p.B), st, p);
+}
+
+template <typename T>
+cudaError_t launch16(const ctr_attn_s *pl, const AttnParams &p, cudaStream_t st) {
+    return p.D <= 64    ? launch16<T, 64>(pl, p, st)
+           : p.D <= 128 ? launch16<T, 128>(pl, p, st)
+                        : launch16<T, 256>(pl, p, st);
 }
 
 template <typename T>
@@ -120,8 +142,8 @@ cudaError_t launch(const AttnParams &p, cudaStream_t st) {
 
 cudaError_t launch_attention(const ctr_attn_s *pl, const AttnParams &p, cudaStream_t st) {
     cudaError_t e = pl->dtype == CTR_F32    ? launch<float>(p, st)
-                    : pl->dtype == CTR_BF16 ? launch<__nv_bfloat16>(p, st)
-                                            : launch<__half>(p, st);
+                    : pl->dtype == CTR_BF16 ? launch16<__nv_bfloat16>(pl, p, st)
+                                            : launch16<__half>(pl, p, st);
     if (e != cudaSuccess || !p.w_out) return e;
     const int chunks = std::min((p.cache.cap + 1023) / 1024, 64);
     weights_kernel<<<(unsigned)(p.B * p.Hkv) * chunks, 256, 0, st>>>(p, chunks);

@@ -12,12 +12,26 @@ size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 int esize_of(const ctr_attn_s *pl) { return pl->dtype == CTR_F32 ? 4 : 2; }
 
+// Units of work: one for each sequence, KV head and set of up to 16 of its query heads.
+int64_t units_of(const ctr_attn_s *pl) {
+    return pl->B * pl->Hkv * ((pl->Hq / pl->Hkv + 15) / 16);
+}
+
+// The status word, the units' counters (both cleared by ctr_attn_reset), the parts of shared
+// units, and with weights the softmax statistics and scores.
 void layout_workspace(ctr_attn_s *pl) {
-    pl->off_scores = 256;    // the status word in front
-    pl->ws_needed = pl->off_scores;
-    if (pl->weights)
-        pl->ws_needed += align256((size_t)(pl->B * pl->Hq) * (size_t)(pl->max_pages * pl->page) *
-                                  sizeof(float));
+    const int64_t parts = 2 * ctr::kMaxPerSm * (int64_t)pl->num_sms;
+    pl->score_pitch = (pl->max_pages * pl->page + ctr::kScoreTile - 1) / ctr::kScoreTile * ctr::kScoreTile;
+    pl->off_parts = align256(256 + (size_t)units_of(pl) * sizeof(uint32_t));
+    pl->off_ml = pl->off_parts + align256((size_t)(parts * 16 * pl->D) * sizeof(float));
+    pl->off_stats = pl->off_ml + align256((size_t)(parts * 16) * sizeof(float2));
+    pl->off_scores = pl->off_stats;
+    pl->ws_needed = pl->off_stats;
+    if (pl->weights) {
+        pl->off_scores += align256((size_t)(pl->B * pl->Hq) * sizeof(float2));
+        pl->ws_needed = pl->off_scores +
+                        (size_t)(pl->B * pl->Hq) * (size_t)pl->score_pitch * sizeof(float);
+    }
     pl->ws = nullptr;
     pl->ws_bytes = 0;
     pl->ready = 0;
@@ -50,8 +64,9 @@ ctr_status ctr_attn_create(ctr_attn_t *out, int64_t B, int64_t H_q, int64_t H_kv
     if (B < 1 || H_q < 1 || H_kv < 1 || D < 1 || page_size < 1 || max_pages < 1 || H_q % H_kv)
         return CTR_ERR_INVALID_ARG;
     const int64_t cap = (int64_t)1 << 28;
-    if (B > 4096 || H_kv > ((int64_t)1 << 20) / B || H_q / H_kv > 128 || D > 256 || D % 16 ||
-        page_size > cap || max_pages > cap / page_size)
+    if (B > 2048 || H_kv > ((int64_t)1 << 20) / B || H_q / H_kv > 128 || D > 256 || D % 16 ||
+        page_size > cap || max_pages > cap / page_size ||
+        B * page_size * max_pages > ((int64_t)1 << 36))
         return CTR_ERR_UNSUPPORTED;
     ctr_attn_s *pl = new (std::nothrow) ctr_attn_s();
     if (!pl) return CTR_ERR_INVALID_ARG;
@@ -116,7 +131,7 @@ ctr_status ctr_attn_bind_workspace(ctr_attn_t pl, void *ws, size_t bytes) {
 ctr_status ctr_attn_reset(ctr_attn_t pl, void *stream) {
     if (!pl) return CTR_ERR_INVALID_ARG;
     if (!pl->ws) return CTR_ERR_NO_WORKSPACE;
-    if (cudaMemsetAsync(pl->ws, 0, pl->off_scores, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    if (cudaMemsetAsync(pl->ws, 0, pl->off_parts, static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return CTR_ERR_CUDA;
     pl->ready = 1;
     return CTR_OK;
@@ -158,8 +173,19 @@ ctr_status ctr_attn_forward(ctr_attn_t pl, const void *q, int64_t q_stride, cons
     p.q_stride = q_stride;
     p.kv_stride = kv_stride;
     p.out = out;
-    p.scores = pl->weights ? reinterpret_cast<float *>(static_cast<char *>(pl->ws) + pl->off_scores)
-                           : nullptr;
+    char *ws = static_cast<char *>(pl->ws);
+    p.counters = reinterpret_cast<uint32_t *>(ws + 256);
+    p.part_o = reinterpret_cast<float *>(ws + pl->off_parts);
+    p.part_ml = reinterpret_cast<float2 *>(ws + pl->off_ml);
+    if (pl->weights) {
+        p.stats = reinterpret_cast<float2 *>(ws + pl->off_stats);
+        p.scores = reinterpret_cast<float *>(ws + pl->off_scores);
+    }
+    p.score_pitch = pl->score_pitch;
+    p.min_chunk = 1;
+    p.page_shift = -1;
+    for (int s = 0; s < 29; ++s)
+        if (pl->page == (int64_t)1 << s) p.page_shift = s;
     p.w_in = weights_in;
     p.w_out = weights_out;
     p.B = (int)pl->B;

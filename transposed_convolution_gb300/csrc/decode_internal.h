@@ -11,7 +11,8 @@ struct ctr_attn_s {
     float scale;
     void *k_pages, *v_pages;
     int64_t num_pages;
-    size_t off_scores, ws_needed;
+    size_t off_parts, off_ml, off_stats, off_scores, ws_needed;
+    int64_t score_pitch;
     void *ws;
     size_t ws_bytes;
     int ready;               // ctr_attn_reset ran on the bound workspace
@@ -39,7 +40,16 @@ struct AttnParams {
     const void *q, *k_new, *v_new;
     int64_t q_stride, kv_stride;
     void *out;
-    float *scores;           // [B * Hq][cap], with weights
+    float *scores;           // [B * Hq][score_pitch] scores in units of log 2, with weights
+    float2 *stats;           // [B * Hq] maximum score and sum of the softmax, with weights
+    int64_t score_pitch;
+    // Parts of units that several blocks share: at most two a block (its run's first and last
+    // unit), [16][D] outputs and [16] (maximum, sum) each; blocks that have arrived, by unit.
+    float *part_o;
+    float2 *part_ml;
+    uint32_t *counters;
+    int min_chunk;           // fewest tiles in a block's run
+    int page_shift;          // log2 of the page size, or -1
     const float *w_in;
     float *w_out;
     int B, Hq, Hkv, G, D;
@@ -58,6 +68,11 @@ struct EvictParams {
     float *w_out;
     int B, Hkv, row_bytes, esize;
 };
+
+// Blocks of an attention launch: `per_sm` to an SM, of which the workspace holds kMaxPerSm.
+constexpr int kMaxPerSm = 2;
+// Tiles of the 16-bit kernel's scores (slots): its score rows are padded to whole tiles.
+constexpr int kScoreTile = 64;
 
 cudaError_t launch_attention(const ctr_attn_s *pl, const AttnParams &p, cudaStream_t st);
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t st);
