@@ -105,26 +105,31 @@ __global__ void weights_kernel(AttnParams p, int chunks) {
     }
 }
 
-template <typename T, int DP>
+template <typename T, int DP, int NH>
 cudaError_t launch16(const ctr_attn_s *pl, const AttnParams &p, cudaStream_t st) {
     static PerDeviceOnce once;
-    const auto kernel = attn16::attention16_kernel<T, DP>;
+    const auto kernel = attn16::attention16_kernel<T, DP, NH>;
     const cudaError_t e = once.run(current_device(), cudaSuccess, [&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)attn16::smem_bytes<DP>(DP, 2048));
+                                    (int)attn16::smem_bytes<DP, NH>(DP, 2048));
     });
     if (e != cudaSuccess) return e;
     const int per_sm = DP == 256 ? 1 : kMaxPerSm;
     count_launches(1);
     return launch_pdl(kernel, dim3((unsigned)(pl->num_sms * per_sm)), dim3(attn16::kThreads),
-                      attn16::smem_bytes<DP>(p.D, p.B), st, p);
+                      attn16::smem_bytes<DP, NH>(p.D, p.B), st, p);
+}
+
+template <typename T, int NH>
+cudaError_t launch16(const ctr_attn_s *pl, const AttnParams &p, cudaStream_t st) {
+    return p.D <= 64    ? launch16<T, 64, NH>(pl, p, st)
+           : p.D <= 128 ? launch16<T, 128, NH>(pl, p, st)
+                        : launch16<T, 256, NH>(pl, p, st);
 }
 
 template <typename T>
 cudaError_t launch16(const ctr_attn_s *pl, const AttnParams &p, cudaStream_t st) {
-    return p.D <= 64    ? launch16<T, 64>(pl, p, st)
-           : p.D <= 128 ? launch16<T, 128>(pl, p, st)
-                        : launch16<T, 256>(pl, p, st);
+    return p.G <= 8 ? launch16<T, 1>(pl, p, st) : launch16<T, 2>(pl, p, st);
 }
 
 template <typename T>

@@ -12,9 +12,9 @@ size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 int esize_of(const ctr_attn_s *pl) { return pl->dtype == CTR_F32 ? 4 : 2; }
 
-// Units of work: one for each sequence, KV head and set of up to 16 of its query heads.
+// Units of work: one for each sequence, KV head and set of eight or sixteen of its query heads.
 int64_t units_of(const ctr_attn_s *pl) {
-    return pl->B * pl->Hkv * ((pl->Hq / pl->Hkv + 15) / 16);
+    return pl->B * pl->Hkv * ((pl->Hq / pl->Hkv + 7) / 8);
 }
 
 // The status word, the units' counters (both cleared by ctr_attn_reset), the parts of shared
