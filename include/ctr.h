@@ -558,9 +558,10 @@ typedef enum {
 } ctr_cache_layout;
 
 /*
- * Create an attention plan (host only).  1 <= B <= 2048; 1 <= H_kv, H_q a multiple of it,
+ * Create an attention plan (host only).  1 <= B <= 1024; 1 <= H_kv, H_q a multiple of it,
  * H_q / H_kv <= 128; D a multiple of 16 up to 256; page_size >= 1; max_pages >= 1;
- * B * H_kv <= 2^20, max_pages * page_size <= 2^28, their product with B <= 2^36.  dtype: CTR_F32, CTR_BF16 or CTR_F16.
+ * B * H_kv <= 2^20, max_pages * page_size <= 2^28, and the product of all four (times H_q /
+ * H_kv / 8, rounded up) <= 2^36.  dtype: CTR_F32, CTR_BF16 or CTR_F16.
  * CTR_ERR_INVALID_ARG for sizes < 1 or H_q no multiple of H_kv, CTR_ERR_UNSUPPORTED
  * beyond the limits.
  */

@@ -29,11 +29,11 @@ P = ctypes.c_void_p
     ((1, 8, 8, 64, 16, 4, -1), "CTR_ERR_INVALID_ARG"),
     ((1, 8, 8, 72, 16, 4, 0), "CTR_ERR_UNSUPPORTED"),
     ((1, 8, 8, 272, 16, 4, 0), "CTR_ERR_UNSUPPORTED"),
-    ((2049, 8, 8, 64, 16, 4, 0), "CTR_ERR_UNSUPPORTED"),
+    ((1025, 8, 8, 64, 16, 4, 0), "CTR_ERR_UNSUPPORTED"),
     ((1, 129, 1, 64, 16, 4, 0), "CTR_ERR_UNSUPPORTED"),
     ((1, 8, 8, 64, 1 << 20, 1 << 20, 0), "CTR_ERR_UNSUPPORTED"),
     ((1, 8, 8, 64, 1 << 62, 4, 0), "CTR_ERR_UNSUPPORTED"),
-    ((2048, 1 << 40, 1 << 40, 64, 16, 4, 0), "CTR_ERR_UNSUPPORTED"),
+    ((1024, 1 << 40, 1 << 40, 64, 16, 4, 0), "CTR_ERR_UNSUPPORTED"),
 ])
 def test_attention_create_refuses(ctr, args, status):
     h = P(1)

@@ -111,13 +111,20 @@ cudaError_t launch16(const ctr_attn_s *pl, const AttnParams &p, cudaStream_t st)
     const auto kernel = attn16::attention16_kernel<T, DP, NH>;
     const cudaError_t e = once.run(current_device(), cudaSuccess, [&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)attn16::smem_bytes<DP, NH>(DP, 2048));
+                                    (int)attn16::smem_bytes<DP>(DP, 1024));
     });
     if (e != cudaSuccess) return e;
-    const int per_sm = DP == 256 ? 1 : kMaxPerSm;
+    const int grid = pl->num_sms * (DP > 128 ? 1 : kMaxPerSm);
     count_launches(1);
-    return launch_pdl(kernel, dim3((unsigned)(pl->num_sms * per_sm)), dim3(attn16::kThreads),
-                      attn16::smem_bytes<DP, NH>(p.D, p.B), st, p);
+    cudaError_t run = launch_pdl(kernel, dim3((unsigned)grid), dim3(attn16::kThreads),
+                                 attn16::smem_bytes<DP>(p.D, p.B), st, p);
+    if (run != cudaSuccess || p.whole_units) return run;
+    // Few heads have many parts each: eight warps join one; else two.
+    count_launches(1);
+    const int64_t heads = (int64_t)p.B * p.Hq;
+    if (heads <= 2048)
+        return launch_pdl(attn16::join_kernel<T, 8, DP / 128 ? DP / 128 : 1>, dim3((unsigned)heads), dim3(256), 0, st, p, grid);
+    return launch_pdl(attn16::join_kernel<T, 2, DP / 128 ? DP / 128 : 1>, dim3((unsigned)((heads + 3) / 4)), dim3(256), 0, st, p, grid);
 }
 
 template <typename T, int NH>

@@ -10,13 +10,19 @@
 // tcgen05 would want 128 rows of queries: no group has them.
 //
 // Work: a unit is one sequence, KV head and set of 8 or 16 query heads; its slots come in tiles of
-// 64, 16 to each of a block's four warps.  All tiles of all units in a row are cut into
-// equal runs, one for each resident block, so ragged lengths and long sequences fill the GPU
-// alike.  Every warp streams its own slots through a ring of cp.async stages without block
-// barriers, and keeps a running maximum, sum and output of its own; the warps join once for each
-// unit of the block's run.  (Bulk copies, one a row as the pages want them, issue from one lane
-// at a time: 655 instructions a step against 230, and 532 us for the full batch.)  A unit that several blocks share is joined by the
-// last of them to finish, in block order, so the result does not depend on timing.
+// 64, 16 to each of a block's four warps.  All units' tiles, in a row, are cut into chunks: the
+// first three quarters into one for each resident block, the rest into small ones that the
+// blocks draw from a queue, because blocks do not run equally fast (with equal shares of
+// 131072 slots the first block ended at 35 us, the median at 79 and the last at 98).  The
+// cuts depend on the lengths alone, and the parts of a unit that several chunks share are joined
+// in chunk order by a second kernel, so the result does not depend on timing.  (Joined by the
+// last block to arrive, behind a fence and a counter, two parts took 3.4 us and 190 parts 50.)
+// Entering a unit counts as one tile more: the queries' loads and the warps' join take about as
+// long.  Caches of up to kWholeSlots slots are cut into whole units, without a second kernel.
+// Every warp streams its own slots through a ring of cp.async stages without block barriers,
+// and keeps a running maximum, sum and output of its own; the warps join once for each unit of
+// a chunk.  (Bulk copies, one a row as the pages want them, issue from one lane at a time:
+// 655 instructions a step against 430, and 532 us for the full batch against 370.)
 //
 // Rounding: scores, statistics and outputs are fp32.  The probabilities enter the product with
 // V as two 16-bit terms (the rounded value and what rounding left), so they keep at least 15
@@ -31,6 +37,7 @@ namespace attn16 {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kTile = 16 * kWarps;      // slots of one block step
+constexpr int kDynamicShare = 8;        // tiles a block from which on the queue is used
 constexpr float kNegInf = -__builtin_inff();
 
 template <typename T> struct Pair;
@@ -100,66 +107,47 @@ __host__ __device__ inline int row_pitch(int D) { return 2 * D + 16; }
 // Stages of a warp's ring.  Two blocks of 128 columns fit an SM with three stages of 8.5 KB to
 // a warp: 139 KB in flight an SM, where 45 KB would cover 1 us of latency at full rate.
 template <int DP> struct Ring { static constexpr int kStages = DP == 64 ? 5 : 3; };
-// Output columns joined at a time, for NH sets of eight heads.
-template <int NH> struct Join {
-    static constexpr int kSlice = 64 / NH, kPitch = kSlice + 4;
-    static constexpr int kBytes = (int)sizeof(float) * kWarps * 8 * NH * kPitch;
-};
-template <int DP, int NH> inline size_t smem_bytes(int D, int B) {
-    return (size_t)kWarps * Ring<DP>::kStages * 32 * row_pitch(D) + Join<NH>::kBytes + 8 * (size_t)B;
+template <int DP> inline size_t smem_bytes(int D, int B) {
+    return (size_t)kWarps * Ring<DP>::kStages * 32 * row_pitch(D) + 8 * (size_t)B;
 }
 
-// The parts of one unit, of blocks c0 .. c1, to its outputs.  A block's part of the unit that
-// its run begins with is its first, else its second.
-template <typename T>
-__device__ __noinline__ void join_parts(const AttnParams &p, int64_t c0, int64_t c1, bool first_of_c0,
-                                        int rows, int64_t h0) {
-    const int quads = p.D / 4;
-    for (int x = threadIdx.x; x < rows * quads; x += kThreads) {
-        const int row = x / quads, d = x % quads * 4;
-        float M = kNegInf, L = 0.0f;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int64_t c = c0; c <= c1; c += 8) {
-            float2 ml[8];
-            float4 u[8];
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-                const int64_t id = c + y == c0 && !first_of_c0 ? c0 * 2 + 1 : (c + y) * 2;
-                const bool on = c + y <= c1;
-                ml[y] = on ? __ldcg(p.part_ml + id * 16 + row) : make_float2(kNegInf, 0.0f);
-                u[y] = on ? __ldcg(reinterpret_cast<const float4 *>(p.part_o + (id * 16 + row) * p.D + d))
-                          : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            float M2 = M;
-#pragma unroll
-            for (int y = 0; y < 8; ++y) M2 = fmaxf(M2, ml[y].x);
-            const float shrink = M == kNegInf ? 0.0f : pow2(M - M2);
-            M = M2;
-            L *= shrink;
-            v.x *= shrink;
-            v.y *= shrink;
-            v.z *= shrink;
-            v.w *= shrink;
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-                const float g = ml[y].x == kNegInf ? 0.0f : pow2(ml[y].x - M);
-                L = fmaf(ml[y].y, g, L);
-                v.x = fmaf(u[y].x, g, v.x);
-                v.y = fmaf(u[y].y, g, v.y);
-                v.z = fmaf(u[y].z, g, v.z);
-                v.w = fmaf(u[y].w, g, v.w);
-            }
+// The first slot that n tokens attend to, and the tiles they take (one at least).
+__device__ __forceinline__ int first_slot(const AttnParams &p, int n) {
+    return p.window > 0 && n > p.window ? n - (int)p.window : 0;
+}
+__device__ __forceinline__ int unit_tiles(const AttnParams &p, int n) {
+    return max(1, (n + kTile - 1) / kTile - first_slot(p, n) / kTile);
+}
+
+// How the row of all tiles is cut: `grid` chunks of s0, then chunks of s1.
+struct Cuts {
+    int total, grid, s0, s1, count;
+    __device__ int begin(int c) const { return c < grid ? c * s0 : grid * s0 + (c - grid) * s1; }
+    __device__ int end(int c) const { return min(total, begin(c) + (c < grid ? s0 : s1)); }
+    __device__ int of(int x) const { return x < grid * s0 ? x / s0 : grid + (x - grid * s0) / s1; }
+    __device__ Cuts(int total_, int grid_, int max_chunks) : total(total_), grid(grid_) {
+        const int share = total / grid;
+        s0 = share * 3 / 4;
+        s1 = max(3, (share + 31) / 32);
+        count = grid + (total - grid * s0 + s1 - 1) / s1;
+        // Short runs are cut evenly: the queue's latency would cost more than it evens out.
+        if (share < kDynamicShare || count > max_chunks) {
+            s0 = (total + grid - 1) / grid;
+            s1 = 1;
+            count = (total + s0 - 1) / s0;
         }
-        const float r = L > 0.0f ? 1.0f / L : 0.0f;
-        *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + (h0 + row) * p.D + d) =
-            make_uint2(Pair<T>::pack(v.x * r, v.y * r), Pair<T>::pack(v.z * r, v.w * r));
-        if (p.scores && d == 0) p.stats[h0 + row] = make_float2(M, L);
     }
-}
+};
 
-// A tile's place: tile `tile` of head set hv of sequence b.
-struct Place {
-    int b, hv, tile, tiles, n, lo, first;
+// A walk over the units of a block's chunks.
+struct Walk {
+    int k;                   // the k-th chunk of this block
+    int x, x1;               // place in it and its end
+    int b, hv;               // unit
+    int n, lo, first, tiles; // its sequence's
+    int unit;                // the unit's place: its entry, then its tiles
+    int tile, left;          // segment: next tile, and tiles left
+    bool first_of_chunk;     // whether it is its chunk's first
 };
 
 // A running maximum is raised only when a score exceeds it by 2^kSlack: until then the
@@ -170,26 +158,26 @@ constexpr float kSlack = 8.0f;
 template <typename T, int DP, int NH>
 __global__ void __launch_bounds__(kThreads) attention16_kernel(AttnParams p) {
     constexpr int S = Ring<DP>::kStages, KS = DP / 16, HN = 8 * NH;
-    constexpr int kSlice = Join<NH>::kSlice, kPitch = Join<NH>::kPitch;
     typedef Pair<T> P;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint32_t slot_masks[kWarps][S];
     __shared__ float red_m[kWarps][HN], red_l[kWarps][HN];
     __shared__ int warp_sum[kWarps];
-    __shared__ int is_last;
+    __shared__ int drawn[4];                 // numbers of this block's chunks, a ring by k
     const int t = threadIdx.x, warp = t / 32, lane = t % 32;
     const int pitch = row_pitch(p.D), stage_bytes = 32 * pitch;
     unsigned char *ring = smem + (size_t)warp * S * stage_bytes;
-    float *merge = reinterpret_cast<float *>(smem + (size_t)kWarps * S * stage_bytes);
-    int *prefix = reinterpret_cast<int *>(merge + kWarps * HN * kPitch);           // [B]
-    int *ntok = prefix + p.B;                                                      // [B]
+    int *prefix = reinterpret_cast<int *>(smem + (size_t)kWarps * S * stage_bytes);   // [B]
+    int *ntok = prefix + p.B;                                                         // [B]
     const bool with_new = p.k_new != nullptr;
     ptx::griddep_wait();
 
-    // Tiles before each sequence (of one head set), and all of them.
-    auto lo_of = [&](int n) { return p.window > 0 && n > p.window ? n - (int)p.window : 0; };
-    auto tiles_of = [&](int n) { return max(1, (n + kTile - 1) / kTile - lo_of(n) / kTile); };
-    int64_t total;
+    ptx::griddep_launch_dependents();
+
+    // Entries and tiles before each sequence (of one head set), and all of them.
+    auto lo_of = [&](int n) { return first_slot(p, n); };
+    auto tiles_of = [&](int n) { return unit_tiles(p, n); };
+    int total;
     const int sets = (p.G + HN - 1) / HN, Hu = p.Hkv * sets;
     {
         const int per = (p.B + kThreads - 1) / kThreads, b0 = min(t * per, p.B),
@@ -199,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) attention16_kernel(AttnParams p) {
             const int n = tokens_of(p.cache, b, with_new, &len);
             // The sign says whether the last token is the new one.
             ntok[b] = with_new && n > len && len >= 0 ? -n : n;
-            sum += tiles_of(n);
+            sum += 1 + tiles_of(n);
         }
         int incl = sum;
 #pragma unroll
@@ -217,49 +205,90 @@ __global__ void __launch_bounds__(kThreads) attention16_kernel(AttnParams p) {
         }
         for (int b = b0; b < b1; ++b) {
             prefix[b] = base;
-            base += tiles_of(abs(ntok[b]));
+            base += 1 + tiles_of(abs(ntok[b]));
         }
-        total = (int64_t)all * Hu;
+        total = all * Hu;       // at most 2^31 - 1: a plan's limit
         __syncthreads();
     }
-    const int64_t chunk = max((total + gridDim.x - 1) / gridDim.x, (int64_t)p.min_chunk);
-    const int64_t t0 = chunk * blockIdx.x, t1 = min(t0 + chunk, total);
-    if (t0 >= t1) return;
+    Cuts cuts(total, gridDim.x, p.max_chunks);
+    if (p.whole_units) cuts.count = p.B * Hu;      // chunk c is unit c, and blocks take turns
+    if ((int)blockIdx.x >= cuts.count) return;
+    const bool dynamic = !p.whole_units && cuts.count > (int)gridDim.x;
 
-    auto enter = [&](Place &at) {
-        at.n = abs(ntok[at.b]);
-        at.lo = lo_of(at.n);
-        at.first = at.lo / kTile * kTile;
-        at.tiles = tiles_of(at.n);
+    // A number from the queue, as the chunk it stands for.  Every block draws until its number
+    // is past the end; the very last number drawn leaves the queue as it was found.
+    auto chunk_drawn = [&](uint32_t v) {
+        if (v == (uint32_t)(cuts.count - 1)) *p.queue = 0;
+        return (int)min(v + gridDim.x, (uint32_t)cuts.count);
     };
-    auto advance = [&](Place &at) {
-        if (++at.tile == at.tiles) {
-            at.tile = 0;
-            if (++at.hv == Hu) {
-                at.hv = 0;
-                if (++at.b < p.B) enter(at);
+    auto enter = [&](Walk &w) {
+        w.n = abs(ntok[w.b]);
+        w.lo = lo_of(w.n);
+        w.first = w.lo / kTile * kTile;
+        w.tiles = tiles_of(w.n);
+    };
+    // To chunk c, the k-th of this block.
+    auto begin_chunk = [&](Walk &w, int c) {
+        if (p.whole_units) {
+            w.b = c / Hu;
+            w.hv = c - w.b * Hu;
+            enter(w);
+            w.unit = w.x = 0;
+            w.x1 = 1 + w.tiles;
+            return;
+        }
+        w.x = cuts.begin(c);
+        w.x1 = cuts.end(c);
+        const int q = w.x / Hu;
+        int lo = 0, hi = p.B - 1;        // the last sequence with prefix <= q
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (prefix[mid] <= q) lo = mid; else hi = mid - 1;
+        }
+        w.b = lo;
+        enter(w);
+        w.hv = (w.x - prefix[lo] * Hu) / (w.tiles + 1);
+        w.unit = prefix[lo] * Hu + w.hv * (w.tiles + 1);
+    };
+    // The next segment of the walk: a unit's tiles in one chunk.  False at the end, or when the
+    // number of the next chunk is not yet known to this warp: it knows them up to k_known.
+    auto next_segment = [&](Walk &w, int k_known, bool fresh = false) {
+        for (;;) {
+            if (w.x >= w.x1) {
+                if (!(dynamic || p.whole_units) || w.k + 1 > k_known) return false;
+                const int c = p.whole_units ? (int)(blockIdx.x + (w.k + 1) * gridDim.x) : drawn[(w.k + 1) & 3];
+                if (c >= cuts.count) return false;
+                ++w.k;
+                begin_chunk(w, c);
+                fresh = true;
+            } else if (w.x >= w.unit + 1 + w.tiles) {
+                w.unit += 1 + w.tiles;
+                if (++w.hv == Hu) {
+                    w.hv = 0;
+                    ++w.b;
+                    enter(w);
+                }
+            }
+            const int from = max(w.x, w.unit + 1), to = min(w.x1, w.unit + 1 + w.tiles);
+            w.x = max(to, w.x + 1);
+            if (from < to) {
+                w.tile = from - (w.unit + 1);
+                w.left = to - from;
+                w.first_of_chunk = fresh;
+                return true;
             }
         }
     };
-    Place use;
-    {
-        const int x = (int)(t0 / Hu);
-        int lo = 0, hi = p.B - 1;        // the last sequence with prefix <= x
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (prefix[mid] <= x) lo = mid; else hi = mid - 1;
-        }
-        use.b = lo;
-        enter(use);
-        const int64_t rem = t0 - (int64_t)prefix[lo] * Hu;
-        use.hv = (int)(rem / use.tiles);
-        use.tile = (int)(rem % use.tiles);
-    }
+    Walk use;
+    use.k = 0;
+    begin_chunk(use, blockIdx.x);
+    use.left = 0;
 
     // The producer side: kLanes lanes copy a row, 16 bytes each, kRows rows at a time.
     constexpr int kLanes = DP / 8, kRows = 32 / kLanes;
-    Place in = use;
-    int64_t to_issue = t1 - t0;
+    Walk in = use;
+    const bool more = next_segment(in, 0, true);
+    int ahead = 0, in_slot = 0;         // stages under way, and the next one to fill
     const int row0 = lane / kLanes, col = lane % kLanes;
     const bool copies = col * 8 < p.D;
     // With pages of whole sixteens a warp's slots lie in one page.
@@ -275,18 +304,23 @@ __global__ void __launch_bounds__(kThreads) attention16_kernel(AttnParams p) {
                       ? __ldg(p.cache.tables + (int64_t)in.b * p.cache.table_pitch + page_index(j))
                       : -1;
     };
-    auto issue = [&](int slot) {
-        if (to_issue > 0) {
+    // Fills a stage with the next tile, if the walk has one.
+    auto issue = [&](int k_known) {
+        if (in.left == 0) {
+            if (!more || !next_segment(in, k_known)) return;
+            fetch_page();
+        }
+        {
             const int j0 = in.first + in.tile * kTile + warp * 16, j = j0 + (lane & 15);
             const int hk = sets == 1 ? in.hv : in.hv / sets;
             const bool ok = (unsigned)page_no < (unsigned)p.cache.num_pages;
             const unsigned mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
             int64_t off = page_no * p.cache.page_stride + hk * p.cache.head_stride +
                           (j - page_index(j) * p.cache.page) * p.cache.row_stride;
-            if (lane == 0) slot_masks[warp][slot] = mask;
+            if (lane == 0) slot_masks[warp][in_slot] = mask;
             if (mask != 0xffffu && !ok && j >= in.lo && j < in.n)
                 atomicOr(p.cache.status, kStatusBadPage);
-            const uint32_t dst = lane_dst + slot * stage_bytes;
+            const uint32_t dst = lane_dst + in_slot * stage_bytes;
             const int newest = ntok[in.b];       // -n where slot n - 1 is the new token's
             if (mask == 0xffffu && one_page && !(newest < 0 && -newest - 1 < j0 + 16)) {
                 off = __shfl_sync(0xffffffffu, off, 0) + lane_off;
@@ -309,15 +343,10 @@ __global__ void __launch_bounds__(kThreads) attention16_kernel(AttnParams p) {
                     const T *ks = static_cast<const T *>(p.k) + o, *vs = static_cast<const T *>(p.v) + o;
                     if (!copies) continue;
                     if (on && newest == -(j0 + row + 1)) {
-                        // The new token's row comes from the arguments, and goes to the cache.
+                        // The new token's row comes from the arguments.
                         const int64_t x = in.b * p.kv_stride + (int64_t)hk * p.D + col * 8;
-                        T *kc = const_cast<T *>(ks), *vc = const_cast<T *>(vs);
                         ks = static_cast<const T *>(p.k_new) + x;
                         vs = static_cast<const T *>(p.v_new) + x;
-                        if (in.hv == hk * sets) {
-                            *reinterpret_cast<uint4 *>(kc) = *reinterpret_cast<const uint4 *>(ks);
-                            *reinterpret_cast<uint4 *>(vc) = *reinterpret_cast<const uint4 *>(vs);
-                        }
                     }
                     // Hidden slots are filled with zeros: no probability is given to them, and
                     // what V holds there must be finite.  (The address is not read.)
@@ -325,43 +354,63 @@ __global__ void __launch_bounds__(kThreads) attention16_kernel(AttnParams p) {
                     copy16(dst + (16 + i * kRows) * pitch, on ? vs : p.v, on);
                 }
             }
-            if (--to_issue > 0) {
-                advance(in);
-                fetch_page();
-            }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
+        ++ahead;
+        if (++in_slot == S) in_slot = 0;
+        ++in.tile;
+        if (--in.left == 0 && !next_segment(in, k_known)) return;
+        fetch_page();
     };
-    fetch_page();
+    if (more) fetch_page();
 #pragma unroll 1
-    for (int s = 0; s < S - 1; ++s) issue(s);
+    for (int s = 0; s < S - 1; ++s) issue(0);
+    uint32_t number = 0;          // thread 0: drawn for the chunk after the next, under way
+    bool drawing = false;
+    if (dynamic) {
+        if (t == 0) {
+            drawn[1] = chunk_drawn(atomicAdd(p.queue, 1u));
+            if (drawn[1] < cuts.count) {
+                number = atomicAdd(p.queue, 1u);
+                drawing = true;
+            }
+        }
+        __syncthreads();
+    }
 
     const int r0 = lane / 4, quad = lane % 4;
     int slot = 0;
-    for (int64_t at = t0; at < t1;) {
-        // One unit's share of this block's run.
+    uint32_t q[NH][KS][2];
+    // Queries as the products' second operand: heads r0 (and r0 + 8), columns quad * 2.
+    auto load_queries = [&]() {
+        const int hk = use.hv / sets, set = use.hv % sets, rows = p.G - set * HN;
+        const T *qb = static_cast<const T *>(p.q) + use.b * p.q_stride + (hk * p.G + set * HN) * p.D;
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    q[h][i][e] = h * 8 + r0 < rows && i * 16 < p.D
+                                     ? __ldg(reinterpret_cast<const uint32_t *>(
+                                           qb + (h * 8 + r0) * p.D + i * 16 + e * 8 + quad * 2))
+                                     : 0u;
+    };
+    bool go = next_segment(use, 0, true);
+    if (go) load_queries();
+    while (go) {
+        // One unit's share of a chunk.
         const int hk = use.hv / sets, set = use.hv % sets;
-        const int rows = min(HN, p.G - set * HN);
+        const int rows = min(HN, p.G - set * HN), k = use.k;
         const int64_t h0 = (int64_t)use.b * p.Hq + (int64_t)hk * p.G + set * HN;   // first query head
-        const int64_t unit_start = (int64_t)prefix[use.b] * Hu + (int64_t)use.hv * use.tiles;
-        const int64_t unit_end = unit_start + use.tiles;
-        const int steps = (int)(min(unit_end, t1) - at);
-        // Queries as the products' second operand: heads r0 (and r0 + 8), columns quad * 2.
-        uint32_t q[NH][KS][2];
-        {
-            const T *qb = static_cast<const T *>(p.q) + use.b * p.q_stride +
-                          ((int64_t)hk * p.G + set * HN) * p.D;
-#pragma unroll
-            for (int h = 0; h < NH; ++h)
-#pragma unroll
-                for (int i = 0; i < KS; ++i)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        q[h][i][e] = h * 8 + r0 < rows && i * 16 < p.D
-                                         ? __ldg(reinterpret_cast<const uint32_t *>(
-                                               qb + (h * 8 + r0) * p.D + i * 16 + e * 8 + quad * 2))
-                                         : 0u;
-        }
+        const int steps = use.left;
+        const int chunk = k == 0 ? blockIdx.x : drawn[k & 3];
+        const int unit_b = use.b;
+        const bool whole = use.tile == 0 && steps == use.tiles;
+        const int part = chunk * 2 + (use.first_of_chunk ? 0 : 1);
+        // The slot that this unit puts in the cache, once for a KV head.
+        const int new_slot = ntok[use.b] < 0 && set == 0 ? use.n - 1 : -1;
+        const int j_first = use.first + use.tile * kTile + warp * 16;
         float o[NH][KS][4];      // columns i * 16 + r0 (+ 8) of heads quad * 2 (+ 1)
         float m[NH][2], l[NH][2];
 #pragma unroll
@@ -372,12 +421,33 @@ __global__ void __launch_bounds__(kThreads) attention16_kernel(AttnParams p) {
             for (int i = 0; i < KS; ++i) o[h][i][0] = o[h][i][1] = o[h][i][2] = o[h][i][3] = 0.0f;
         }
         for (int step = 0; step < steps; ++step) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+            if (ahead == 0) issue(k + 1);
+            if (ahead >= S - 1)
+                asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+            else
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
             __syncwarp();
             const uint32_t mask = slot_masks[warp][slot];
-            issue(slot == 0 ? S - 1 : slot - 1);
-            const uint32_t ks = ptx::smem_u32(ring + slot * stage_bytes), vs = ks + 16 * pitch;
+            --ahead;
+            issue(k + 1);
+            const unsigned char *slot_base = ring + slot * stage_bytes;
+            const uint32_t ks = ptx::smem_u32(slot_base), vs = ks + 16 * pitch;
             if (++slot == S) slot = 0;
+            if (new_slot >= 0) {
+                // The new token's row goes on to the cache.
+                const int row = new_slot - (j_first + step * kTile);
+                if (row >= 0 && row < 16 && (mask >> row & 1) && lane < p.D / 8) {
+                    const int pg = p.cache.tables[(int64_t)unit_b * p.cache.table_pitch + page_index(new_slot)];
+                    const int64_t to = pg * p.cache.page_stride + hk * p.cache.head_stride +
+                                       (new_slot - page_index(new_slot) * p.cache.page) * p.cache.row_stride +
+                                       lane * 8;
+                    const unsigned char *from = slot_base + row * pitch + lane * 16;
+                    *reinterpret_cast<uint4 *>(static_cast<T *>(p.k) + to) =
+                        *reinterpret_cast<const uint4 *>(from);
+                    *reinterpret_cast<uint4 *>(static_cast<T *>(p.v) + to) =
+                        *reinterpret_cast<const uint4 *>(from + 16 * pitch);
+                }
+            }
             if (mask == 0 && !p.scores) continue;
             float s[NH][4] = {};     // slots r0 (+ 8 from the third) of heads quad * 2 (+ 1)
             {
@@ -406,8 +476,7 @@ __global__ void __launch_bounds__(kThreads) attention16_kernel(AttnParams p) {
             }
             if (p.scores) {
                 // The pitch covers whole tiles.
-                float *dst = p.scores + h0 * p.score_pitch + use.first + (use.tile + step) * kTile +
-                             warp * 16 + r0;
+                float *dst = p.scores + h0 * p.score_pitch + j_first + step * kTile + r0;
 #pragma unroll
                 for (int h = 0; h < NH; ++h)
 #pragma unroll
@@ -473,103 +542,200 @@ __global__ void __launch_bounds__(kThreads) attention16_kernel(AttnParams p) {
                 }
             }
         }
-        at += steps;
 
-        // Join the four warps: the heads' maxima and sums, then the outputs slice by slice.
+        // Join the four warps, through the stage that each has just used: it is filled again in the
+        // next step at the earliest, and holds [HN][D + 4] fp32.
+        const int used = (slot == 0 ? S : slot) - 1, join_pitch = p.D + 4;
+        {
+            float *mine = reinterpret_cast<float *>(ring + used * stage_bytes);
+            __syncwarp();
 #pragma unroll
-        for (int h = 0; h < NH; ++h)
+            for (int h = 0; h < NH; ++h)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float v = l[h][e];
-                v += __shfl_xor_sync(0xffffffffu, v, 4);
-                v += __shfl_xor_sync(0xffffffffu, v, 8);
-                v += __shfl_xor_sync(0xffffffffu, v, 16);
-                if (r0 == 0) {
-                    red_m[warp][h * 8 + quad * 2 + e] = m[h][e];
-                    red_l[warp][h * 8 + quad * 2 + e] = v;
+                for (int e = 0; e < 2; ++e) {
+                    float v = l[h][e];
+                    v += __shfl_xor_sync(0xffffffffu, v, 4);
+                    v += __shfl_xor_sync(0xffffffffu, v, 8);
+                    v += __shfl_xor_sync(0xffffffffu, v, 16);
+                    const int head = h * 8 + quad * 2 + e;
+                    if (r0 == 0) {
+                        red_m[warp][head] = m[h][e];
+                        red_l[warp][head] = v;
+                    }
+                    float *row = mine + head * join_pitch + r0;
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) {
+                        if (i * 16 >= p.D) break;
+                        row[i * 16] = o[h][i][e];
+                        row[i * 16 + 8] = o[h][i][e + 2];
+                    }
                 }
-            }
+        }
+        if (drawing) {
+            drawn[(k + 2) & 3] = chunk_drawn(number);
+            drawing = false;
+        }
         __syncthreads();
-        float f[NH][2];
-#pragma unroll
-        for (int h = 0; h < NH; ++h)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float top = kNegInf;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, red_m[w][h * 8 + quad * 2 + e]);
-                f[h][e] = m[h][e] == kNegInf ? 0.0f : pow2(m[h][e] - top);
-            }
-        // This thread's head of the joined output, and its four columns of each slice.
-        const int jh = t / (kSlice / 4), jc = t % (kSlice / 4) * 4;
-        float top = kNegInf, sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, red_m[w][jh]);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-            if (red_m[w][jh] != kNegInf) sum += red_l[w][jh] * pow2(red_m[w][jh] - top);
-        const bool whole = at == unit_end && unit_start >= t0;
-        const int64_t part = (int64_t)blockIdx.x * 2 + (unit_start <= t0 ? 0 : 1);
-        float *part_o = p.part_o + part * 16 * p.D;
-#pragma unroll
-        for (int k = 0; k < DP / kSlice; ++k) {
-            const int d0 = k * kSlice;
-            if (d0 >= p.D) break;
-#pragma unroll
-            for (int x = 0; x < kSlice / 16; ++x)
-#pragma unroll
-                for (int h = 0; h < NH; ++h)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        merge[(warp * HN + h * 8 + quad * 2 + (e & 1)) * kPitch + x * 16 + r0 +
-                              (e >> 1) * 8] = o[h][k * (kSlice / 16) + x][e] * f[h][e & 1];
-            __syncthreads();
-            if (jh < rows && d0 + jc < p.D) {
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float4 u = *reinterpret_cast<const float4 *>(merge + (w * HN + jh) * kPitch + jc);
-                    v.x += u.x;
-                    v.y += u.y;
-                    v.z += u.z;
-                    v.w += u.w;
-                }
-                if (whole) {
-                    const float r = sum > 0.0f ? 1.0f / sum : 0.0f;
-                    *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + (h0 + jh) * p.D + d0 + jc) =
-                        make_uint2(P::pack(v.x * r, v.y * r), P::pack(v.z * r, v.w * r));
-                } else {
-                    *reinterpret_cast<float4 *>(part_o + jh * p.D + d0 + jc) = v;
-                }
-            }
-            __syncthreads();
+        // The next unit's queries come in meanwhile.
+        go = next_segment(use, k + 1);
+        if (go) load_queries();
+        if (t == 0 && dynamic && use.k != k && drawn[(k + 2) & 3] < cuts.count) {
+            number = atomicAdd(p.queue, 1u);
+            drawing = true;
         }
-        if (jh < rows && jc == 0) {
-            if (!whole)
-                p.part_ml[part * 16 + jh] = make_float2(top, sum);
-            else if (p.scores)
-                p.stats[h0 + jh] = make_float2(top, sum);
-        }
-        if (!whole) {
-            // The last block of the unit's to arrive joins the parts, in block order.
-            const int64_t c0 = unit_start / chunk, c1 = (unit_end - 1) / chunk;
-            __threadfence();
-            __syncthreads();
-            if (t == 0) {
-                uint32_t *count = p.counters + (int64_t)use.b * Hu + use.hv;
-                is_last = atomicAdd(count, 1u) == (uint32_t)(c1 - c0);
-                if (is_last) *count = 0;
+        constexpr int kQuads = DP / 4;
+#pragma unroll
+        for (int x0 = 0; x0 < HN * kQuads; x0 += kThreads) {
+            const int head = (x0 + t) / kQuads, d = (x0 + t) % kQuads * 4;
+            if (head >= rows || d >= p.D) continue;
+            float top = kNegInf, sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, red_m[w][head]);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = red_m[w][head] == kNegInf ? 0.0f : pow2(red_m[w][head] - top);
+                const float4 u = *reinterpret_cast<const float4 *>(
+                    smem + (size_t)(w * S + used) * stage_bytes + (head * join_pitch + d) * 4);
+                sum = fmaf(red_l[w][head], f, sum);
+                v.x = fmaf(u.x, f, v.x);
+                v.y = fmaf(u.y, f, v.y);
+                v.z = fmaf(u.z, f, v.z);
+                v.w = fmaf(u.w, f, v.w);
             }
-            __syncthreads();
-            if (is_last) {
-                __threadfence();
-                join_parts<T>(p, c0, c1, unit_start == c0 * chunk, rows, h0);
+            if (whole) {
+                const float r = sum > 0.0f ? 1.0f / sum : 0.0f;
+                *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + (h0 + head) * p.D + d) =
+                    make_uint2(P::pack(v.x * r, v.y * r), P::pack(v.z * r, v.w * r));
+                if (p.scores && d == 0) p.stats[h0 + head] = make_float2(top, sum);
+            } else {
+                const int64_t row = (int64_t)part * p.part_rows + head;
+                *reinterpret_cast<float4 *>(p.part_o + row * p.D + d) = v;
+                if (d == 0) p.part_ml[row] = make_float2(top, sum);
             }
         }
-        // The next unit of the run.
-        use.tile = use.tiles - 1;
-        if (at < t1) advance(use);
+        __syncthreads();
     }
+}
+
+
+// The second kernel: joins the parts of the units that several chunks share, in chunk order.
+// kRowWarps warps take one query head, each a run of its parts kDepth at a time.  What it reads
+// is in L2; its time is the launch, which overlaps the first kernel's end, and one or two trips to
+// L2.
+constexpr int kJoinWarps = 8;
+template <typename T, int kRowWarps, int N>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(AttnParams p, int grid) {
+    constexpr int kDepth = 16 / N, kRows = kJoinWarps / kRowWarps;
+    __shared__ float2 ml[kJoinWarps];
+    __shared__ __align__(16) float outs[kJoinWarps][256];
+    const int t = threadIdx.x, warp = t / 32, lane = t % 32, sub = warp % kRowWarps;
+    const int64_t row_no = (int64_t)blockIdx.x * kRows + warp / kRowWarps;    // b * Hq + head
+    // A block's heads may belong to two sequences: each warp sums up for its own.
+    const bool on = row_no < (int64_t)p.B * p.Hq;
+    const int b = on ? (int)(row_no / p.Hq) : p.B - 1, h = on ? (int)(row_no % p.Hq) : 0;
+    const int hn = p.G <= 8 ? 8 : 16, sets = (p.G + hn - 1) / hn, Hu = p.Hkv * sets;
+    int before = 0, all = 0, mine = 0;
+    for (int i = lane; i < p.B; i += 32) {
+        const int tiles = unit_tiles(p, token_count(p.cache, i, p.k_new != nullptr));
+        all += 1 + tiles;
+        if (i < b) before += 1 + tiles;
+        if (i == b) mine = tiles;
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    all = __reduce_add_sync(0xffffffffu, all);
+    const int tiles = __reduce_add_sync(0xffffffffu, mine);
+    const Cuts cuts(all * Hu, grid, p.max_chunks);
+    const int hk = h / p.G, g = h % p.G, hv = hk * sets + g / hn, row = g % hn;
+    const int unit = before * Hu + hv * (tiles + 1);
+    const int c0 = cuts.of(unit + 1), parts = on ? cuts.of(unit + tiles) - c0 + 1 : 1;
+    const int head = c0 * 2 + (cuts.begin(c0) >= unit ? 0 : 1);
+    ptx::griddep_wait();
+    if (kRowWarps == kJoinWarps && parts == 1) return;
+    // This warp's run of the parts.
+    const int run = (parts + kRowWarps - 1) / kRowWarps, from = min(sub * run, parts),
+              to = parts == 1 ? from : min(from + run, parts);
+    float M = kNegInf, L = 0.0f;
+    float4 v[N];                     // columns lane * 4 (and, past 128 of them, 128 further)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int d = lane * 4;
+    for (int c = from; c < to; c += kDepth) {
+        // Past the end the last part is read again, for nothing: loads behind a condition would
+        // wait for one another.
+        float2 s[kDepth];
+        float4 u[N][kDepth];
+#pragma unroll
+        for (int y = 0; y < kDepth; ++y) {
+            const int at = min(c + y, to - 1);
+            const int64_t id = (int64_t)(at == 0 ? head : (c0 + at) * 2) * p.part_rows + row;
+            s[y] = __ldcg(p.part_ml + id);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                u[i][y] = __ldcg(reinterpret_cast<const float4 *>(
+                    p.part_o + id * p.D + min(d + i * 128, p.D - 4)));
+        }
+        float M2 = M;
+#pragma unroll
+        for (int y = 0; y < kDepth; ++y) {
+            if (c + y >= to) s[y] = make_float2(kNegInf, 0.0f);
+            M2 = fmaxf(M2, s[y].x);
+        }
+        const float shrink = M == kNegInf ? 0.0f : pow2(M - M2);
+        M = M2;
+        L *= shrink;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            v[i].x *= shrink;
+            v[i].y *= shrink;
+            v[i].z *= shrink;
+            v[i].w *= shrink;
+        }
+#pragma unroll
+        for (int y = 0; y < kDepth; ++y) {
+            const float f = s[y].x == kNegInf ? 0.0f : pow2(s[y].x - M);
+            L = fmaf(s[y].y, f, L);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                v[i].x = fmaf(u[i][y].x, f, v[i].x);
+                v[i].y = fmaf(u[i][y].y, f, v[i].y);
+                v[i].z = fmaf(u[i][y].z, f, v[i].z);
+                v[i].w = fmaf(u[i][y].w, f, v[i].w);
+            }
+        }
+    }
+    if (lane == 0) ml[warp] = make_float2(M, L);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (d + i * 128 < p.D) *reinterpret_cast<float4 *>(&outs[warp][d + i * 128]) = v[i];
+    __syncthreads();
+    if (sub != 0 || parts == 1) return;
+    float top = kNegInf, sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kRowWarps; ++w) top = fmaxf(top, ml[warp + w].x);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kRowWarps; ++w) {
+        const float f = ml[warp + w].x == kNegInf ? 0.0f : pow2(ml[warp + w].x - top);
+        sum = fmaf(ml[warp + w].y, f, sum);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (d + i * 128 >= p.D) continue;
+            const float4 u = *reinterpret_cast<const float4 *>(&outs[warp + w][d + i * 128]);
+            v[i].x = fmaf(u.x, f, v[i].x);
+            v[i].y = fmaf(u.y, f, v[i].y);
+            v[i].z = fmaf(u.z, f, v[i].z);
+            v[i].w = fmaf(u.w, f, v[i].w);
+        }
+    }
+    const float r = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (d + i * 128 < p.D)
+            *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + row_no * p.D + d + i * 128) =
+                make_uint2(Pair<T>::pack(v[i].x * r, v[i].y * r), Pair<T>::pack(v[i].z * r, v[i].w * r));
+    if (p.scores && lane == 0) p.stats[row_no] = make_float2(top, sum);
 }
 
 }  // namespace attn16

@@ -1,5 +1,6 @@
 // decode.cu -- C ABI of the attention plan: validation, workspace layout and the launches of
 // ctr_attn_forward and ctr_attn_evict (kernels in attention.cu and evict.cu).
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <new>
@@ -12,21 +13,19 @@ size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 int esize_of(const ctr_attn_s *pl) { return pl->dtype == CTR_F32 ? 4 : 2; }
 
-// Units of work: one for each sequence, KV head and set of eight or sixteen of its query heads.
-int64_t units_of(const ctr_attn_s *pl) {
-    return pl->B * pl->Hkv * ((pl->Hq / pl->Hkv + 7) / 8);
-}
+int blocks_per_sm(const ctr_attn_s *pl) { return pl->D > 128 ? 1 : ctr::kMaxPerSm; }
+int part_rows(const ctr_attn_s *pl) { return (int)std::min<int64_t>(16, pl->Hq / pl->Hkv); }
 
-// The status word, the units' counters (both cleared by ctr_attn_reset), the parts of shared
-// units, and with weights the softmax statistics and scores.
+// The status word and the queue (cleared by ctr_attn_reset), the parts of shared units, and with
+// weights the softmax statistics and scores.
 void layout_workspace(ctr_attn_s *pl) {
-    const int64_t parts = 2 * ctr::kMaxPerSm * (int64_t)pl->num_sms;
+    const int64_t parts = 2 * ctr::kMaxChunks * blocks_per_sm(pl) * (int64_t)pl->num_sms;
     pl->score_pitch = (pl->max_pages * pl->page + ctr::kScoreTile - 1) / ctr::kScoreTile * ctr::kScoreTile;
-    pl->off_parts = align256(256 + (size_t)units_of(pl) * sizeof(uint32_t));
-    pl->off_ml = pl->off_parts + align256((size_t)(parts * 16 * pl->D) * sizeof(float));
-    pl->off_stats = pl->off_ml + align256((size_t)(parts * 16) * sizeof(float2));
-    pl->off_scores = pl->off_stats;
+    pl->off_parts = 256;
+    pl->off_ml = pl->off_parts + align256((size_t)(parts * part_rows(pl) * pl->D) * sizeof(float));
+    pl->off_stats = pl->off_ml + align256((size_t)(parts * part_rows(pl)) * sizeof(float2));
     pl->ws_needed = pl->off_stats;
+    pl->off_scores = pl->off_stats;
     if (pl->weights) {
         pl->off_scores += align256((size_t)(pl->B * pl->Hq) * sizeof(float2));
         pl->ws_needed = pl->off_scores +
@@ -64,9 +63,9 @@ ctr_status ctr_attn_create(ctr_attn_t *out, int64_t B, int64_t H_q, int64_t H_kv
     if (B < 1 || H_q < 1 || H_kv < 1 || D < 1 || page_size < 1 || max_pages < 1 || H_q % H_kv)
         return CTR_ERR_INVALID_ARG;
     const int64_t cap = (int64_t)1 << 28;
-    if (B > 2048 || H_kv > ((int64_t)1 << 20) / B || H_q / H_kv > 128 || D > 256 || D % 16 ||
+    if (B > 1024 || H_kv > ((int64_t)1 << 20) / B || H_q / H_kv > 128 || D > 256 || D % 16 ||
         page_size > cap || max_pages > cap / page_size ||
-        B * page_size * max_pages > ((int64_t)1 << 36))
+        B * H_kv * ((H_q / H_kv + 7) / 8) > ((int64_t)1 << 36) / (page_size * max_pages))
         return CTR_ERR_UNSUPPORTED;
     ctr_attn_s *pl = new (std::nothrow) ctr_attn_s();
     if (!pl) return CTR_ERR_INVALID_ARG;
@@ -174,15 +173,17 @@ ctr_status ctr_attn_forward(ctr_attn_t pl, const void *q, int64_t q_stride, cons
     p.kv_stride = kv_stride;
     p.out = out;
     char *ws = static_cast<char *>(pl->ws);
-    p.counters = reinterpret_cast<uint32_t *>(ws + 256);
+    p.queue = reinterpret_cast<uint32_t *>(ws + 128);
     p.part_o = reinterpret_cast<float *>(ws + pl->off_parts);
     p.part_ml = reinterpret_cast<float2 *>(ws + pl->off_ml);
+    p.part_rows = part_rows(pl);
+    p.max_chunks = ctr::kMaxChunks * blocks_per_sm(pl) * pl->num_sms;
     if (pl->weights) {
         p.stats = reinterpret_cast<float2 *>(ws + pl->off_stats);
         p.scores = reinterpret_cast<float *>(ws + pl->off_scores);
     }
+    p.whole_units = pl->max_pages * pl->page <= ctr::kWholeSlots;
     p.score_pitch = pl->score_pitch;
-    p.min_chunk = 1;
     p.page_shift = -1;
     for (int s = 0; s < 29; ++s)
         if (pl->page == (int64_t)1 << s) p.page_shift = s;

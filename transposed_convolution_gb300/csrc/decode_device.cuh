@@ -32,6 +32,12 @@ __device__ __forceinline__ int tokens_of(const CacheView &c, int b, bool with_ne
     return n + (with_new ? 1 : 0);
 }
 
+// The same count, without the report.
+__device__ __forceinline__ int token_count(const CacheView &c, int b, bool with_new) {
+    const int n = c.lens[b];
+    return n < 0 ? 0 : n > c.cap - (with_new ? 1 : 0) ? min(n, c.cap) : n + (with_new ? 1 : 0);
+}
+
 // First element of slot j of sequence b, or -1 when the table names no page of the cache.
 __device__ __forceinline__ int64_t slot_offset(const CacheView &c, int b, int h, int j) {
     const int pg = c.tables[(int64_t)b * c.table_pitch + j / c.page];

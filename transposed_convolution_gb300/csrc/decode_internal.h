@@ -43,12 +43,13 @@ struct AttnParams {
     float *scores;           // [B * Hq][score_pitch] scores in units of log 2, with weights
     float2 *stats;           // [B * Hq] maximum score and sum of the softmax, with weights
     int64_t score_pitch;
-    // Parts of units that several blocks share: at most two a block (its run's first and last
-    // unit), [16][D] outputs and [16] (maximum, sum) each; blocks that have arrived, by unit.
+    // Parts of units that several chunks of the work share, two to a chunk (its first segment
+    // and a later one): [part_rows][D] outputs and [part_rows] (maximum, sum) each.
     float *part_o;
     float2 *part_ml;
-    uint32_t *counters;
-    int min_chunk;           // fewest tiles in a block's run
+    uint32_t *queue;         // the next chunk's number
+    int part_rows, max_chunks;
+    int whole_units;         // every chunk is a whole unit: no parts
     int page_shift;          // log2 of the page size, or -1
     const float *w_in;
     float *w_out;
@@ -71,6 +72,10 @@ struct EvictParams {
 
 // Blocks of an attention launch: `per_sm` to an SM, of which the workspace holds kMaxPerSm.
 constexpr int kMaxPerSm = 2;
+// Chunks the work is cut into, for each block: one large, and at most nine small ones.
+constexpr int kMaxChunks = 10;
+// Caches of up to this many slots a sequence are cut into whole units.
+constexpr int kWholeSlots = 256;
 // Tiles of the 16-bit kernel's scores (slots): its score rows are padded to whole tiles.
 constexpr int kScoreTile = 64;
 
