@@ -9,20 +9,20 @@
 // heads], in m16n8k16 steps, once for each eight heads of a group of up to sixteen.
 // tcgen05 would want 128 rows of queries: no group has them.
 //
-// Work: a unit is one sequence, KV head and set of 8 or 16 query heads; its slots come in tiles of
-// 64, 16 to each of a block's four warps.  All units' tiles, in a row, are cut into chunks: the
-// first three quarters into one for each resident block, the rest into small ones that the
-// blocks draw from a queue, because blocks do not run equally fast (with equal shares of
-// 131072 slots the first block ended at 35 us, the median at 79 and the last at 98).  The
-// cuts depend on the lengths alone, and the parts of a unit that several chunks share are joined
-// in chunk order by a second kernel, so the result does not depend on timing.  (Joined by the
-// last block to arrive, behind a fence and a counter, two parts took 3.4 us and 190 parts 50.)
-// Entering a unit counts as one tile more: the queries' loads and the warps' join take about as
-// long.  Caches of up to kWholeSlots slots are cut into whole units, without a second kernel.
+// Work: a unit is one sequence, KV head and set of 8 or 16 query heads; its slots come in tiles,
+// 16 to each of a block's warps.  All units' tiles, in a row, are cut into equal chunks, one for
+// each resident block, so ragged lengths and long sequences fill the GPU alike; entering a
+// unit counts as one tile more.  The parts of a unit that several chunks share are joined in
+// chunk order by a second kernel, whose launch overlaps the first one's end, so the result does
+// not depend on timing.  (Joined by the last block to arrive, behind a fence and a counter, two
+// parts took 3.4 us and 33 parts 7.)  Caches of up to kWholeSlots slots are cut into whole
+// units, without a second kernel.  A queue of small chunks for the last quarter, for blocks that
+// run ahead, gained less than its parts cost once the rings were as short as they are.
+//
 // Every warp streams its own slots through a ring of cp.async stages without block barriers,
 // and keeps a running maximum, sum and output of its own; the warps join once for each unit of
 // a chunk.  (Bulk copies, one a row as the pages want them, issue from one lane at a time:
-// 655 instructions a step against 430, and 532 us for the full batch against 370.)
+// 655 instructions a step, and 532 us for the full batch.)
 //
 // Rounding: scores, statistics and outputs are fp32.  The probabilities enter the product with
 // V as two 16-bit terms (the rounded value and what rounding left), so they keep at least 15
@@ -35,10 +35,16 @@
 namespace ctr {
 namespace attn16 {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kTile = 16 * kWarps;      // slots of one block step
-constexpr int kDynamicShare = 8;        // tiles a block from which on the queue is used
 constexpr float kNegInf = -__builtin_inff();
+
+// Launch shapes by the largest head size.  What matters is warps an SM (each is held up by its own
+// chain of products and exponentials) and short rings: with 70 KB in flight an SM, 128
+// columns, 131072 slots took 92 us; with 140 KB 102 us, because the blocks then ran less evenly;
+// 45 KB would cover 1 us of latency.
+template <int DP> struct Shape;
+template <> struct Shape<64> { static constexpr int kWarps = 4, kStages = 3, kPerSm = 4; };
+template <> struct Shape<128> { static constexpr int kWarps = 4, kStages = 2, kPerSm = 3; };
+template <> struct Shape<256> { static constexpr int kWarps = 6, kStages = 2, kPerSm = 1; };
 
 template <typename T> struct Pair;
 template <> struct Pair<__nv_bfloat16> {
@@ -106,48 +112,26 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool on) {
 __host__ __device__ inline int row_pitch(int D) { return 2 * D + 16; }
 // Stages of a warp's ring.  Two blocks of 128 columns fit an SM with three stages of 8.5 KB to
 // a warp: 139 KB in flight an SM, where 45 KB would cover 1 us of latency at full rate.
-template <int DP> struct Ring { static constexpr int kStages = DP == 64 ? 5 : 3; };
 template <int DP> inline size_t smem_bytes(int D, int B) {
-    return (size_t)kWarps * Ring<DP>::kStages * 32 * row_pitch(D) + 8 * (size_t)B;
+    return (size_t)Shape<DP>::kWarps * Shape<DP>::kStages * 32 * row_pitch(D) + 8 * (size_t)B;
 }
 
 // The first slot that n tokens attend to, and the tiles they take (one at least).
 __device__ __forceinline__ int first_slot(const AttnParams &p, int n) {
     return p.window > 0 && n > p.window ? n - (int)p.window : 0;
 }
-__device__ __forceinline__ int unit_tiles(const AttnParams &p, int n) {
+template <int kTile> __device__ __forceinline__ int unit_tiles(const AttnParams &p, int n) {
     return max(1, (n + kTile - 1) / kTile - first_slot(p, n) / kTile);
 }
 
-// How the row of all tiles is cut: `grid` chunks of s0, then chunks of s1.
-struct Cuts {
-    int total, grid, s0, s1, count;
-    __device__ int begin(int c) const { return c < grid ? c * s0 : grid * s0 + (c - grid) * s1; }
-    __device__ int end(int c) const { return min(total, begin(c) + (c < grid ? s0 : s1)); }
-    __device__ int of(int x) const { return x < grid * s0 ? x / s0 : grid + (x - grid * s0) / s1; }
-    __device__ Cuts(int total_, int grid_, int max_chunks) : total(total_), grid(grid_) {
-        const int share = total / grid;
-        s0 = share * 3 / 4;
-        s1 = max(3, (share + 31) / 32);
-        count = grid + (total - grid * s0 + s1 - 1) / s1;
-        // Short runs are cut evenly: the queue's latency would cost more than it evens out.
-        if (share < kDynamicShare || count > max_chunks) {
-            s0 = (total + grid - 1) / grid;
-            s1 = 1;
-            count = (total + s0 - 1) / s0;
-        }
-    }
-};
-
-// A walk over the units of a block's chunks.
+// A walk over the units of a block's chunk (or, with whole units, over the block's units).
 struct Walk {
-    int k;                   // the k-th chunk of this block
-    int x, x1;               // place in it and its end
+    int x, x1;               // place in the chunk and its end
     int b, hv;               // unit
     int n, lo, first, tiles; // its sequence's
     int unit;                // the unit's place: its entry, then its tiles
     int tile, left;          // segment: next tile, and tiles left
-    bool first_of_chunk;     // whether it is its chunk's first
+    int count;               // segments (whole units) so far
 };
 
 // A running maximum is raised only when a score exceeds it by 2^kSlack: until then the
@@ -155,28 +139,30 @@ struct Walk {
 // reduction over the warp.
 constexpr float kSlack = 8.0f;
 
-template <typename T, int DP, int NH>
-__global__ void __launch_bounds__(kThreads) attention16_kernel(AttnParams p) {
-    constexpr int S = Ring<DP>::kStages, KS = DP / 16, HN = 8 * NH;
+// kD is the head size, or 0 for any up to DP.
+template <typename T, int DP, int NH, int kD>
+__global__ void __launch_bounds__(32 * Shape<DP>::kWarps, Shape<DP>::kPerSm)
+attention16_kernel(AttnParams p) {
+    constexpr int kWarps = Shape<DP>::kWarps, kThreads = 32 * kWarps, kTile = 16 * kWarps;
+    constexpr int S = Shape<DP>::kStages, KS = DP / 16, HN = 8 * NH;
     typedef Pair<T> P;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint32_t slot_masks[kWarps][S];
     __shared__ float red_m[kWarps][HN], red_l[kWarps][HN];
     __shared__ int warp_sum[kWarps];
-    __shared__ int drawn[4];                 // numbers of this block's chunks, a ring by k
     const int t = threadIdx.x, warp = t / 32, lane = t % 32;
-    const int pitch = row_pitch(p.D), stage_bytes = 32 * pitch;
+    const int D = kD ? kD : p.D;
+    const int pitch = row_pitch(D), stage_bytes = 32 * pitch;
     unsigned char *ring = smem + (size_t)warp * S * stage_bytes;
     int *prefix = reinterpret_cast<int *>(smem + (size_t)kWarps * S * stage_bytes);   // [B]
     int *ntok = prefix + p.B;                                                         // [B]
     const bool with_new = p.k_new != nullptr;
     ptx::griddep_wait();
-
     ptx::griddep_launch_dependents();
 
     // Entries and tiles before each sequence (of one head set), and all of them.
     auto lo_of = [&](int n) { return first_slot(p, n); };
-    auto tiles_of = [&](int n) { return unit_tiles(p, n); };
+    auto tiles_of = [&](int n) { return unit_tiles<kTile>(p, n); };
     int total;
     const int sets = (p.G + HN - 1) / HN, Hu = p.Hkv * sets;
     {
@@ -210,58 +196,32 @@ __global__ void __launch_bounds__(kThreads) attention16_kernel(AttnParams p) {
         total = all * Hu;       // at most 2^31 - 1: a plan's limit
         __syncthreads();
     }
-    Cuts cuts(total, gridDim.x, p.max_chunks);
-    if (p.whole_units) cuts.count = p.B * Hu;      // chunk c is unit c, and blocks take turns
-    if ((int)blockIdx.x >= cuts.count) return;
-    const bool dynamic = !p.whole_units && cuts.count > (int)gridDim.x;
+    // Chunks of equal size, or whole units that the blocks take in turns.
+    const int chunk = (total + gridDim.x - 1) / gridDim.x;
+    if (p.whole_units ? (int)blockIdx.x >= p.B * Hu : (int)blockIdx.x * (int64_t)chunk >= total) return;
 
-    // A number from the queue, as the chunk it stands for.  Every block draws until its number
-    // is past the end; the very last number drawn leaves the queue as it was found.
-    auto chunk_drawn = [&](uint32_t v) {
-        if (v == (uint32_t)(cuts.count - 1)) *p.queue = 0;
-        return (int)min(v + gridDim.x, (uint32_t)cuts.count);
-    };
     auto enter = [&](Walk &w) {
         w.n = abs(ntok[w.b]);
         w.lo = lo_of(w.n);
         w.first = w.lo / kTile * kTile;
         w.tiles = tiles_of(w.n);
     };
-    // To chunk c, the k-th of this block.
-    auto begin_chunk = [&](Walk &w, int c) {
+    // The next segment of the walk: the tiles of one unit in the chunk.  False at the end.
+    auto next_segment = [&](Walk &w) {
         if (p.whole_units) {
-            w.b = c / Hu;
-            w.hv = c - w.b * Hu;
+            const int u = (int)blockIdx.x + w.count * (int)gridDim.x;
+            if (u >= p.B * Hu) return false;
+            ++w.count;
+            w.b = u / Hu;
+            w.hv = u - w.b * Hu;
             enter(w);
-            w.unit = w.x = 0;
-            w.x1 = 1 + w.tiles;
-            return;
+            w.tile = 0;
+            w.left = w.tiles;
+            return true;
         }
-        w.x = cuts.begin(c);
-        w.x1 = cuts.end(c);
-        const int q = w.x / Hu;
-        int lo = 0, hi = p.B - 1;        // the last sequence with prefix <= q
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (prefix[mid] <= q) lo = mid; else hi = mid - 1;
-        }
-        w.b = lo;
-        enter(w);
-        w.hv = (w.x - prefix[lo] * Hu) / (w.tiles + 1);
-        w.unit = prefix[lo] * Hu + w.hv * (w.tiles + 1);
-    };
-    // The next segment of the walk: a unit's tiles in one chunk.  False at the end, or when the
-    // number of the next chunk is not yet known to this warp: it knows them up to k_known.
-    auto next_segment = [&](Walk &w, int k_known, bool fresh = false) {
         for (;;) {
-            if (w.x >= w.x1) {
-                if (!(dynamic || p.whole_units) || w.k + 1 > k_known) return false;
-                const int c = p.whole_units ? (int)(blockIdx.x + (w.k + 1) * gridDim.x) : drawn[(w.k + 1) & 3];
-                if (c >= cuts.count) return false;
-                ++w.k;
-                begin_chunk(w, c);
-                fresh = true;
-            } else if (w.x >= w.unit + 1 + w.tiles) {
+            if (w.x >= w.x1) return false;
+            if (w.x >= w.unit + 1 + w.tiles) {
                 w.unit += 1 + w.tiles;
                 if (++w.hv == Hu) {
                     w.hv = 0;
@@ -272,60 +232,82 @@ __global__ void __launch_bounds__(kThreads) attention16_kernel(AttnParams p) {
             const int from = max(w.x, w.unit + 1), to = min(w.x1, w.unit + 1 + w.tiles);
             w.x = max(to, w.x + 1);
             if (from < to) {
+                ++w.count;
                 w.tile = from - (w.unit + 1);
                 w.left = to - from;
-                w.first_of_chunk = fresh;
                 return true;
             }
         }
     };
     Walk use;
-    use.k = 0;
-    begin_chunk(use, blockIdx.x);
-    use.left = 0;
+    use.left = use.count = 0;
+    if (!p.whole_units) {
+        use.x = blockIdx.x * chunk;
+        use.x1 = min(total, use.x + chunk);
+        const int q = use.x / Hu;
+        int lo = 0, hi = p.B - 1;        // the last sequence with prefix <= q
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (prefix[mid] <= q) lo = mid; else hi = mid - 1;
+        }
+        use.b = lo;
+        enter(use);
+        use.hv = (use.x - prefix[lo] * Hu) / (use.tiles + 1);
+        use.unit = prefix[lo] * Hu + use.hv * (use.tiles + 1);
+    }
 
     // The producer side: kLanes lanes copy a row, 16 bytes each, kRows rows at a time.
     constexpr int kLanes = DP / 8, kRows = 32 / kLanes;
     Walk in = use;
-    const bool more = next_segment(in, 0, true);
+    const bool more = next_segment(in);
     int ahead = 0, in_slot = 0;         // stages under way, and the next one to fill
     const int row0 = lane / kLanes, col = lane % kLanes;
-    const bool copies = col * 8 < p.D;
+    const bool copies = col * 8 < D;
     // With pages of whole sixteens a warp's slots lie in one page.
     const bool one_page = p.cache.page % 16 == 0;
     const int64_t lane_off = (one_page ? row0 * p.cache.row_stride : 0) + col * 8;
     const int64_t row_step = kRows * p.cache.row_stride;
     const uint32_t lane_dst = ptx::smem_u32(ring) + row0 * pitch + col * 16;
-    int page_no = 0;           // of slot (lane & 15) of the next stage, under way
+    // Page numbers, fetched before they are wanted: one for each of 32 tiles where a warp's slots
+    // lie in one page (lane i has tile pages_from + i's), else those of the next tile's slots.
+    int pages = 0, pages_from = 0;
     auto page_index = [&](int j) { return p.page_shift >= 0 ? j >> p.page_shift : j / p.cache.page; };
-    auto fetch_page = [&]() {
-        const int j = in.first + in.tile * kTile + warp * 16 + (lane & 15);
-        page_no = j >= in.lo && j < in.n
-                      ? __ldg(p.cache.tables + (int64_t)in.b * p.cache.table_pitch + page_index(j))
-                      : -1;
+    auto fetch_pages = [&]() {
+        const int j0 = in.first + in.tile * kTile + warp * 16;
+        const int j = one_page ? j0 + lane * kTile : j0 + (lane & 15);
+        pages_from = in.tile;
+        // A warp's sixteen slots may begin before the window or end past the last token.
+        const bool wanted = one_page ? j + 15 >= in.lo && j < in.n : j >= in.lo && j < in.n;
+        pages = wanted ? __ldg(p.cache.tables + (int64_t)in.b * p.cache.table_pitch + page_index(j)) : -1;
     };
     // Fills a stage with the next tile, if the walk has one.
-    auto issue = [&](int k_known) {
-        if (in.left == 0) {
-            if (!more || !next_segment(in, k_known)) return;
-            fetch_page();
-        }
+    auto issue = [&]() {
+        if (in.left == 0) return;
         {
             const int j0 = in.first + in.tile * kTile + warp * 16, j = j0 + (lane & 15);
             const int hk = sets == 1 ? in.hv : in.hv / sets;
-            const bool ok = (unsigned)page_no < (unsigned)p.cache.num_pages;
+            const int page_no = one_page ? __shfl_sync(0xffffffffu, pages, in.tile - pages_from) : pages;
+            const bool inside = j >= in.lo && j < in.n;
+            const bool ok = inside && (unsigned)page_no < (unsigned)p.cache.num_pages;
             const unsigned mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
             int64_t off = page_no * p.cache.page_stride + hk * p.cache.head_stride +
                           (j - page_index(j) * p.cache.page) * p.cache.row_stride;
             if (lane == 0) slot_masks[warp][in_slot] = mask;
-            if (mask != 0xffffu && !ok && j >= in.lo && j < in.n)
+            if (inside && !ok)
                 atomicOr(p.cache.status, kStatusBadPage);
             const uint32_t dst = lane_dst + in_slot * stage_bytes;
             const int newest = ntok[in.b];       // -n where slot n - 1 is the new token's
             if (mask == 0xffffu && one_page && !(newest < 0 && -newest - 1 < j0 + 16)) {
                 off = __shfl_sync(0xffffffffu, off, 0) + lane_off;
                 const T *ks = static_cast<const T *>(p.k) + off, *vs = static_cast<const T *>(p.v) + off;
-                if (copies) {
+                if (kD && p.cache.row_stride == kD) {
+                    // Rows one behind the other: every offset is a constant.
+#pragma unroll
+                    for (int i = 0; copies && i < KS; ++i) {
+                        copy16(dst + i * kRows * pitch, ks + i * kRows * kD, true);
+                        copy16(dst + (16 + i * kRows) * pitch, vs + i * kRows * kD, true);
+                    }
+                } else if (copies) {
 #pragma unroll
                     for (int i = 0; i < KS; ++i) {
                         copy16(dst + i * kRows * pitch, ks, true);
@@ -344,7 +326,7 @@ __global__ void __launch_bounds__(kThreads) attention16_kernel(AttnParams p) {
                     if (!copies) continue;
                     if (on && newest == -(j0 + row + 1)) {
                         // The new token's row comes from the arguments.
-                        const int64_t x = in.b * p.kv_stride + (int64_t)hk * p.D + col * 8;
+                        const int64_t x = in.b * p.kv_stride + (int64_t)hk * D + col * 8;
                         ks = static_cast<const T *>(p.k_new) + x;
                         vs = static_cast<const T *>(p.v_new) + x;
                     }
@@ -359,55 +341,44 @@ __global__ void __launch_bounds__(kThreads) attention16_kernel(AttnParams p) {
         ++ahead;
         if (++in_slot == S) in_slot = 0;
         ++in.tile;
-        if (--in.left == 0 && !next_segment(in, k_known)) return;
-        fetch_page();
-    };
-    if (more) fetch_page();
-#pragma unroll 1
-    for (int s = 0; s < S - 1; ++s) issue(0);
-    uint32_t number = 0;          // thread 0: drawn for the chunk after the next, under way
-    bool drawing = false;
-    if (dynamic) {
-        if (t == 0) {
-            drawn[1] = chunk_drawn(atomicAdd(p.queue, 1u));
-            if (drawn[1] < cuts.count) {
-                number = atomicAdd(p.queue, 1u);
-                drawing = true;
-            }
+        if (--in.left == 0) {
+            if (next_segment(in)) fetch_pages();
+        } else if (!one_page || in.tile - pages_from == 32) {
+            fetch_pages();
         }
-        __syncthreads();
-    }
-
+    };
+    if (more) fetch_pages();
+#pragma unroll 1
+    for (int s = 0; s < S - 1; ++s) issue();
     const int r0 = lane / 4, quad = lane % 4;
     int slot = 0;
     uint32_t q[NH][KS][2];
     // Queries as the products' second operand: heads r0 (and r0 + 8), columns quad * 2.
     auto load_queries = [&]() {
         const int hk = use.hv / sets, set = use.hv % sets, rows = p.G - set * HN;
-        const T *qb = static_cast<const T *>(p.q) + use.b * p.q_stride + (hk * p.G + set * HN) * p.D;
+        const T *qb = static_cast<const T *>(p.q) + use.b * p.q_stride + (hk * p.G + set * HN) * D;
 #pragma unroll
         for (int h = 0; h < NH; ++h)
 #pragma unroll
             for (int i = 0; i < KS; ++i)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    q[h][i][e] = h * 8 + r0 < rows && i * 16 < p.D
+                    q[h][i][e] = h * 8 + r0 < rows && i * 16 < D
                                      ? __ldg(reinterpret_cast<const uint32_t *>(
-                                           qb + (h * 8 + r0) * p.D + i * 16 + e * 8 + quad * 2))
+                                           qb + (h * 8 + r0) * D + i * 16 + e * 8 + quad * 2))
                                      : 0u;
     };
-    bool go = next_segment(use, 0, true);
+    bool go = next_segment(use);
     if (go) load_queries();
     while (go) {
         // One unit's share of a chunk.
         const int hk = use.hv / sets, set = use.hv % sets;
-        const int rows = min(HN, p.G - set * HN), k = use.k;
+        const int rows = min(HN, p.G - set * HN);
         const int64_t h0 = (int64_t)use.b * p.Hq + (int64_t)hk * p.G + set * HN;   // first query head
         const int steps = use.left;
-        const int chunk = k == 0 ? blockIdx.x : drawn[k & 3];
         const int unit_b = use.b;
         const bool whole = use.tile == 0 && steps == use.tiles;
-        const int part = chunk * 2 + (use.first_of_chunk ? 0 : 1);
+        const int part = blockIdx.x * 2 + (use.count == 1 ? 0 : 1);
         // The slot that this unit puts in the cache, once for a KV head.
         const int new_slot = ntok[use.b] < 0 && set == 0 ? use.n - 1 : -1;
         const int j_first = use.first + use.tile * kTile + warp * 16;
@@ -421,7 +392,6 @@ __global__ void __launch_bounds__(kThreads) attention16_kernel(AttnParams p) {
             for (int i = 0; i < KS; ++i) o[h][i][0] = o[h][i][1] = o[h][i][2] = o[h][i][3] = 0.0f;
         }
         for (int step = 0; step < steps; ++step) {
-            if (ahead == 0) issue(k + 1);
             if (ahead >= S - 1)
                 asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
             else
@@ -429,14 +399,14 @@ __global__ void __launch_bounds__(kThreads) attention16_kernel(AttnParams p) {
             __syncwarp();
             const uint32_t mask = slot_masks[warp][slot];
             --ahead;
-            issue(k + 1);
+            issue();
             const unsigned char *slot_base = ring + slot * stage_bytes;
             const uint32_t ks = ptx::smem_u32(slot_base), vs = ks + 16 * pitch;
             if (++slot == S) slot = 0;
             if (new_slot >= 0) {
                 // The new token's row goes on to the cache.
                 const int row = new_slot - (j_first + step * kTile);
-                if (row >= 0 && row < 16 && (mask >> row & 1) && lane < p.D / 8) {
+                if (row >= 0 && row < 16 && (mask >> row & 1) && lane < D / 8) {
                     const int pg = p.cache.tables[(int64_t)unit_b * p.cache.table_pitch + page_index(new_slot)];
                     const int64_t to = pg * p.cache.page_stride + hk * p.cache.head_stride +
                                        (new_slot - page_index(new_slot) * p.cache.page) * p.cache.row_stride +
@@ -454,7 +424,7 @@ __global__ void __launch_bounds__(kThreads) attention16_kernel(AttnParams p) {
                 const uint32_t a = ks + ((lane & 7) + (lane >> 3 & 1) * 8) * pitch + (lane >> 4) * 16;
 #pragma unroll
                 for (int i = 0; i < KS; ++i) {
-                    if (i * 16 >= p.D) break;
+                    if (i * 16 >= D) break;
                     uint32_t k[4];
                     ldmatrix_x4(k, a + i * 32);
 #pragma unroll
@@ -531,7 +501,7 @@ __global__ void __launch_bounds__(kThreads) attention16_kernel(AttnParams p) {
                 const uint32_t a = vs + ((lane & 7) + (lane >> 4) * 8) * pitch + (lane >> 3 & 1) * 16;
 #pragma unroll
                 for (int i = 0; i < KS; ++i) {
-                    if (i * 16 >= p.D) break;
+                    if (i * 16 >= D) break;
                     uint32_t v[4];
                     ldmatrix_x4_trans(v, a + i * 32);
 #pragma unroll
@@ -545,7 +515,7 @@ __global__ void __launch_bounds__(kThreads) attention16_kernel(AttnParams p) {
 
         // Join the four warps, through the stage that each has just used: it is filled again in the
         // next step at the earliest, and holds [HN][D + 4] fp32.
-        const int used = (slot == 0 ? S : slot) - 1, join_pitch = p.D + 4;
+        const int used = (slot == 0 ? S : slot) - 1, join_pitch = D + 4;
         {
             float *mine = reinterpret_cast<float *>(ring + used * stage_bytes);
             __syncwarp();
@@ -565,29 +535,21 @@ __global__ void __launch_bounds__(kThreads) attention16_kernel(AttnParams p) {
                     float *row = mine + head * join_pitch + r0;
 #pragma unroll
                     for (int i = 0; i < KS; ++i) {
-                        if (i * 16 >= p.D) break;
+                        if (i * 16 >= D) break;
                         row[i * 16] = o[h][i][e];
                         row[i * 16 + 8] = o[h][i][e + 2];
                     }
                 }
         }
-        if (drawing) {
-            drawn[(k + 2) & 3] = chunk_drawn(number);
-            drawing = false;
-        }
         __syncthreads();
         // The next unit's queries come in meanwhile.
-        go = next_segment(use, k + 1);
+        go = next_segment(use);
         if (go) load_queries();
-        if (t == 0 && dynamic && use.k != k && drawn[(k + 2) & 3] < cuts.count) {
-            number = atomicAdd(p.queue, 1u);
-            drawing = true;
-        }
         constexpr int kQuads = DP / 4;
 #pragma unroll
         for (int x0 = 0; x0 < HN * kQuads; x0 += kThreads) {
             const int head = (x0 + t) / kQuads, d = (x0 + t) % kQuads * 4;
-            if (head >= rows || d >= p.D) continue;
+            if (head >= rows || d >= D) continue;
             float top = kNegInf, sum = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) top = fmaxf(top, red_m[w][head]);
@@ -605,12 +567,12 @@ __global__ void __launch_bounds__(kThreads) attention16_kernel(AttnParams p) {
             }
             if (whole) {
                 const float r = sum > 0.0f ? 1.0f / sum : 0.0f;
-                *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + (h0 + head) * p.D + d) =
+                *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + (h0 + head) * D + d) =
                     make_uint2(P::pack(v.x * r, v.y * r), P::pack(v.z * r, v.w * r));
                 if (p.scores && d == 0) p.stats[h0 + head] = make_float2(top, sum);
             } else {
                 const int64_t row = (int64_t)part * p.part_rows + head;
-                *reinterpret_cast<float4 *>(p.part_o + row * p.D + d) = v;
+                *reinterpret_cast<float4 *>(p.part_o + row * D + d) = v;
                 if (d == 0) p.part_ml[row] = make_float2(top, sum);
             }
         }
@@ -624,8 +586,9 @@ __global__ void __launch_bounds__(kThreads) attention16_kernel(AttnParams p) {
 // is in L2; its time is the launch, which overlaps the first kernel's end, and one or two trips to
 // L2.
 constexpr int kJoinWarps = 8;
-template <typename T, int kRowWarps, int N>
+template <typename T, int DP, int kRowWarps>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(AttnParams p, int grid) {
+    constexpr int N = DP > 128 ? 2 : 1, kTile = 16 * Shape<DP>::kWarps;
     constexpr int kDepth = 16 / N, kRows = kJoinWarps / kRowWarps;
     __shared__ float2 ml[kJoinWarps];
     __shared__ __align__(16) float outs[kJoinWarps][256];
@@ -637,7 +600,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(AttnParams p, int
     const int hn = p.G <= 8 ? 8 : 16, sets = (p.G + hn - 1) / hn, Hu = p.Hkv * sets;
     int before = 0, all = 0, mine = 0;
     for (int i = lane; i < p.B; i += 32) {
-        const int tiles = unit_tiles(p, token_count(p.cache, i, p.k_new != nullptr));
+        const int tiles = unit_tiles<kTile>(p, token_count(p.cache, i, p.k_new != nullptr));
         all += 1 + tiles;
         if (i < b) before += 1 + tiles;
         if (i == b) mine = tiles;
@@ -645,11 +608,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(AttnParams p, int
     before = __reduce_add_sync(0xffffffffu, before);
     all = __reduce_add_sync(0xffffffffu, all);
     const int tiles = __reduce_add_sync(0xffffffffu, mine);
-    const Cuts cuts(all * Hu, grid, p.max_chunks);
+    const int total = all * Hu, chunk = (total + grid - 1) / grid;
     const int hk = h / p.G, g = h % p.G, hv = hk * sets + g / hn, row = g % hn;
     const int unit = before * Hu + hv * (tiles + 1);
-    const int c0 = cuts.of(unit + 1), parts = on ? cuts.of(unit + tiles) - c0 + 1 : 1;
-    const int head = c0 * 2 + (cuts.begin(c0) >= unit ? 0 : 1);
+    const int c0 = (unit + 1) / chunk, parts = on ? (unit + tiles) / chunk - c0 + 1 : 1;
+    // The first part is its chunk's first unless the chunk has tiles of an earlier unit.
+    const int head = c0 * 2 + (c0 * chunk >= unit ? 0 : 1);
     ptx::griddep_wait();
     if (kRowWarps == kJoinWarps && parts == 1) return;
     // This warp's run of the parts.

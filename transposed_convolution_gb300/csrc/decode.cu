@@ -13,13 +13,12 @@ size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 int esize_of(const ctr_attn_s *pl) { return pl->dtype == CTR_F32 ? 4 : 2; }
 
-int blocks_per_sm(const ctr_attn_s *pl) { return pl->D > 128 ? 1 : ctr::kMaxPerSm; }
 int part_rows(const ctr_attn_s *pl) { return (int)std::min<int64_t>(16, pl->Hq / pl->Hkv); }
 
-// The status word and the queue (cleared by ctr_attn_reset), the parts of shared units, and with
+// The status word (cleared by ctr_attn_reset), the parts of shared units, and with
 // weights the softmax statistics and scores.
 void layout_workspace(ctr_attn_s *pl) {
-    const int64_t parts = 2 * ctr::kMaxChunks * blocks_per_sm(pl) * (int64_t)pl->num_sms;
+    const int64_t parts = 2 * ctr::kMaxPerSm * (int64_t)pl->num_sms;
     pl->score_pitch = (pl->max_pages * pl->page + ctr::kScoreTile - 1) / ctr::kScoreTile * ctr::kScoreTile;
     pl->off_parts = 256;
     pl->off_ml = pl->off_parts + align256((size_t)(parts * part_rows(pl) * pl->D) * sizeof(float));
@@ -173,11 +172,9 @@ ctr_status ctr_attn_forward(ctr_attn_t pl, const void *q, int64_t q_stride, cons
     p.kv_stride = kv_stride;
     p.out = out;
     char *ws = static_cast<char *>(pl->ws);
-    p.queue = reinterpret_cast<uint32_t *>(ws + 128);
     p.part_o = reinterpret_cast<float *>(ws + pl->off_parts);
     p.part_ml = reinterpret_cast<float2 *>(ws + pl->off_ml);
     p.part_rows = part_rows(pl);
-    p.max_chunks = ctr::kMaxChunks * blocks_per_sm(pl) * pl->num_sms;
     if (pl->weights) {
         p.stats = reinterpret_cast<float2 *>(ws + pl->off_stats);
         p.scores = reinterpret_cast<float *>(ws + pl->off_scores);

@@ -47,8 +47,7 @@ struct AttnParams {
     // and a later one): [part_rows][D] outputs and [part_rows] (maximum, sum) each.
     float *part_o;
     float2 *part_ml;
-    uint32_t *queue;         // the next chunk's number
-    int part_rows, max_chunks;
+    int part_rows;
     int whole_units;         // every chunk is a whole unit: no parts
     int page_shift;          // log2 of the page size, or -1
     const float *w_in;
@@ -70,14 +69,12 @@ struct EvictParams {
     int B, Hkv, row_bytes, esize;
 };
 
-// Blocks of an attention launch: `per_sm` to an SM, of which the workspace holds kMaxPerSm.
-constexpr int kMaxPerSm = 2;
-// Chunks the work is cut into, for each block: one large, and at most nine small ones.
-constexpr int kMaxChunks = 10;
+// Most blocks an SM that an attention launch has; the workspace holds two parts for each.
+constexpr int kMaxPerSm = 4;
+// Score rows are padded to whole tiles (64 or 96 slots).
+constexpr int kScoreTile = 192;
 // Caches of up to this many slots a sequence are cut into whole units.
 constexpr int kWholeSlots = 256;
-// Tiles of the 16-bit kernel's scores (slots): its score rows are padded to whole tiles.
-constexpr int kScoreTile = 64;
 
 cudaError_t launch_attention(const ctr_attn_s *pl, const AttnParams &p, cudaStream_t st);
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t st);
