@@ -175,6 +175,7 @@ attention16_kernel(AttnParams p) {
             ntok[b] = with_new && n > len && len >= 0 ? -n : n;
             sum += 1 + tiles_of(n);
         }
+        __syncwarp();
         int incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o *= 2) {
@@ -605,6 +606,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(AttnParams p, int
         if (i < b) before += 1 + tiles;
         if (i == b) mine = tiles;
     }
+    __syncwarp();
     before = __reduce_add_sync(0xffffffffu, before);
     all = __reduce_add_sync(0xffffffffu, all);
     const int tiles = __reduce_add_sync(0xffffffffu, mine);

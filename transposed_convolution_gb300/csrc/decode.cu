@@ -77,12 +77,7 @@ ctr_status ctr_attn_create(ctr_attn_t *out, int64_t B, int64_t H_q, int64_t H_kv
     pl->dtype = dtype;
     pl->layout = CTR_CACHE_HEAD_MAJOR;
     pl->scale = (float)(1.0 / std::sqrt((double)D));
-    int dev = ctr::current_device(), sms = 0;
-    if (dev < 0 || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        sms = 152;
-    }
-    pl->num_sms = sms > 0 ? sms : 152;
+    pl->num_sms = ctr::device_sms();
     layout_workspace(pl);
     *out = pl;
     return CTR_OK;

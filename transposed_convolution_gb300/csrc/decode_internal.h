@@ -76,6 +76,17 @@ constexpr int kScoreTile = 192;
 // Caches of up to this many slots a sequence are cut into whole units.
 constexpr int kWholeSlots = 256;
 
+// SMs of the current device (152 without one).
+inline int device_sms() {
+    const int dev = current_device();
+    int n = 0;
+    if (dev < 0 || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    return n > 0 ? n : 152;
+}
+
 cudaError_t launch_attention(const ctr_attn_s *pl, const AttnParams &p, cudaStream_t st);
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t st);
 

@@ -1,18 +1,47 @@
 // sampler.cu -- sampling with temperature, top-k, top-p and min-p from given random numbers.
+//
+// Every filter keeps a prefix of the order (logit descending, index ascending), so the kept set
+// is a lowest key, and how many of the tokens with that key stay.  The logits are read once, which
+// bounds the operator: V elements of 2 or 4 bytes a row, and the random numbers of the kept
+// tokens only.  25 million of them take the CUDA cores about as long as the memory, so the work on
+// each is kept to half a packed maximum, and then a conversion, a scaled difference and an
+// exponential (for the mass of top-p).  A row's block (or cluster of blocks)
+//   1. reads its part into shared memory and takes the maximum;
+//   2. sums the mass, and lists the tokens within 2^-kListBits of the maximum (or min_p of it:
+//      nothing below is kept then) at the cluster's first block; the others are done;
+//   3. finds the cuts among the listed tokens, by a histogram of their distance to the maximum
+//      and, inside the bin that a cut falls into, histograms of their keys;
+//   4. races the kept ones: best w / noise, ties to the lowest index.
+// Where the list cannot hold the cuts (flat logits without min_p) the first block does 3 and 4 on
+// the whole row, which it reads again.
+//
+// Sums: a thread's masses are added in fp32 in a fixed order, everything beyond as 64-bit integers in
+// units of 2^-40, and the list's order matters to nothing: equal inputs give equal tokens.
+#include <algorithm>
+#include <cooperative_groups.h>
 #include <cstdio>
 #include <new>
 
 #include "decode_device.cuh"
+#include "ptx.cuh"
+
+namespace cg = cooperative_groups;
 
 struct ctr_sampler_s {
     int64_t rows, vocab;
-    int dtype;
+    int dtype, num_sms;
 };
 
 namespace ctr {
 namespace {
 
-constexpr int kThreads = 512;
+typedef unsigned long long u64;
+constexpr float kNegInf = -__builtin_inff();
+constexpr int kBins = 1024;
+constexpr int kListMax = 2048;
+constexpr float kListBits = 12.0f;    // tokens within 2^-12 of the maximum are listed
+constexpr int kMaxCluster = 8;
+constexpr int kStageBytes = 80 * 1024;  // most logits a block keeps in shared memory
 
 struct SampleParams {
     const void *logits;
@@ -21,142 +50,580 @@ struct SampleParams {
     const float *temperature, *top_p, *min_p;
     const int32_t *top_k;
     int64_t *tokens;
-    int vocab;
+    int vocab, chunk;        // elements of a row, and of a block's part (a multiple of 16)
 };
 
 // Order-preserving key of a logit (NaN as -inf, -0 as +0) and back.
 __device__ __forceinline__ uint32_t logit_key(float l) {
-    if (l != l) l = -__builtin_inff();
-    const uint32_t u = __float_as_uint(l + 0.0f);
+    const uint32_t u = __float_as_uint(fmaxf(l, kNegInf) + 0.0f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 __device__ __forceinline__ float key_logit(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
-
 // w_i = exp((l - m) / T), 1 at the maximum (also when it is infinite).
 __device__ __forceinline__ float weight_of(float l, float m, float T) {
     return l == m ? 1.0f : expf((l - m) / T);
 }
 // Masses are sums of weights (at most 1, up to 2^20 of them) in units of 2^-40.
-__device__ __forceinline__ unsigned long long fixed_of(float w) {
-    return __float2ull_rn(w * 1099511627776.0f);
+__device__ __forceinline__ u64 fixed_of(float w) { return __float2ull_rn(w * 1099511627776.0f); }
+__device__ __forceinline__ float pow2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-template <typename V, typename F>
-__device__ V block_reduce(V v, V *red, F f) {
+// The best score so far and its index; equal scores go to the lower one.
+struct Best {
+    float score = -1.0f;
+    int index = 0;
+    __device__ __forceinline__ void offer(float v, int i) {
+        if (v > score || (v == score && i < index)) {
+            score = v;
+            index = i;
+        }
+    }
+    // Larger is better; 0 for none.
+    __device__ __forceinline__ u64 packed() const {
+        return score < 0.0f ? 0 : (u64)__float_as_uint(score) << 32 | (uint32_t)~index;
+    }
+};
+
+// The kept prefix: keys above `low`, and of those equal to it the `ties` with the lowest indices.
+struct Cut {
+    uint32_t low;
+    uint32_t ties;           // 0xffffffff: all
+};
+
+template <int kThreads> struct Shared {
+    u64 red[kThreads / 32], red2[kThreads / 32];
+    u64 mass[kBins];
+    uint32_t count[kBins];
+    // What a boundary search found: its bin and the counts and masses before and in it.
+    uint32_t bin, before, inside;
+    u64 mass_before, mass_inside;
+    uint32_t low, high;              // lowest and highest key of a bin
+    // Written by the cluster's blocks: the maxima at every block, the others at the first.
+    uint32_t tops[kMaxCluster];
+    u64 bests[kMaxCluster];
+    u64 total;                       // mass of the row
+    int listed;                      // tokens listed
+    uint32_t list_key[kListMax], list_index[kListMax];
+};
+
+// The largest (or the sum) of the block's values.  Not inlined: behind a loop that lanes leave at
+// different times, nvcc 13.0.88 otherwise copies the shuffles into both ways out of it, and lanes
+// that meet at different copies do not see one another.
+template <int kThreads, bool kSum> __device__ __noinline__ u64 block_reduce(u64 v, u64 *red) {
+    auto f = [](u64 a, u64 b) { return kSum ? a + b : a > b ? a : b; };
+#pragma unroll
     for (int o = 16; o; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
     __syncthreads();
     if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
     __syncthreads();
     v = red[0];
+#pragma unroll
     for (int i = 1; i < kThreads / 32; ++i) v = f(v, red[i]);
     return v;
 }
+template <int kThreads> __device__ __forceinline__ u64 block_max(u64 v, u64 *red) {
+    return block_reduce<kThreads, false>(v, red);
+}
+template <int kThreads> __device__ __forceinline__ u64 block_sum(u64 v, u64 *red) {
+    return block_reduce<kThreads, true>(v, red);
+}
 
-// One block a row.  Every filter keeps a prefix of the order (logit descending, index
-// ascending), so the kept set is: keys above `cut`, and the first `ties` tokens with key `cut`.
-template <typename T>
-__global__ void sample_kernel(SampleParams p) {
-    typedef unsigned long long u64;
-    __shared__ u64 red[kThreads / 32];
-    const int row = blockIdx.x, t = threadIdx.x, V = p.vocab;
+// 16 bytes' elements as fp32, and the largest of them (NaN only if all are).
+__device__ __forceinline__ void unpack(const uint4 &u, float (&f)[4], float) {
+    f[0] = __uint_as_float(u.x);
+    f[1] = __uint_as_float(u.y);
+    f[2] = __uint_as_float(u.z);
+    f[3] = __uint_as_float(u.w);
+}
+__device__ __forceinline__ __half2 pair_of(uint32_t u, __half) {
+    return __halves2half2(__ushort_as_half((unsigned short)u), __ushort_as_half((unsigned short)(u >> 16)));
+}
+__device__ __forceinline__ __nv_bfloat162 pair_of(uint32_t u, __nv_bfloat16) {
+    return __halves2bfloat162(__ushort_as_bfloat16((unsigned short)u),
+                              __ushort_as_bfloat16((unsigned short)(u >> 16)));
+}
+__device__ __forceinline__ float2 floats_of(__half2 v) { return __half22float2(v); }
+__device__ __forceinline__ float2 floats_of(__nv_bfloat162 v) { return __bfloat1622float2(v); }
+template <typename T> __device__ __forceinline__ void unpack(const uint4 &u, float (&f)[8], T tag) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = floats_of(pair_of(w[i], tag));
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+    }
+}
+__device__ __forceinline__ float max_of(const uint4 &u, float) {
+    return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)),
+                 fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+}
+template <typename T> __device__ __forceinline__ float max_of(const uint4 &u, T tag) {
+    const float2 f = floats_of(__hmax2(__hmax2(pair_of(u.x, tag), pair_of(u.y, tag)),
+                                       __hmax2(pair_of(u.z, tag), pair_of(u.w, tag))));
+    return fmaxf(f.x, f.y);
+}
+
+// Bits of -inf.
+__device__ __forceinline__ uint32_t neg_inf_bits(float) { return 0xff800000u; }
+__device__ __forceinline__ uint32_t neg_inf_bits(__half) { return 0xfc00u; }
+__device__ __forceinline__ uint32_t neg_inf_bits(__nv_bfloat16) { return 0xff80u; }
+
+// A block's part of a row, 16 bytes at a time from the 16-byte boundary `skew` elements before it;
+// what a vector holds beside the part's elements reads as -inf, which no filter keeps.
+template <typename T> struct Part {
+    const T *at;             // the boundary
+    int skew, count;
+    int base;                // index of the first element
+    static constexpr int kVec = 16 / sizeof(T);
+    __device__ __forceinline__ int vecs() const { return (skew + count + kVec - 1) / kVec; }
+    __device__ __forceinline__ int index(int v) const { return base + v * kVec - skew; }
+    __device__ __forceinline__ uint4 load(int v) const {
+        const int first = v * kVec - skew;
+        if (first >= 0 && first + kVec <= count) return __ldg(reinterpret_cast<const uint4 *>(at) + v);
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (sizeof(T) == 4) {
+                w[i] = (unsigned)(first + i) < (unsigned)count
+                           ? __ldg(reinterpret_cast<const uint32_t *>(at) + v * kVec + i) : neg_inf_bits(T());
+            } else {
+                w[i] = 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int e = 2 * i + h;
+                    const uint32_t x = (unsigned)(first + e) < (unsigned)count
+                                           ? (uint32_t)__ldg(reinterpret_cast<const unsigned short *>(at) + v * kVec + e)
+                                           : neg_inf_bits(T());
+                    w[i] |= x << (16 * h);
+                }
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// Finds the boundary bin of the histograms in `s`: the first whose counts (or masses) bring the
+// sum to `target`; target is at most the total.  Called by all threads.
+template <int kThreads>
+__device__ __noinline__ void find_bin(Shared<kThreads> &s, bool by_mass, u64 target) {
+    constexpr int kEach = kBins / kThreads;
+    static_assert(kBins % kThreads == 0, "bins");
+    const int t = threadIdx.x, lane = t % 32, warp = t / 32;
+    u64 c[kEach], m[kEach], cs = 0, ms = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        c[i] = s.count[t * kEach + i];
+        m[i] = s.mass[t * kEach + i];
+        cs += c[i];
+        ms += m[i];
+    }
+    u64 ci = cs, mi = ms;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const u64 a = __shfl_up_sync(0xffffffffu, ci, o), b = __shfl_up_sync(0xffffffffu, mi, o);
+        if (lane >= o) {
+            ci += a;
+            mi += b;
+        }
+    }
+    __syncthreads();
+    if (lane == 31) {
+        s.red[warp] = ci;
+        s.red2[warp] = mi;
+    }
+    __syncthreads();
+    u64 cb = ci - cs, mb = mi - ms;
+    for (int i = 0; i < warp; ++i) {
+        cb += s.red[i];
+        mb += s.red2[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const u64 b = by_mass ? mb : cb, in = by_mass ? m[i] : c[i];
+        if (b < target && target <= b + in) {
+            s.bin = t * kEach + i;
+            s.before = (uint32_t)cb;
+            s.inside = (uint32_t)c[i];
+            s.mass_before = mb;
+            s.mass_inside = m[i];
+        }
+        cb += c[i];
+        mb += m[i];
+    }
+    __syncthreads();
+}
+
+// Histograms of keys in [lo, hi], each of the bin of the last one that the boundary falls into, until
+// that holds one key, one element, or is kept whole.  each(f) calls f(key, weight()) of every
+// element; count0 and mass0 are of the elements above hi.
+template <int kThreads, typename Each>
+__device__ Cut cut_by_keys(Shared<kThreads> &s, uint32_t lo, uint32_t hi, bool by_mass, u64 target,
+                           u64 count0, u64 mass0, u64 *mass, Each each) {
+    for (;;) {
+        const int shift = max(0, 32 - __clz(hi - lo) - 10);
+        for (int i = threadIdx.x; i < kBins; i += kThreads) {
+            s.count[i] = 0;
+            s.mass[i] = 0;
+        }
+        __syncthreads();
+        each([&](uint32_t key, auto weight) {
+            if (key < lo || key > hi) return;
+            const uint32_t bin = (hi - key) >> shift;
+            atomicAdd(&s.count[bin], 1u);
+            const u64 w = weight();
+            if (w) atomicAdd(&s.mass[bin], w);
+        });
+        __syncthreads();
+        find_bin<kThreads>(s, by_mass, target - (by_mass ? mass0 : count0));
+        const uint32_t bin = s.bin, inside = s.inside;
+        const u64 before = count0 + s.before, above = mass0 + s.mass_before, in = s.mass_inside;
+        __syncthreads();
+        const uint32_t top = hi - (bin << shift);
+        const uint32_t low = top - lo < (1u << shift) ? lo : top - ((1u << shift) - 1);
+        if (inside == 1 || (!by_mass && before + inside == target)) {
+            *mass = above + in;
+            return Cut{low, 0xffffffffu};
+        }
+        if (shift == 0) {
+            // All of one key: the first so many of them.
+            const u64 w = in / inside;
+            u64 r = by_mass ? (w ? (target - above + w - 1) / w : inside) : target - before;
+            r = max((u64)1, min(r, (u64)inside));
+            *mass = above + r * w;
+            return Cut{low, r == inside ? 0xffffffffu : (uint32_t)r};
+        }
+        count0 = before;
+        mass0 = above;
+        hi = top;
+        lo = low;
+    }
+}
+
+// The cut at which the count (or, by_mass, the mass) of the prefix reaches `target` (at most the
+// total), over the elements that each(f) passes to f(logit), leaving out keys below `floor_key`.
+// *mass is the mass of the prefix, where `weigh`.  First a histogram of the distance to the maximum,
+// in kBins - 1 steps over `range` powers of two and one for the rest.
+template <int kThreads, typename Each>
+__device__ Cut find_cut(Shared<kThreads> &s, float m, float T_, float c, float range, bool by_mass,
+                        bool weigh, u64 target, uint32_t floor_key, u64 *mass, Each each) {
+    const float steps = (kBins - 1) / range;
+    auto bin_of = [&](float l) { return min(kBins - 1, (int)((m - l) * c * steps)); };
+    auto weight = [&](float l) { return weigh ? fixed_of(weight_of(l, m, T_)) : 0; };
+    for (int i = threadIdx.x; i < kBins; i += kThreads) {
+        s.count[i] = 0;
+        s.mass[i] = 0;
+    }
+    if (threadIdx.x == 0) {
+        s.low = 0xffffffffu;
+        s.high = 0;
+    }
+    __syncthreads();
+    uint32_t rest = 0;
+    u64 rest_mass = 0;
+    each([&](float l) {
+        if (logit_key(l) < floor_key) return;
+        const int bin = bin_of(l);
+        const u64 w = weight(l);
+        if (bin == kBins - 1) {
+            ++rest;
+            rest_mass += w;
+        } else {
+            atomicAdd(&s.count[bin], 1u);
+            if (weigh) atomicAdd(&s.mass[bin], w);
+        }
+    });
+    if (rest) {
+        atomicAdd(&s.count[kBins - 1], rest);
+        if (weigh) atomicAdd(&s.mass[kBins - 1], rest_mass);
+    }
+    __syncthreads();
+    find_bin<kThreads>(s, by_mass, target);
+    const int bin = s.bin;
+    const uint32_t inside = s.inside;
+    const u64 before = s.before, above = s.mass_before, in = s.mass_inside;
+    // The bin's keys.
+    uint32_t low = 0xffffffffu, high = 0;
+    each([&](float l) {
+        const uint32_t k = logit_key(l);
+        if (k < floor_key || bin_of(l) != bin) return;
+        low = min(low, k);
+        high = max(high, k);
+    });
+    if (high) {
+        atomicMin(&s.low, low);
+        atomicMax(&s.high, high);
+    }
+    __syncthreads();
+    low = s.low;
+    high = s.high;
+    __syncthreads();
+    if (inside == 1 || (!by_mass && before + inside == target)) {
+        *mass = above + in;
+        return Cut{low, 0xffffffffu};
+    }
+    return cut_by_keys<kThreads>(s, low, high, by_mass, target, before, above, mass, [&](auto f) {
+        each([&](float l) { f(logit_key(l), [&]() { return weight(l); }); });
+    });
+}
+
+// kStaged: a block's part of a row fits shared memory.
+template <typename T, int kThreads, bool kStaged>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(SampleParams p) {
+    extern __shared__ __align__(16) unsigned char staged[];
+    __shared__ Shared<kThreads> s;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = cluster.num_blocks(), rank = cluster.block_rank();
+    const int row = blockIdx.x / C, t = threadIdx.x, V = p.vocab;
     const T *logits = static_cast<const T *>(p.logits) + row * p.logits_stride;
     const float *noise = p.noise + row * p.noise_stride;
-    auto key = [&](int i) { return logit_key(to_f(logits[i])); };
-    auto sum = [](u64 a, u64 b) { return a + b; };
-    auto most = [](u64 a, u64 b) { return a > b ? a : b; };
+    if (t == 0) {
+        s.listed = 0;
+        s.total = 0;
+    }
+    ptx::griddep_wait();
 
-    u64 top = 0;
-    for (int i = t; i < V; i += kThreads) top = most(top, key(i));
-    top = block_reduce(top, red, most);
-    const float m = key_logit((uint32_t)top);
-    if (m == -__builtin_inff()) {
-        if (t == 0) p.tokens[row] = -1;
+    // 1. This block's part, and the maximum.
+    constexpr int kVec = Part<T>::kVec;
+    auto part_of = [&](int from, int to) {
+        Part<T> q;
+        q.base = min(from, V);
+        q.count = min(to, V) - q.base;
+        const T *first = logits + q.base;
+        q.skew = (int)(reinterpret_cast<uintptr_t>(first) % 16 / sizeof(T));
+        q.at = first - q.skew;
+        return q;
+    };
+    const Part<T> part = part_of(rank * p.chunk, (rank + 1) * p.chunk);
+    uint4 *const copy = reinterpret_cast<uint4 *>(staged);
+    float top_here = kNegInf;
+    const int vecs = part.vecs();
+    for (int v0 = t; v0 < vecs + t; v0 += 4 * kThreads) {
+        // Four vectors under way at a time.
+        uint4 u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[i] = part.load(min(v0 + i * kThreads, vecs - 1));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int v = v0 + i * kThreads;
+            if (kStaged && v < vecs) copy[v] = u[i];
+            top_here = fmaxf(top_here, max_of(u[i], T()));
+        }
+    }
+    // f(vector, index of its first element), and f(logit, index), of the part.
+    auto each_vector = [&](auto f) {
+#pragma unroll 2
+        for (int v = t; v < vecs; v += kThreads) f(kStaged ? copy[v] : part.load(v), part.index(v));
+    };
+    auto each_of = [&](auto vectors, auto f) {
+        vectors([&](const uint4 &u, int index) {
+            float e[kVec];
+            unpack(u, e, T());
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) f(e[i], index + i);
+        });
+    };
+    uint32_t top_key = (uint32_t)block_max<kThreads>(logit_key(top_here), s.red);
+    if (C > 1) {
+        if (t < C) cluster.map_shared_rank(&s, t)->tops[rank] = top_key;
+        cluster.sync();
+        for (int i = 0; i < C; ++i) top_key = max(top_key, s.tops[i]);
+    } else {
+        __syncthreads();
+    }
+    Shared<kThreads> *lead = C > 1 ? cluster.map_shared_rank(&s, 0) : &s;
+    // The others have told the first block all that it needs: true where this block goes on alone.
+    auto hand_over = [&]() {
+        if (C == 1) {
+            __syncthreads();
+            return true;
+        }
+        asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+        if (rank != 0) return false;
+        asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        return true;
+    };
+    const float m = key_logit(top_key);
+    const float temp = p.temperature ? p.temperature[row] : 1.0f;
+    const float min_p = p.min_p ? p.min_p[row] : 0.0f, top_p = p.top_p ? p.top_p[row] : 1.0f;
+    const int asked = p.top_k ? p.top_k[row] : 0;
+    const bool greedy = !(temp > 0.0f) || min_p > 1.0f || asked == 1 || m == kNegInf;
+    const bool by_k = asked > 0 && asked < V, by_p = top_p < 1.0f, by_min = min_p > 0.0f;
+    const float T_ = temp > 0.0f ? temp : 1.0f;
+    Best best;
+    auto race = [&](float l, int i) {
+        best.offer(weight_of(l, m, T_) / fmaxf(__ldg(noise + i), 1.17549435e-38f), i);
+    };
+    if (greedy || !(by_k || by_p || by_min)) {
+        if (greedy)
+            each_of(each_vector, [&](float l, int i) {
+                if (l == m) best.offer(0.0f, i);
+            });
+        else
+            each_of(each_vector, [&](float l, int i) {
+                if (l > kNegInf) race(l, i);
+            });
+        u64 mine = block_max<kThreads>(best.packed(), s.red);
+        if (t == 0) lead->bests[rank] = mine;
+        if (!hand_over()) return;
+        if (t == 0) {
+            for (int i = 0; i < C; ++i) mine = max(mine, s.bests[i]);
+            p.tokens[row] = m == kNegInf ? -1 : (int64_t)(uint32_t)~(uint32_t)mine;
+        }
         return;
     }
-    const float temp = p.temperature ? p.temperature[row] : 1.0f;
-    const float min_p = p.min_p ? p.min_p[row] : 0.0f;
-    const bool greedy = !(temp > 0.0f) || min_p > 1.0f;   // only the first token is kept
-    const int top_k = greedy ? 1 : p.top_k ? p.top_k[row] : 0;
-    const float T_ = temp > 0.0f ? temp : 1.0f;
-    uint32_t cut = 0;
-    u64 ties = V;
-    if (top_k > 0 && top_k < V) {
-        for (int bit = 31; bit >= 0; --bit) {
-            const uint32_t trial = cut | (1u << bit);
-            u64 c = 0;
-            for (int i = t; i < V; i += kThreads) c += key(i) >= trial;
-            if (block_reduce(c, red, sum) >= (u64)top_k) cut = trial;
-        }
-        u64 above = 0;
-        for (int i = t; i < V; i += kThreads) above += key(i) > cut;
-        ties = top_k - block_reduce(above, red, sum);
-    }
-    const float top_p = p.top_p ? p.top_p[row] : 1.0f;
-    if (!greedy && top_p < 1.0f) {
-        // Mass of the top_k tokens, and the lowest key whose predecessors hold less than
-        // top_p of it.
-        u64 mass = 0, at_cut = 0;
-        for (int i = t; i < V; i += kThreads) {
-            const uint32_t k = key(i);
-            const u64 w = fixed_of(weight_of(key_logit(k), m, T_));
-            if (k > cut) mass += w;
-            if (k == cut) at_cut += 1;
-        }
-        mass = block_reduce(mass, red, sum);
-        at_cut = block_reduce(at_cut, red, sum);
-        mass += min(at_cut, ties) * fixed_of(weight_of(key_logit(cut), m, T_));
-        const double limit = (double)top_p * (double)mass;
-        auto mass_above = [&](uint32_t x) {
-            u64 s = 0;
-            for (int i = t; i < V; i += kThreads) {
-                const uint32_t k = key(i);
-                if (k > x) s += fixed_of(weight_of(key_logit(k), m, T_));
-            }
-            return block_reduce(s, red, sum);
+
+    // 2. The mass and the list, in powers of two.  The list's edge lies a little below min_p's; with
+    // top-k and top-p it is the far one, since top-p's share is of all the top-k tokens' mass.
+    const float c = 1.44269504f / T_;
+    const float far = -log2f(min_p) * 1.00001f + 1e-4f;
+    const bool to_min = by_min && far < kListBits && !(by_k && by_p);   // nothing below the list is kept
+    const float edge = to_min ? far : kListBits;
+    const bool usable = m < __builtin_inff() && c < __builtin_inff();
+    if (usable) {
+        float mass = 0.0f;
+        auto add = [&](float l) {
+            if (by_p) mass += pow2(fmaxf((l - m) * c, -200.0f));
         };
-        uint32_t lo = 0;   // the answer's bits above `bit`; every smaller key fails
-        for (int bit = 31; bit >= 0; --bit) {
-            const uint32_t trial = lo | ((1u << bit) - 1);
-            if (!((double)mass_above(trial) < limit)) lo |= 1u << bit;
-        }
-        const uint32_t pcut = min(lo, (uint32_t)top);
-        if (pcut >= cut) {
-            const double room = limit - (double)mass_above(pcut);
-            const u64 w = fixed_of(weight_of(key_logit(pcut), m, T_));
-            // Ties kept: those with fewer than room / w before them.
-            u64 r = w ? (u64)fmin(ceil(room / (double)w), 1e9) : (u64)V;
-            if (pcut == (uint32_t)top && r < 1) r = 1;
-            ties = pcut == cut ? min(ties, r) : r;
-            cut = pcut;
+        auto list = [&](float l, int i) {
+            if ((l - m) * c >= -edge) {
+                const cg::coalesced_group g = cg::coalesced_threads();
+                int at = 0;
+                if (g.thread_rank() == 0) at = atomicAdd(&lead->listed, (int)g.size());
+                at = g.shfl(at, 0) + g.thread_rank();
+                if (at < kListMax) {
+                    lead->list_key[at] = logit_key(l);
+                    lead->list_index[at] = i;
+                }
+            }
+        };
+        each_vector([&](const uint4 &u, int index) {
+            float e[kVec];
+            unpack(u, e, T());
+            if (by_p) {
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) add(e[i]);
+            }
+            if ((max_of(u, T()) - m) * c >= -edge) {
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) list(e[i], index + i);
+            }
+        });
+        if (by_p) {
+            const u64 total = block_sum<kThreads>(fixed_of(mass), s.red);
+            if (t == 0) atomicAdd(&lead->total, total);
         }
     }
-    // The race: best score, then lowest index, packed so that the larger wins.
-    u64 best = 0, tied = 0;
-    for (int base = 0; base < V; base += kThreads) {
-        const int i = base + t;
-        const uint32_t k = i < V ? key(i) : 0;
-        const bool eq = i < V && k == cut;
-        const unsigned ballot = __ballot_sync(0xffffffffu, eq);
-        __syncthreads();
-        if (t % 32 == 0) red[t / 32] = __popc(ballot);
-        __syncthreads();
-        u64 r = tied + __popc(ballot & ((1u << (t % 32)) - 1));
-        for (int j = 0; j < kThreads / 32; ++j) {
-            if (j < t / 32) r += red[j];
-            tied += red[j];
+    if (!hand_over()) return;
+
+    // 3. The cuts.  `each` passes the logits of the list, or of the row, and with_index the indices
+    // too.
+    const int n = s.listed;
+    auto finish = [&](auto with_index, float range, u64 mass, u64 have) {
+        auto each = [&](auto f) { with_index([&](float l, int) { f(l); }); };
+        Cut cut = {0, 0xffffffffu};
+        if (by_k && have > (u64)asked)
+            cut = find_cut<kThreads>(s, m, T_, c, range, false, by_p, asked, 0, &mass, each);
+        if (by_p) {
+            u64 all = mass;
+            if (!by_k || have <= (u64)asked) {
+                all = 0;
+                each([&](float l) { all += fixed_of(weight_of(l, m, T_)); });
+                all = block_sum<kThreads>(all, s.red);
+                if (by_k || mass == 0) mass = all;
+            }
+            const u64 target = max((u64)1, (u64)fmax(ceil((double)top_p * (double)mass), 0.0));
+            if (target <= all) {
+                u64 unused;
+                const Cut at = find_cut<kThreads>(s, m, T_, c, range, true, true, target, cut.low, &unused, each);
+                cut = at.low == cut.low ? Cut{cut.low, min(cut.ties, at.ties)} : at;
+            } else if (!to_min) {
+                return false;
+            }
         }
-        if (i >= V || !(k > cut || (eq && r < ties))) continue;
-        const float l = key_logit(k);
-        if (l == -__builtin_inff()) continue;
-        const float w = weight_of(l, m, T_);
-        if (w < min_p && !greedy) continue;
-        const float score = w / fmaxf(noise[i], 1.17549435e-38f);
-        best = most(best, ((u64)__float_as_uint(score) << 32 | (uint32_t)~i));
-    }
-    best = block_reduce(best, red, most);
-    if (t == 0) p.tokens[row] = (uint32_t)~(uint32_t)best;
+        // Of the ties at the cut the lowest indices: the highest complements.
+        uint32_t low_index = 0;
+        if (cut.ties != 0xffffffffu) {
+            u64 unused;
+            low_index = cut_by_keys<kThreads>(s, ~(uint32_t)(V - 1), 0xffffffffu, false, cut.ties, 0, 0, &unused,
+                                              [&](auto f) {
+                with_index([&](float l, int i) {
+                    if (logit_key(l) == cut.low) f(~(uint32_t)i, []() { return (u64)0; });
+                });
+            }).low;
+        }
+        // 4. The race.
+        with_index([&](float l, int i) {
+            const uint32_t k = logit_key(l);
+            if (k < cut.low || (k == cut.low && ~(uint32_t)i < low_index) || l == kNegInf) return;
+            if (weight_of(l, m, T_) >= min_p) race(l, i);
+        });
+        const u64 won = block_max<kThreads>(best.packed(), s.red);
+        if (t == 0) p.tokens[row] = (int64_t)(uint32_t)~(uint32_t)won;
+        return true;
+    };
+    // The list holds the cuts if top-k's is inside; top-p's is looked for.
+    if (usable && n <= kListMax && (by_k ? n >= asked || (to_min && !by_p) : by_p || to_min) &&
+        finish([&](auto f) {
+            for (int i = t; i < n; i += kThreads) f(key_logit(s.list_key[i]), (int)s.list_index[i]);
+        }, edge * 1.001f, s.total, n))
+        return;
+    __syncthreads();
+    const Part<T> whole = part_of(0, V);
+    auto whole_vectors = [&](auto f) {
+#pragma unroll 1
+        for (int v = t; v < whole.vecs(); v += kThreads) f(whole.load(v), whole.index(v));
+    };
+    // A histogram over 30 powers of two; temperatures that overflow the scale take key histograms.
+    finish([&](auto f) {
+        each_of(whole_vectors, [&](float l, int i) { f(fmaxf(l, kNegInf), i); });
+    }, 30.0f, 0, V);
+}
+
+template <typename T, int kThreads, bool kStaged>
+cudaError_t launch(const SampleParams &p, int rows, int cluster, cudaStream_t st) {
+    const auto kernel = sample_kernel<T, kThreads, kStaged>;
+    const size_t smem = kStaged ? (size_t)p.chunk * sizeof(T) + 32 : 0;
+    static PerDeviceOnce once;
+    const cudaError_t e = once.run(current_device(), cudaSuccess, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageBytes + 32);
+    });
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(rows * cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    count_launches(1);
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <typename T>
+cudaError_t launch(const ctr_sampler_s *pl, SampleParams p, cudaStream_t st) {
+    // Blocks a row: enough that a part fits shared memory, and that few rows fill the GPU, but
+    // at least 4096 elements each.
+    int cluster = 1;
+    const int rows = (int)pl->rows;
+    while (cluster < kMaxCluster &&
+           ((int64_t)p.vocab * (int64_t)sizeof(T) > (int64_t)cluster * kStageBytes ||
+            (rows * cluster * 2 <= pl->num_sms && p.vocab >= 4096 * 2 * cluster)))
+        cluster *= 2;
+    p.chunk = ((p.vocab + cluster - 1) / cluster + 15) / 16 * 16;
+    if (p.chunk <= 4096) return launch<T, 256, true>(p, rows, cluster, st);
+    return (size_t)p.chunk * sizeof(T) <= kStageBytes ? launch<T, 512, true>(p, rows, cluster, st)
+                                                      : launch<T, 512, false>(p, rows, cluster, st);
 }
 
 }  // namespace
@@ -175,6 +642,7 @@ ctr_status ctr_sampler_create(ctr_sampler_t *out, int64_t rows, int64_t vocab, i
     pl->rows = rows;
     pl->vocab = vocab;
     pl->dtype = dtype;
+    pl->num_sms = ctr::device_sms();
     *out = pl;
     return CTR_OK;
 }
@@ -192,18 +660,22 @@ ctr_status ctr_sampler_forward(ctr_sampler_t pl, const void *logits, int64_t log
     if (off(logits, pl->dtype == CTR_F32 ? 4 : 2) || off(noise, 4) || off(temperature, 4) ||
         off(top_k, 4) || off(top_p, 4) || off(min_p, 4) || off(tokens, 8))
         return CTR_ERR_MISALIGNED;
-    ctr::SampleParams p = {logits, noise, logits_stride, noise_stride, temperature, top_p, min_p,
-                           top_k, tokens, (int)pl->vocab};
+    ctr::SampleParams p = {};
+    p.logits = logits;
+    p.noise = noise;
+    p.logits_stride = logits_stride;
+    p.noise_stride = noise_stride;
+    p.temperature = temperature;
+    p.top_k = top_k;
+    p.top_p = top_p;
+    p.min_p = min_p;
+    p.tokens = tokens;
+    p.vocab = (int)pl->vocab;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const unsigned rows = (unsigned)pl->rows;
-    if (pl->dtype == CTR_F32)
-        ctr::sample_kernel<float><<<rows, ctr::kThreads, 0, st>>>(p);
-    else if (pl->dtype == CTR_BF16)
-        ctr::sample_kernel<__nv_bfloat16><<<rows, ctr::kThreads, 0, st>>>(p);
-    else
-        ctr::sample_kernel<__half><<<rows, ctr::kThreads, 0, st>>>(p);
-    ctr::count_launches(1);
-    return cudaGetLastError() == cudaSuccess ? CTR_OK : CTR_ERR_CUDA;
+    const cudaError_t e = pl->dtype == CTR_F32    ? ctr::launch<float>(pl, p, st)
+                          : pl->dtype == CTR_BF16 ? ctr::launch<__nv_bfloat16>(pl, p, st)
+                                                  : ctr::launch<__half>(pl, p, st);
+    return e == cudaSuccess ? CTR_OK : CTR_ERR_CUDA;
 }
 
 ctr_status ctr_sampler_describe(ctr_sampler_t pl, char *buf, size_t len) {
