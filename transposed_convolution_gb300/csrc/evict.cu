@@ -1,12 +1,24 @@
 // evict.cu -- eviction from the paged cache by accumulated attention weight.
+//
+// Two kernels.  The first reads each (sequence, KV head)'s weights once, as order-preserving keys
+// in shared memory where they fit, finds the lowest key that stays by three histograms (11, 11
+// and 10 bits), and lists the kept slots in order: counts by warp, their sum, and the list, which
+// takes a ballot for each 32 slots.  The second copies the listed rows; it moves
+// 4 D elements a row and is bound by the cache's memory, so its blocks are many and small, each
+// with the row addresses of 64 rows in shared memory and two 16-byte loads of K and V under way
+// for each thread at a time.  It is launched while the first still runs, and waits for its end.
 #include <algorithm>
 
 #include "decode_device.cuh"
+#include "ptx.cuh"
 
 namespace ctr {
 namespace {
 
-constexpr int kSelectThreads = 512;
+constexpr int kSelectThreads = 1024, kSelectWarps = kSelectThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kStageKeys = 40 * 1024;      // most keys kept in shared memory (160 KB)
+constexpr int kCopyThreads = 256, kCopyRows = 64;
 
 // Order-preserving key: larger weight, larger key; NaN lowest, -0 as +0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -15,105 +27,211 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__device__ int block_sum(int v, int *red) {
-    v = __reduce_add_sync(0xffffffffu, v);
+// Exclusive prefix sums of two counts by warp, and their totals.  Not inlined, so that lanes meet
+// at one copy of its shuffles.
+__device__ __noinline__ void scan_warps(int (&a)[kSelectWarps], int (&b)[kSelectWarps]) {
     __syncthreads();
-    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        const int x = a[lane], y = b[lane];
+        int xi = x, yi = y;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int u = __shfl_up_sync(0xffffffffu, xi, o), v = __shfl_up_sync(0xffffffffu, yi, o);
+            if (lane >= o) {
+                xi += u;
+                yi += v;
+            }
+        }
+        a[lane] = xi - x;
+        b[lane] = yi - y;
+    }
     __syncthreads();
-    v = 0;
-    for (int i = 0; i < kSelectThreads / 32; ++i) v += red[i];
-    return v;
 }
 
-// One block per (sequence, KV head): the smallest key that stays, found bit by bit, then the
-// kept slots in order by a scan over the slots.
-__global__ void select_kernel(EvictParams p) {
-    __shared__ int red[kSelectThreads / 32];
-    const int unit = blockIdx.x, b = unit / p.Hkv, t = threadIdx.x;
+struct Boundary {
+    int bin, before, inside;
+};
+
+// The bin of the histogram, from the top one down, in which the count reaches `target`.
+__device__ __noinline__ void find_bin(const int (&hist)[kBins], int target, int (&warp_a)[kSelectWarps],
+                                      Boundary *found) {
+    constexpr int kEach = kBins / kSelectThreads;
+    const int t = threadIdx.x, lane = t % 32, warp = t / 32;
+    int c[kEach], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        c[i] = hist[kBins - 1 - (t * kEach + i)];
+        sum += c[i];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+    }
+    if (lane == 31) warp_a[warp] = incl;
+    __syncthreads();
+    int before = incl - sum;
+    for (int i = 0; i < warp; ++i) before += warp_a[i];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        if (before < target && target <= before + c[i])
+            *found = Boundary{kBins - 1 - (t * kEach + i), before, c[i]};
+        before += c[i];
+    }
+    __syncthreads();
+}
+
+// One block for each (sequence, KV head).
+template <bool kStaged>
+__global__ void __launch_bounds__(kSelectThreads) select_kernel(EvictParams p) {
+    extern __shared__ __align__(16) unsigned char staged[];
+    __shared__ int hist[kBins], warp_a[kSelectWarps], warp_b[kSelectWarps];
+    __shared__ Boundary found;
+    uint32_t *const keys = reinterpret_cast<uint32_t *>(staged);
+    const int unit = blockIdx.x, b = unit / p.Hkv, t = threadIdx.x, lane = t % 32, warp = t / 32;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     const int len = p.cache.lens[b];
-    int n = len < 0 ? 0 : len;
+    int n = max(len, 0);
     if (n > p.cache.cap) {
         n = p.cache.cap;
         if (t == 0) atomicOr(p.cache.status, kStatusBadLength);
     }
     const int keep = min(n, p.budget);
-    const float *w = p.w + (int64_t)unit * p.cache.cap;
+    const float *const w = p.w + (int64_t)unit * p.cache.cap;
     const int s0 = min(p.sinks, n), r0 = max(s0, n - p.recent);   // the others: s0 <= j < r0
     const int want = keep - s0 - (n - r0);                        // of the others
-    uint32_t cut = 0;      // the want-th largest key
-    int ties = 0;          // how many of the slots with key == cut stay
-    if (want > 0 && want < r0 - s0) {
-        for (int bit = 31; bit >= 0; --bit) {
-            const uint32_t trial = cut | (1u << bit);
-            int c = 0;
-            for (int j = s0 + t; j < r0; j += kSelectThreads) c += weight_key(w[j]) >= trial;
-            if (block_sum(c, red) >= want) cut = trial;
-        }
-        int above = 0;
-        for (int j = s0 + t; j < r0; j += kSelectThreads) above += weight_key(w[j]) > cut;
-        ties = want - block_sum(above, red);
-    }
     const bool all = want >= r0 - s0;
-    int32_t *slots = p.slots + (int64_t)unit * p.budget;
-    int done = 0, tied = 0;      // kept slots and ties before this round
-    for (int base = 0; base < n; base += kSelectThreads) {
-        const int j = base + t;
-        bool eq = false, on = false;
-        if (j < n) {
-            on = j < s0 || j >= r0 || all;
-            if (!on && want > 0) {
-                const uint32_t k = weight_key(w[j]);
-                on = k > cut;
-                eq = k == cut;
+    auto key_at = [&](int j) { return kStaged ? keys[j] : weight_key(w[j]); };
+
+    // The lowest key that stays, by histograms of its bits from the top.
+    uint32_t cut = 0;
+    int ties = 0;          // how many of the others with key == cut stay
+    if (want > 0 && !all) {
+        int target = want, above = 32;      // bits of the keys not yet decided
+        for (int round = 0; round < 3; ++round) {
+            const int bits = round < 2 ? 11 : 10, shift = above - bits;
+            for (int i = t; i < kBins; i += kSelectThreads) hist[i] = 0;
+            __syncthreads();
+#pragma unroll 4
+            for (int j = s0 + t; j < r0; j += kSelectThreads) {
+                uint32_t k;
+                if (round == 0) {
+                    k = weight_key(w[j]);
+                    if (kStaged) keys[j] = k;
+                } else {
+                    k = key_at(j);
+                }
+                if (round == 0 || k >> above == cut >> above)
+                    atomicAdd(&hist[k >> shift & ((1u << bits) - 1)], 1);
             }
+            __syncthreads();
+            find_bin(hist, target, warp_a, &found);
+            cut |= (uint32_t)found.bin << shift;
+            target -= found.before;
+            above = shift;
+            // The whole bin stays: nothing below is to be decided.
+            if (found.inside == target) {
+                target = 0x7fffffff;
+                break;
+            }
+            __syncthreads();
         }
-        // Ranks inside the round: ties first, then the kept.
-        const unsigned be = __ballot_sync(0xffffffffu, eq), before = (1u << (t % 32)) - 1;
-        __syncthreads();
-        if (t % 32 == 0) red[t / 32] = __popc(be);
-        __syncthreads();
-        int r = tied + __popc(be & before);
-        for (int i = 0; i < t / 32; ++i) r += red[i];
-        for (int i = 0; i < kSelectThreads / 32; ++i) tied += red[i];
-        if (eq && r < ties) on = true;
+        ties = target;
+    }
+    const bool whole_bin = ties == 0x7fffffff;     // every key >= cut stays
+    __syncthreads();
+
+    // The list: each warp takes a run of the slots.
+    const int run = ((n + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
+    const int from = min(warp * run, n), to = min(from + run, n);
+    auto judge = [&](int j, bool *on, bool *eq) {
+        *on = *eq = false;
+        if (j >= to) return;
+        *on = j < s0 || j >= r0 || all;
+        if (!*on && want > 0) {
+            const uint32_t k = key_at(j);
+            *on = whole_bin ? k >= cut : k > cut;
+            *eq = !whole_bin && k == cut;
+        }
+    };
+    int sure = 0, equal = 0;
+    for (int base = from; base < to; base += 32) {
+        bool on, eq;
+        judge(base + lane, &on, &eq);
+        sure += __popc(__ballot_sync(0xffffffffu, on));
+        equal += __popc(__ballot_sync(0xffffffffu, eq));
+    }
+    if (lane == 0) {
+        warp_a[warp] = sure;
+        warp_b[warp] = equal;
+    }
+    scan_warps(warp_a, warp_b);
+    int tie = warp_b[warp], at = warp_a[warp] + min(tie, ties);
+    int32_t *const slots = p.slots + (int64_t)unit * p.budget;
+    const unsigned below = (1u << lane) - 1;
+    for (int base = from; base < to; base += 32) {
+        bool on, eq;
+        judge(base + lane, &on, &eq);
+        const unsigned be = __ballot_sync(0xffffffffu, eq);
+        if (eq && tie + __popc(be & below) < ties) on = true;
+        tie += __popc(be);
         const unsigned bo = __ballot_sync(0xffffffffu, on);
-        __syncthreads();
-        if (t % 32 == 0) red[t / 32] = __popc(bo);
-        __syncthreads();
-        r = done + __popc(bo & before);
-        for (int i = 0; i < t / 32; ++i) r += red[i];
-        for (int i = 0; i < kSelectThreads / 32; ++i) done += red[i];
-        if (on) slots[r] = j;
+        if (on) slots[at + __popc(bo & below)] = base + lane;
+        at += __popc(bo);
     }
     for (int i = keep + t; i < p.budget; i += kSelectThreads) slots[i] = -1;
     if (unit % p.Hkv == 0 && t == 0) p.lens_out[b] = len < 0 ? len : keep;
 }
 
-// One warp per kept row: K, V and the weight to the destination slot.
-__global__ void copy_kernel(EvictParams p, int chunks) {
-    const int unit = blockIdx.x / chunks, b = unit / p.Hkv, h = unit % p.Hkv;
-    const int warps = blockDim.x / 32;
-    for (int i = blockIdx.x % chunks * warps + threadIdx.x / 32; i < p.budget; i += chunks * warps) {
-        const int j = p.slots[(int64_t)unit * p.budget + i];
-        if (j < 0) break;
-        const int64_t src = slot_offset(p.cache, b, h, j);
-        const int pg = p.dst_tables[b * p.dst_pitch + i / p.cache.page];
-        if ((unsigned)pg >= (unsigned)p.cache.num_pages) {
-            atomicOr(p.cache.status, kStatusBadPage);
-            continue;
-        }
-        const int64_t dst = pg * p.cache.page_stride + h * p.cache.head_stride +
-                            (i % p.cache.page) * p.cache.row_stride;
-        if (src >= 0) {
-            for (int c = threadIdx.x % 32; c < p.row_bytes / 16; c += 32) {
-                const uint4 k = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.k) + src * p.esize)[c];
-                const uint4 v = reinterpret_cast<const uint4 *>(static_cast<const char *>(p.v) + src * p.esize)[c];
-                reinterpret_cast<uint4 *>(static_cast<char *>(p.k) + dst * p.esize)[c] = k;
-                reinterpret_cast<uint4 *>(static_cast<char *>(p.v) + dst * p.esize)[c] = v;
+// kCopyRows kept rows of one (sequence, KV head) a block: K, V and weights.
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(EvictParams p, int blocks_a_unit) {
+    __shared__ int64_t from[kCopyRows], to[kCopyRows];     // 16-byte chunks; -1: not to be copied
+    const int unit = blockIdx.x / blocks_a_unit, b = unit / p.Hkv, h = unit % p.Hkv;
+    const int i0 = blockIdx.x % blocks_a_unit * kCopyRows, t = threadIdx.x;
+    ptx::griddep_wait();
+    if (t < kCopyRows) {
+        const int i = i0 + t, j = i < p.budget ? p.slots[(int64_t)unit * p.budget + i] : -1;
+        int64_t src = -1, dst = -1;
+        if (j >= 0) {
+            src = slot_offset(p.cache, b, h, j);
+            const int pg = p.dst_tables[b * p.dst_pitch + i / p.cache.page];
+            if ((unsigned)pg >= (unsigned)p.cache.num_pages) {
+                atomicOr(p.cache.status, kStatusBadPage);
+                src = -1;
+            } else {
+                dst = pg * p.cache.page_stride + h * p.cache.head_stride +
+                      (i % p.cache.page) * p.cache.row_stride;
             }
+            if (p.w_out) p.w_out[unit * p.w_pitch + i] = p.w[(int64_t)unit * p.cache.cap + j];
         }
-        if (p.w_out && threadIdx.x % 32 == 0)
-            p.w_out[unit * p.w_pitch + i] = p.w[(int64_t)unit * p.cache.cap + j];
+        from[t] = src < 0 ? -1 : src * p.esize / 16;
+        to[t] = dst * p.esize / 16;
+    }
+    __syncthreads();
+    const int chunks = p.row_bytes / 16, total = kCopyRows * chunks;
+    const uint4 *const k = static_cast<const uint4 *>(p.k), *const v = static_cast<const uint4 *>(p.v);
+    uint4 *const ko = static_cast<uint4 *>(p.k), *const vo = static_cast<uint4 *>(p.v);
+    for (int x0 = t; x0 < total; x0 += 2 * kCopyThreads) {
+        uint4 a[2], c[2];
+        int64_t at[2];
+        // Past the end the last chunk is read again, for nothing, as are chunks of no row.
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int x = min(x0 + u * kCopyThreads, total - 1), r = x / chunks, e = x - r * chunks;
+            const int64_t f = from[r] < 0 ? 0 : from[r];
+            at[u] = from[r] < 0 || x0 + u * kCopyThreads >= total ? -1 : to[r] + e;
+            a[u] = k[f + e];
+            c[u] = v[f + e];
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            if (at[u] >= 0) {
+                ko[at[u]] = a[u];
+                vo[at[u]] = c[u];
+            }
     }
 }
 
@@ -121,11 +239,23 @@ __global__ void copy_kernel(EvictParams p, int chunks) {
 
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t st) {
     const int units = p.B * p.Hkv;
-    select_kernel<<<units, kSelectThreads, 0, st>>>(p);
-    const int chunks = std::min((p.budget + 31) / 32, 1024);
-    copy_kernel<<<(unsigned)units * chunks, 256, 0, st>>>(p, chunks);
+    cudaError_t e;
+    if (p.cache.cap <= kStageKeys) {
+        static PerDeviceOnce once;
+        e = once.run(current_device(), cudaSuccess, [] {
+            return cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        kStageKeys * (int)sizeof(uint32_t));
+        });
+        if (e != cudaSuccess) return e;
+        e = launch_pdl(select_kernel<true>, dim3((unsigned)units), dim3(kSelectThreads),
+                       (size_t)p.cache.cap * sizeof(uint32_t), st, p);
+    } else {
+        e = launch_pdl(select_kernel<false>, dim3((unsigned)units), dim3(kSelectThreads), 0, st, p);
+    }
+    if (e != cudaSuccess) return e;
+    const int blocks = (int)((std::min<int64_t>(p.budget, p.cache.cap) + kCopyRows - 1) / kCopyRows);
     count_launches(2);
-    return cudaGetLastError();
+    return launch_pdl(copy_kernel, dim3((unsigned)units * blocks), dim3(kCopyThreads), 0, st, p, blocks);
 }
 
 }  // namespace ctr

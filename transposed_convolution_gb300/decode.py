@@ -21,6 +21,13 @@ def _device_of(device):
     return torch.device("cuda", torch.cuda.current_device() if d.index is None else d.index)
 
 
+def _numel(shape):
+    n = 1
+    for v in shape[1:]:
+        n *= v
+    return n
+
+
 class _DecodePlan:
     """A plan handle on one device, and the checks both plans make of their arguments."""
 
@@ -29,25 +36,46 @@ class _DecodePlan:
 
     def _stream(self, stream, *made):
         """The raw stream of a call; tensors that the call made are kept for it."""
-        if stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
-        if stream != torch.cuda.current_stream(self.device):
-            for t in made:
-                t.record_stream(stream)
+        current = torch._C._cuda_getCurrentRawStream(self._index)
+        if stream is None or stream.cuda_stream == current:
+            return current
+        for t in made:
+            t.record_stream(stream)
         return stream.cuda_stream
 
-    def _checked(self, t, name, shape, dtype, rows=False):
-        """t's address, after its shape, type, device and layout have been checked.  With
-        ``rows`` the first dimension may have any stride; otherwise t is contiguous."""
+    def _at(self, t, name, shape, dtype):
+        """The address of a contiguous tensor, after its shape, type, device and layout have been
+        checked: one expression, because small calls take as long as their checks."""
+        if (t.shape != shape or t.dtype is not dtype or t.get_device() != self._index
+                or not t.is_contiguous()):
+            self._refuse(t, name, shape, dtype)
+            raise ValueError("%s must be contiguous" % name)
+        return t.data_ptr()
+
+    def _rows_at(self, t, name, shape, dtype):
+        """The address and the row stride of a tensor whose rows (of all but the first dimension)
+        are contiguous and lie at any distance."""
+        if t.is_contiguous():
+            return self._at(t, name, shape, dtype), t.stride(0) if shape[0] > 1 else _numel(shape)
+        self._refuse(t, name, shape, dtype)
+        stride = t.stride()
+        if len(shape) == 3 and shape[1] == 1:
+            inner = stride[2] == 1
+        else:
+            inner = stride[1:] == ((1,) if len(shape) == 2 else (shape[2], 1))
+        if not inner and not (shape[0] and t[0].is_contiguous()):
+            raise ValueError("%s must be contiguous within a row" % name)
+        # The stride of a single row is arbitrary.
+        return t.data_ptr(), stride[0] if shape[0] > 1 else _numel(shape)
+
+    def _refuse(self, t, name, shape, dtype):
+        """Raises for a wrong shape, type or device."""
         if t.shape != shape:
             raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-        if t.device != self.device:
+        if t.get_device() != self._index:
             raise ValueError("%s is on %s, the plan on %s" % (name, t.device, self.device))
-        if not (t.is_contiguous() or (rows and t.shape[0] and t[0].is_contiguous())):
-            raise ValueError("%s must be contiguous%s" % (name, " within a row" if rows else ""))
-        return t.data_ptr()
 
     def close(self):
         if self.handle:
@@ -85,6 +113,7 @@ class PagedAttention(_DecodePlan):
             dtype = k_pages.dtype if dtype is None else dtype
             num_pages = k_pages.shape[0] if num_pages is None else num_pages
         self.device = _device_of(device)
+        self._index = self.device.index
         self.dtype = dtype if dtype is not None else torch.float32
         self.B, self.H_q, self.H_kv, self.D = int(B), int(H_q), int(H_kv), int(D)
         self.page_size, self.max_pages = int(page_size), int(max_pages)
@@ -106,14 +135,19 @@ class PagedAttention(_DecodePlan):
             if k_pages is None:
                 k_pages = torch.zeros(shape, dtype=self.dtype, device=self.device)
                 v_pages = torch.zeros(shape, dtype=self.dtype, device=self.device)
-            k = self._checked(k_pages, "k_pages", shape, self.dtype)
-            v = self._checked(v_pages, "v_pages", shape, self.dtype)
+            k = self._at(k_pages, "k_pages", shape, self.dtype)
+            v = self._at(v_pages, "v_pages", shape, self.dtype)
             self.k_pages, self.v_pages = k_pages, v_pages
             _ctr.ctr_attn_bind_cache(self.handle, k, v, self.num_pages)
             self.workspace_bytes = _ctr.ctr_attn_workspace_bytes(self.handle)
             self.workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=self.device)
             _ctr.ctr_attn_bind_workspace(self.handle, self.workspace.data_ptr(),
                                          self.workspace_bytes)
+            self._q_shape, self._kv_shape = (self.B, self.H_q, self.D), (self.B, self.H_kv, self.D)
+            self._table_shape, self._lens_shape = (self.B, self.max_pages), (self.B,)
+            self._weights_shape = (self.B, self.H_kv, self.capacity)
+            self._forward = _ctr.load_library().ctr_attn_forward
+            self._evict = _ctr.load_library().ctr_attn_evict
             with torch.cuda.device(self.device):
                 _ctr.ctr_attn_reset(self.handle, self._stream(None))
                 # The plan may be used on any stream from here on.
@@ -124,9 +158,6 @@ class PagedAttention(_DecodePlan):
 
     _destroy = staticmethod(lambda handle: _ctr.ctr_attn_destroy(handle))
 
-    def _weights(self, t, name):
-        return self._checked(t, name, (self.B, self.H_kv, self.capacity), torch.float32)
-
     def forward(self, q, tables, lens, k_new=None, v_new=None, weights=None, weights_out=None,
                 out=None, stream=None):
         """out [B, H_q, D] of q [B, H_q, D] over each sequence's cached tokens; with k_new and
@@ -135,43 +166,39 @@ class PagedAttention(_DecodePlan):
         and lens [B] are int32; lens[b] < 0 marks an idle row.  A plan with weights adds this
         step's to ``weights`` [B, H_kv, max_pages * page_size] (None: zeros) and writes the sums
         to ``weights_out`` (default: ``weights`` itself)."""
-        if (k_new is None) != (v_new is None):
-            raise ValueError("k_new and v_new belong together")
-        q_ptr = self._checked(q, "q", (self.B, self.H_q, self.D), self.dtype, rows=True)
-        k_ptr = v_ptr = None
+        q_ptr, q_stride = self._rows_at(q, "q", self._q_shape, self.dtype)
+        k_ptr = v_ptr = wi_ptr = wo_ptr = None
         kv_stride = 0
-        if k_new is not None:
-            shape = (self.B, self.H_kv, self.D)
-            k_ptr = self._checked(k_new, "k_new", shape, self.dtype, rows=True)
-            v_ptr = self._checked(v_new, "v_new", shape, self.dtype, rows=True)
-            kv_stride = self._row_stride(k_new)
-            if self._row_stride(v_new) != kv_stride:
+        if k_new is not None and v_new is not None:
+            k_ptr, kv_stride = self._rows_at(k_new, "k_new", self._kv_shape, self.dtype)
+            v_ptr, v_stride = self._rows_at(v_new, "v_new", self._kv_shape, self.dtype)
+            if v_stride != kv_stride:
                 raise ValueError("k_new and v_new must have the same row stride")
-        t_ptr = self._checked(tables, "tables", (self.B, self.max_pages), torch.int32)
-        l_ptr = self._checked(lens, "lens", (self.B,), torch.int32)
-        wi_ptr = wo_ptr = None
+        elif k_new is not None or v_new is not None:
+            raise ValueError("k_new and v_new belong together")
+        t_ptr = self._at(tables, "tables", self._table_shape, torch.int32)
+        l_ptr = self._at(lens, "lens", self._lens_shape, torch.int32)
         if self.weights:
             if weights_out is None:
                 weights_out = weights
             if weights_out is None:
                 raise ValueError("a plan with weights needs weights or weights_out")
-            wi_ptr = None if weights is None else self._weights(weights, "weights")
-            wo_ptr = self._weights(weights_out, "weights_out")
+            if weights is not None:
+                wi_ptr = self._at(weights, "weights", self._weights_shape, torch.float32)
+            wo_ptr = self._at(weights_out, "weights_out", self._weights_shape, torch.float32)
         elif weights is not None or weights_out is not None:
             raise ValueError("the plan was made without weights")
-        made = ()
         if out is None:
-            out = torch.empty((self.B, self.H_q, self.D), dtype=self.dtype, device=self.device)
-            made = (out,)
-        o_ptr = self._checked(out, "out", (self.B, self.H_q, self.D), self.dtype)
-        _ctr.ctr_attn_forward(self.handle, q_ptr, self._row_stride(q), k_ptr, v_ptr, kv_stride, t_ptr,
-                              l_ptr, wi_ptr, wo_ptr, o_ptr, self._stream(stream, *made))
+            out = torch.empty(self._q_shape, dtype=self.dtype, device=self.device)
+            raw = self._stream(stream, out)
+        else:
+            raw = self._stream(stream)
+        o_ptr = self._at(out, "out", self._q_shape, self.dtype)
+        st = self._forward(self.handle, q_ptr, q_stride, k_ptr, v_ptr, kv_stride, t_ptr, l_ptr, wi_ptr,
+                           wo_ptr, o_ptr, raw)
+        if st:
+            raise _ctr.CtrError(st, "ctr_attn_forward")
         return out
-
-    @staticmethod
-    def _row_stride(t):
-        # The stride of a single row is arbitrary: any valid one will do.
-        return t.stride(0) if t.shape[0] > 1 else t[0].numel()
 
     def evict(self, tables, lens, weights, dst_tables, budget, sinks=0, recent=0, slots=None,
               lens_out=None, weights_out=None, stream=None):
@@ -183,10 +210,10 @@ class PagedAttention(_DecodePlan):
         budget = int(budget)
         if dst_tables.dim() != 2 or dst_tables.shape[0] != self.B:
             raise ValueError("dst_tables must be [%d, pages]" % self.B)
-        t_ptr = self._checked(tables, "tables", (self.B, self.max_pages), torch.int32)
-        l_ptr = self._checked(lens, "lens", (self.B,), torch.int32)
-        w_ptr = self._weights(weights, "weights")
-        d_ptr = self._checked(dst_tables, "dst_tables", tuple(dst_tables.shape), torch.int32)
+        t_ptr = self._at(tables, "tables", self._table_shape, torch.int32)
+        l_ptr = self._at(lens, "lens", self._lens_shape, torch.int32)
+        w_ptr = self._at(weights, "weights", self._weights_shape, torch.float32)
+        d_ptr = self._at(dst_tables, "dst_tables", dst_tables.shape, torch.int32)
         made = []
         if slots is None:
             slots = torch.empty((self.B, self.H_kv, max(budget, 0)), dtype=torch.int32,
@@ -202,12 +229,14 @@ class PagedAttention(_DecodePlan):
         if weights_out.dim() != 3:
             raise ValueError("weights_out must be [%d, %d, >= %d]" % (self.B, self.H_kv, budget))
         pitch = weights_out.shape[2]
-        s_ptr = self._checked(slots, "slots", (self.B, self.H_kv, budget), torch.int32)
-        lo_ptr = self._checked(lens_out, "lens_out", (self.B,), torch.int32)
-        wo_ptr = self._checked(weights_out, "weights_out", (self.B, self.H_kv, pitch), torch.float32)
-        _ctr.ctr_attn_evict(self.handle, t_ptr, l_ptr, w_ptr, d_ptr, dst_tables.shape[1], budget,
-                            int(sinks), int(recent), s_ptr, lo_ptr, wo_ptr, pitch,
-                            self._stream(stream, *made))
+        s_ptr = self._at(slots, "slots", (self.B, self.H_kv, budget), torch.int32)
+        lo_ptr = self._at(lens_out, "lens_out", (self.B,), torch.int32)
+        wo_ptr = self._at(weights_out, "weights_out", (self.B, self.H_kv, pitch), torch.float32)
+        st = self._evict(self.handle, t_ptr, l_ptr, w_ptr, d_ptr, dst_tables.shape[1], budget,
+                         int(sinks), int(recent), s_ptr, lo_ptr, wo_ptr, pitch,
+                         self._stream(stream, *made))
+        if st:
+            raise _ctr.CtrError(st, "ctr_attn_evict")
         return slots, lens_out, weights_out
 
     def check(self, stream=None):
@@ -225,35 +254,37 @@ class Sampler(_DecodePlan):
 
     def __init__(self, rows, vocab, dtype=None, device=None):
         self.device = _device_of(device)
+        self._index = self.device.index
         self.dtype = dtype if dtype is not None else torch.float32
         self.rows, self.vocab = int(rows), int(vocab)
+        self._shape, self._row_shape = (self.rows, self.vocab), (self.rows,)
+        self._forward = _ctr.load_library().ctr_sampler_forward
         self.handle = _ctr.ctr_sampler_create(rows, vocab, _ctr._dtype_code(self.dtype))
 
     _destroy = staticmethod(lambda handle: _ctr.ctr_sampler_destroy(handle))
-
-    def _per_row(self, t, name, dtype):
-        return None if t is None else self._checked(t, name, (self.rows,), dtype)
 
     def forward(self, logits, noise, temperature=None, top_k=None, top_p=None, min_p=None,
                 out=None, stream=None):
         """tokens [rows] int64 from logits [rows, vocab] and noise [rows, vocab] (float32, Exp(1)
         draws; both may have any row stride).  temperature, top_p, min_p (float32) and top_k
         (int32) are [rows] or None for 1, 1, 0 and 0 (off); temperature <= 0 is greedy."""
-        shape = (self.rows, self.vocab)
-        x_ptr = self._checked(logits, "logits", shape, self.dtype, rows=True)
-        n_ptr = self._checked(noise, "noise", shape, torch.float32, rows=True)
-        made = ()
+        at, shape = self._at, self._row_shape
+        x_ptr, x_stride = self._rows_at(logits, "logits", self._shape, self.dtype)
+        n_ptr, n_stride = self._rows_at(noise, "noise", self._shape, torch.float32)
         if out is None:
-            out = torch.empty((self.rows,), dtype=torch.int64, device=self.device)
-            made = (out,)
-        o_ptr = self._checked(out, "out", (self.rows,), torch.int64)
-        strides = [t.stride(0) if self.rows > 1 else self.vocab for t in (logits, noise)]
-        _ctr.ctr_sampler_forward(self.handle, x_ptr, strides[0], n_ptr, strides[1],
-                                 self._per_row(temperature, "temperature", torch.float32),
-                                 self._per_row(top_k, "top_k", torch.int32),
-                                 self._per_row(top_p, "top_p", torch.float32),
-                                 self._per_row(min_p, "min_p", torch.float32), o_ptr,
-                                 self._stream(stream, *made))
+            out = torch.empty(shape, dtype=torch.int64, device=self.device)
+            raw = self._stream(stream, out)
+        else:
+            raw = self._stream(stream)
+        st = self._forward(
+            self.handle, x_ptr, x_stride, n_ptr, n_stride,
+            None if temperature is None else at(temperature, "temperature", shape, torch.float32),
+            None if top_k is None else at(top_k, "top_k", shape, torch.int32),
+            None if top_p is None else at(top_p, "top_p", shape, torch.float32),
+            None if min_p is None else at(min_p, "min_p", shape, torch.float32),
+            at(out, "out", shape, torch.int64), raw)
+        if st:
+            raise _ctr.CtrError(st, "ctr_sampler_forward")
         return out
 
     def describe(self) -> str:
