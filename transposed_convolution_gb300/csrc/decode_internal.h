@@ -87,6 +87,9 @@ inline int device_sms() {
     return n > 0 ? n : 152;
 }
 
+cudaError_t launch_attention_f32(const ctr_attn_s *pl, const AttnParams &p, cudaStream_t st);
+cudaError_t launch_attention_bf16(const ctr_attn_s *pl, const AttnParams &p, cudaStream_t st);
+cudaError_t launch_attention_f16(const ctr_attn_s *pl, const AttnParams &p, cudaStream_t st);
 cudaError_t launch_attention(const ctr_attn_s *pl, const AttnParams &p, cudaStream_t st);
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t st);
 
