@@ -15,8 +15,10 @@
 // Where the list cannot hold the cuts (flat logits without min_p) the first block does 3 and 4 on
 // the whole row, which it reads again.
 //
-// Sums: a thread's masses are added in fp32 in a fixed order, everything beyond as 64-bit integers in
-// units of 2^-40, and the list's order matters to nothing: equal inputs give equal tokens.
+// Sums: a thread's masses are added in fp32 in a fixed order, everything beyond as integers in units of
+// 2^-35, and the list's order matters to nothing: equal inputs give equal tokens.  A bin's mass is
+// three 32-bit counters of twelve bits' worth each, because 64-bit additions in shared memory are
+// loops of compare-and-swap (1.8 to 100 times as slow, by how often they meet).
 #include <algorithm>
 #include <cooperative_groups.h>
 #include <cstdio>
@@ -38,10 +40,10 @@ namespace {
 typedef unsigned long long u64;
 constexpr float kNegInf = -__builtin_inff();
 constexpr int kBins = 1024;
-constexpr int kListMax = 2048;
+constexpr int kListMax = 3072;
 constexpr float kListBits = 12.0f;    // tokens within 2^-12 of the maximum are listed
 constexpr int kMaxCluster = 8;
-constexpr int kStageBytes = 80 * 1024;  // most logits a block keeps in shared memory
+constexpr int kStageBytes = 58 * 1024;  // most logits a block keeps in shared memory
 
 struct SampleParams {
     const void *logits;
@@ -65,8 +67,8 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
 __device__ __forceinline__ float weight_of(float l, float m, float T) {
     return l == m ? 1.0f : expf((l - m) / T);
 }
-// Masses are sums of weights (at most 1, up to 2^20 of them) in units of 2^-40.
-__device__ __forceinline__ u64 fixed_of(float w) { return __float2ull_rn(w * 1099511627776.0f); }
+// Masses are sums of weights (at most 1, up to 2^20 of them) in units of 2^-35.
+__device__ __forceinline__ u64 fixed_of(float w) { return __float2ull_rn(w * 34359738368.0f); }
 __device__ __forceinline__ float pow2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -89,26 +91,48 @@ struct Best {
     }
 };
 
+// Weights in powers of two, for masses: a relative error of 2^-22 moves a cut by less than
+// rounding the logits does.
+struct Scale {
+    float m, c;              // the maximum, and log2(e) / T
+    // log2 of the weight; 0 at the maximum also where that is infinite, or the scale.
+    __device__ __forceinline__ float below(float l) const { return l == m ? 0.0f : (l - m) * c; }
+    __device__ __forceinline__ float mass(float l) const { return pow2(fmaxf(below(l), -200.0f)); }
+};
+
 // The kept prefix: keys above `low`, and of those equal to it the `ties` with the lowest indices.
 struct Cut {
     uint32_t low;
     uint32_t ties;           // 0xffffffff: all
 };
 
-template <int kThreads> struct Shared {
+struct Listed {
+    uint32_t key, index;
+};
+constexpr int kLocalMax = 2048;      // tokens listed by one block
+
+// (A multiple of 16 bytes: the staged logits lie behind it.)
+template <int kThreads> struct __align__(16) Shared {
     u64 red[kThreads / 32], red2[kThreads / 32];
-    u64 mass[kBins];
-    uint32_t count[kBins];
+    union {
+        // A histogram: counts, masses (twelve bits each, the lowest first), lowest and highest keys.
+        struct {
+            uint32_t count[kBins], mass[3][kBins], low[kBins], high[kBins];
+        };
+        Listed local[kLocalMax];         // before that, this block's tokens for the list
+    };
     // What a boundary search found: its bin and the counts and masses before and in it.
     uint32_t bin, before, inside;
     u64 mass_before, mass_inside;
-    uint32_t low, high;              // lowest and highest key of a bin
+    uint32_t rest, rest_low, rest_high;  // the last bin's count and keys
+    u64 rest_mass;                       // and mass
+    int locals;
     // Written by the cluster's blocks: the maxima at every block, the others at the first.
     uint32_t tops[kMaxCluster];
     u64 bests[kMaxCluster];
-    u64 total;                       // mass of the row
-    int listed;                      // tokens listed
-    uint32_t list_key[kListMax], list_index[kListMax];
+    u64 totals[kMaxCluster];             // mass of each part
+    int listed;                          // tokens listed
+    Listed list[kListMax];
 };
 
 // The largest (or the sum) of the block's values.  Not inlined: behind a loop that lanes leave at
@@ -207,6 +231,22 @@ template <typename T> struct Part {
     }
 };
 
+template <int kThreads> __device__ __forceinline__ void clear_bins(Shared<kThreads> &s) {
+    for (int i = threadIdx.x; i < kBins; i += kThreads)
+    {
+        s.count[i] = s.mass[0][i] = s.mass[1][i] = s.mass[2][i] = s.high[i] = 0;
+        s.low[i] = 0xffffffffu;
+    }
+}
+// One element to a bin; 2^20 of them overflow no counter.
+template <int kThreads> __device__ __forceinline__ void add_to_bin(Shared<kThreads> &s, int bin, u64 w) {
+    atomicAdd(&s.count[bin], 1u);
+    if (w == 0) return;
+    atomicAdd(&s.mass[0][bin], (uint32_t)w & 0xfffu);
+    atomicAdd(&s.mass[1][bin], (uint32_t)(w >> 12) & 0xfffu);
+    atomicAdd(&s.mass[2][bin], (uint32_t)(w >> 24));
+}
+
 // Finds the boundary bin of the histograms in `s`: the first whose counts (or masses) bring the
 // sum to `target`; target is at most the total.  Called by all threads.
 template <int kThreads>
@@ -218,7 +258,8 @@ __device__ __noinline__ void find_bin(Shared<kThreads> &s, bool by_mass, u64 tar
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         c[i] = s.count[t * kEach + i];
-        m[i] = s.mass[t * kEach + i];
+        m[i] = (u64)s.mass[0][t * kEach + i] + ((u64)s.mass[1][t * kEach + i] << 12) +
+               ((u64)s.mass[2][t * kEach + i] << 24);
         cs += c[i];
         ms += m[i];
     }
@@ -266,17 +307,10 @@ __device__ Cut cut_by_keys(Shared<kThreads> &s, uint32_t lo, uint32_t hi, bool b
                            u64 count0, u64 mass0, u64 *mass, Each each) {
     for (;;) {
         const int shift = max(0, 32 - __clz(hi - lo) - 10);
-        for (int i = threadIdx.x; i < kBins; i += kThreads) {
-            s.count[i] = 0;
-            s.mass[i] = 0;
-        }
+        clear_bins(s);
         __syncthreads();
         each([&](uint32_t key, auto weight) {
-            if (key < lo || key > hi) return;
-            const uint32_t bin = (hi - key) >> shift;
-            atomicAdd(&s.count[bin], 1u);
-            const u64 w = weight();
-            if (w) atomicAdd(&s.mass[bin], w);
+            if (key >= lo && key <= hi) add_to_bin(s, (int)((hi - key) >> shift), weight());
         });
         __syncthreads();
         find_bin<kThreads>(s, by_mass, target - (by_mass ? mass0 : count0));
@@ -309,58 +343,57 @@ __device__ Cut cut_by_keys(Shared<kThreads> &s, uint32_t lo, uint32_t hi, bool b
 // *mass is the mass of the prefix, where `weigh`.  First a histogram of the distance to the maximum,
 // in kBins - 1 steps over `range` powers of two and one for the rest.
 template <int kThreads, typename Each>
-__device__ Cut find_cut(Shared<kThreads> &s, float m, float T_, float c, float range, bool by_mass,
-                        bool weigh, u64 target, uint32_t floor_key, u64 *mass, Each each) {
+__device__ Cut find_cut(Shared<kThreads> &s, const Scale &scale, float range, bool by_mass, bool weigh,
+                        u64 target, uint32_t floor_key, u64 *mass, Each each) {
     const float steps = (kBins - 1) / range;
-    auto bin_of = [&](float l) { return min(kBins - 1, (int)((m - l) * c * steps)); };
-    auto weight = [&](float l) { return weigh ? fixed_of(weight_of(l, m, T_)) : 0; };
-    for (int i = threadIdx.x; i < kBins; i += kThreads) {
-        s.count[i] = 0;
-        s.mass[i] = 0;
-    }
+    auto bin_of = [&](float l) { return min(kBins - 1, (int)(-scale.below(l) * steps)); };
+    auto weight = [&](float l) { return weigh ? fixed_of(scale.mass(l)) : 0; };
+    clear_bins(s);
     if (threadIdx.x == 0) {
-        s.low = 0xffffffffu;
-        s.high = 0;
+        s.rest = s.rest_high = 0;
+        s.rest_low = 0xffffffffu;
+        s.rest_mass = 0;
     }
     __syncthreads();
-    uint32_t rest = 0;
+    uint32_t rest = 0, rest_low = 0xffffffffu, rest_high = 0;
     u64 rest_mass = 0;
     each([&](float l) {
-        if (logit_key(l) < floor_key) return;
+        const uint32_t key = logit_key(l);
+        if (key < floor_key) return;
         const int bin = bin_of(l);
         const u64 w = weight(l);
         if (bin == kBins - 1) {
             ++rest;
             rest_mass += w;
+            rest_low = min(rest_low, key);
+            rest_high = max(rest_high, key);
         } else {
-            atomicAdd(&s.count[bin], 1u);
-            if (weigh) atomicAdd(&s.mass[bin], w);
+            add_to_bin(s, bin, w);
+            atomicMin(&s.low[bin], key);
+            atomicMax(&s.high[bin], key);
         }
     });
+    // The last bin's elements are counted by thread: there may be nearly all of them.
     if (rest) {
-        atomicAdd(&s.count[kBins - 1], rest);
-        if (weigh) atomicAdd(&s.mass[kBins - 1], rest_mass);
+        atomicAdd(&s.rest, rest);
+        atomicAdd(&s.rest_mass, rest_mass);
+        atomicMin(&s.rest_low, rest_low);
+        atomicMax(&s.rest_high, rest_high);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        s.count[kBins - 1] = s.rest;
+        s.mass[0][kBins - 1] = (uint32_t)s.rest_mass & 0xfffu;
+        s.mass[1][kBins - 1] = (uint32_t)(s.rest_mass >> 12) & 0xfffu;
+        s.mass[2][kBins - 1] = (uint32_t)(s.rest_mass >> 24);
+        s.low[kBins - 1] = s.rest_low;
+        s.high[kBins - 1] = s.rest_high;
     }
     __syncthreads();
     find_bin<kThreads>(s, by_mass, target);
     const int bin = s.bin;
-    const uint32_t inside = s.inside;
+    const uint32_t inside = s.inside, low = s.low[bin], high = s.high[bin];
     const u64 before = s.before, above = s.mass_before, in = s.mass_inside;
-    // The bin's keys.
-    uint32_t low = 0xffffffffu, high = 0;
-    each([&](float l) {
-        const uint32_t k = logit_key(l);
-        if (k < floor_key || bin_of(l) != bin) return;
-        low = min(low, k);
-        high = max(high, k);
-    });
-    if (high) {
-        atomicMin(&s.low, low);
-        atomicMax(&s.high, high);
-    }
-    __syncthreads();
-    low = s.low;
-    high = s.high;
     __syncthreads();
     if (inside == 1 || (!by_mass && before + inside == target)) {
         *mass = above + in;
@@ -374,16 +407,15 @@ __device__ Cut find_cut(Shared<kThreads> &s, float m, float T_, float c, float r
 // kStaged: a block's part of a row fits shared memory.
 template <typename T, int kThreads, bool kStaged>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(SampleParams p) {
-    extern __shared__ __align__(16) unsigned char staged[];
-    __shared__ Shared<kThreads> s;
+    extern __shared__ __align__(16) unsigned char dynamic[];
+    Shared<kThreads> &s = *reinterpret_cast<Shared<kThreads> *>(dynamic);
     cg::cluster_group cluster = cg::this_cluster();
     const int C = cluster.num_blocks(), rank = cluster.block_rank();
     const int row = blockIdx.x / C, t = threadIdx.x, V = p.vocab;
     const T *logits = static_cast<const T *>(p.logits) + row * p.logits_stride;
     const float *noise = p.noise + row * p.noise_stride;
     if (t == 0) {
-        s.listed = 0;
-        s.total = 0;
+        s.listed = s.locals = 0;
     }
     ptx::griddep_wait();
 
@@ -399,7 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
         return q;
     };
     const Part<T> part = part_of(rank * p.chunk, (rank + 1) * p.chunk);
-    uint4 *const copy = reinterpret_cast<uint4 *>(staged);
+    static_assert(sizeof(Shared<kThreads>) % 16 == 0, "staged logits need 16-byte alignment");
+    uint4 *const copy = reinterpret_cast<uint4 *>(dynamic + sizeof(Shared<kThreads>));
     float top_here = kNegInf;
     const int vecs = part.vecs();
     for (int v0 = t; v0 < vecs + t; v0 += 4 * kThreads) {
@@ -480,66 +513,84 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
     // 2. The mass and the list, in powers of two.  The list's edge lies a little below min_p's; with
     // top-k and top-p it is the far one, since top-p's share is of all the top-k tokens' mass.
     const float c = 1.44269504f / T_;
+    const Scale scale = {m, c};
     const float far = -log2f(min_p) * 1.00001f + 1e-4f;
     const bool to_min = by_min && far < kListBits && !(by_k && by_p);   // nothing below the list is kept
     const float edge = to_min ? far : kListBits;
     const bool usable = m < __builtin_inff() && c < __builtin_inff();
     if (usable) {
         float mass = 0.0f;
-        auto add = [&](float l) {
-            if (by_p) mass += pow2(fmaxf((l - m) * c, -200.0f));
-        };
-        auto list = [&](float l, int i) {
-            if ((l - m) * c >= -edge) {
-                const cg::coalesced_group g = cg::coalesced_threads();
-                int at = 0;
-                if (g.thread_rank() == 0) at = atomicAdd(&lead->listed, (int)g.size());
-                at = g.shfl(at, 0) + g.thread_rank();
-                if (at < kListMax) {
-                    lead->list_key[at] = logit_key(l);
-                    lead->list_index[at] = i;
-                }
-            }
-        };
-        each_vector([&](const uint4 &u, int index) {
+        const int lane = t % 32;
+        const uint32_t none = neg_inf_bits(T()) * (sizeof(T) == 4 ? 1u : 0x10001u);
+#pragma unroll 1
+        for (int v0 = t - lane; v0 < vecs; v0 += kThreads) {
+            const int v = v0 + lane;
+            const uint4 u = v >= vecs ? make_uint4(none, none, none, none) : kStaged ? copy[v] : part.load(v);
             float e[kVec];
             unpack(u, e, T());
             if (by_p) {
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) add(e[i]);
+                for (int i = 0; i < kVec; ++i) mass += scale.mass(e[i]);
             }
-            if ((max_of(u, T()) - m) * c >= -edge) {
+            if (!__any_sync(0xffffffffu, (max_of(u, T()) - m) * c >= -edge)) continue;
+            // The warp's tokens go behind one another, with one addition to the count.
+            int mine = 0;
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) list(e[i], index + i);
+            for (int i = 0; i < kVec; ++i) mine += (e[i] - m) * c >= -edge;
+            int upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const int x = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += x;
             }
-        });
+            int at = 0;
+            if (lane == 31) at = atomicAdd(&s.locals, upto);
+            at = __shfl_sync(0xffffffffu, at, 31) + upto - mine;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+                if ((e[i] - m) * c >= -edge) {
+                    if (at < kLocalMax) s.local[at] = Listed{logit_key(e[i]), (uint32_t)(part.index(v) + i)};
+                    ++at;
+                }
+            __syncwarp();
+        }
         if (by_p) {
             const u64 total = block_sum<kThreads>(fixed_of(mass), s.red);
-            if (t == 0) atomicAdd(&lead->total, total);
+            if (t == 0) lead->totals[rank] = total;
         }
+        // This block's tokens to the first block's list; one that has too many spoils the list.
+        __syncthreads();
+        const int n = s.locals;
+        if (t == 0) s.bin = atomicAdd(&lead->listed, n > kLocalMax ? kListMax + 1 : n);
+        __syncthreads();
+        for (int i = t; i < min(n, kLocalMax); i += kThreads)
+            if (s.bin + i < kListMax) lead->list[s.bin + i] = s.local[i];
     }
     if (!hand_over()) return;
 
     // 3. The cuts.  `each` passes the logits of the list, or of the row, and with_index the indices
     // too.
     const int n = s.listed;
+    u64 total = 0;
+    for (int i = 0; by_p && usable && i < C; ++i) total += s.totals[i];
     auto finish = [&](auto with_index, float range, u64 mass, u64 have) {
         auto each = [&](auto f) { with_index([&](float l, int) { f(l); }); };
         Cut cut = {0, 0xffffffffu};
         if (by_k && have > (u64)asked)
-            cut = find_cut<kThreads>(s, m, T_, c, range, false, by_p, asked, 0, &mass, each);
+            cut = find_cut<kThreads>(s, scale, range, false, by_p, asked, 0, &mass, each);
         if (by_p) {
+            // The mass that the elements at hand have: the cut lies among them, or not.
             u64 all = mass;
             if (!by_k || have <= (u64)asked) {
                 all = 0;
-                each([&](float l) { all += fixed_of(weight_of(l, m, T_)); });
+                each([&](float l) { all += fixed_of(scale.mass(l)); });
                 all = block_sum<kThreads>(all, s.red);
                 if (by_k || mass == 0) mass = all;
             }
             const u64 target = max((u64)1, (u64)fmax(ceil((double)top_p * (double)mass), 0.0));
             if (target <= all) {
                 u64 unused;
-                const Cut at = find_cut<kThreads>(s, m, T_, c, range, true, true, target, cut.low, &unused, each);
+                const Cut at = find_cut<kThreads>(s, scale, range, true, true, target, cut.low, &unused, each);
                 cut = at.low == cut.low ? Cut{cut.low, min(cut.ties, at.ties)} : at;
             } else if (!to_min) {
                 return false;
@@ -569,14 +620,26 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
     // The list holds the cuts if top-k's is inside; top-p's is looked for.
     if (usable && n <= kListMax && (by_k ? n >= asked || (to_min && !by_p) : by_p || to_min) &&
         finish([&](auto f) {
-            for (int i = t; i < n; i += kThreads) f(key_logit(s.list_key[i]), (int)s.list_index[i]);
-        }, edge * 1.001f, s.total, n))
+            for (int i = t; i < n; i += kThreads) f(key_logit(s.list[i].key), (int)s.list[i].index);
+        }, edge * 1.001f, total, n))
         return;
     __syncthreads();
     const Part<T> whole = part_of(0, V);
     auto whole_vectors = [&](auto f) {
+        if (kStaged && C == 1) {
+            each_vector(f);
+            return;
+        }
+        const int all = whole.vecs();
 #pragma unroll 1
-        for (int v = t; v < whole.vecs(); v += kThreads) f(whole.load(v), whole.index(v));
+        for (int v0 = t; v0 < all + t; v0 += 4 * kThreads) {
+            uint4 u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[i] = whole.load(min(v0 + i * kThreads, all - 1));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (v0 + i * kThreads < all) f(u[i], whole.index(v0 + i * kThreads));
+        }
     };
     // A histogram over 30 powers of two; temperatures that overflow the scale take key histograms.
     finish([&](auto f) {
@@ -587,10 +650,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
 template <typename T, int kThreads, bool kStaged>
 cudaError_t launch(const SampleParams &p, int rows, int cluster, cudaStream_t st) {
     const auto kernel = sample_kernel<T, kThreads, kStaged>;
-    const size_t smem = kStaged ? (size_t)p.chunk * sizeof(T) + 32 : 0;
+    const size_t smem = sizeof(Shared<kThreads>) + (kStaged ? (size_t)p.chunk * sizeof(T) + 32 : 0);
     static PerDeviceOnce once;
     const cudaError_t e = once.run(current_device(), cudaSuccess, [&] {
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageBytes + 32);
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)sizeof(Shared<kThreads>) + kStageBytes + 32);
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
