@@ -4,11 +4,11 @@
 // is a lowest key, and how many of the tokens with that key stay.  The logits are read once, which
 // bounds the operator: V elements of 2 or 4 bytes a row, and the random numbers of the kept
 // tokens only.  25 million of them take the CUDA cores about as long as the memory, so the work on
-// each is kept to half a packed maximum, and then a conversion, a scaled difference and an
-// exponential (for the mass of top-p).  A row's block (or cluster of blocks)
-//   1. reads its part into shared memory and takes the maximum;
-//   2. sums the mass, and lists the tokens within 2^-kListBits of the maximum (or min_p of it:
-//      nothing below is kept then) at the cluster's first block; the others are done;
+// each is kept to half a packed maximum, and for top-p a conversion, a scaled difference and an
+// exponential while the memory is busy.  A row's block (or cluster of blocks)
+//   1. reads its part into shared memory, where it fits, and takes the maximum and the mass;
+//   2. lists the tokens within 2^-kListBits of the maximum (or min_p of it: nothing below is kept
+//      then) at the cluster's first block; the others are done;
 //   3. finds the cuts among the listed tokens, by a histogram of their distance to the maximum
 //      and, inside the bin that a cut falls into, histograms of their keys;
 //   4. races the kept ones: best w / noise, ties to the lowest index.
@@ -418,8 +418,15 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
         s.listed = s.locals = 0;
     }
     ptx::griddep_wait();
+    const float temp = p.temperature ? p.temperature[row] : 1.0f;
+    const float min_p = p.min_p ? p.min_p[row] : 0.0f, top_p = p.top_p ? p.top_p[row] : 1.0f;
+    const int asked = p.top_k ? p.top_k[row] : 0;
+    const bool first_only = !(temp > 0.0f) || min_p > 1.0f || asked == 1;
+    const bool by_k = asked > 0 && asked < V, by_p = top_p < 1.0f, by_min = min_p > 0.0f;
+    const float T_ = temp > 0.0f ? temp : 1.0f, c = 1.44269504f / T_;
 
-    // 1. This block's part, and the maximum.
+    // 1. This block's part, the maximum, and each thread's mass in weights of its own maximum so far
+    // (while the memory is busy there is time for the exponentials).
     constexpr int kVec = Part<T>::kVec;
     auto part_of = [&](int from, int to) {
         Part<T> q;
@@ -433,24 +440,43 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
     const Part<T> part = part_of(rank * p.chunk, (rank + 1) * p.chunk);
     static_assert(sizeof(Shared<kThreads>) % 16 == 0, "staged logits need 16-byte alignment");
     uint4 *const copy = reinterpret_cast<uint4 *>(dynamic + sizeof(Shared<kThreads>));
-    float top_here = kNegInf;
+    float top_here = kNegInf, mass = 0.0f;
+    const bool with_mass = by_p && !first_only;
     const int vecs = part.vecs();
-    for (int v0 = t; v0 < vecs + t; v0 += 4 * kThreads) {
-        // Four vectors under way at a time.
-        uint4 u[4];
+    // f(vector, v) of a part's vectors in memory, four under way at a time.
+    auto from_memory = [&](const Part<T> &q, auto f) {
+        const int all = q.vecs();
+#pragma unroll 1
+        for (int v0 = t; v0 < all + t; v0 += 4 * kThreads) {
+            uint4 u[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) u[i] = part.load(min(v0 + i * kThreads, vecs - 1));
+            for (int i = 0; i < 4; ++i) u[i] = q.load(min(v0 + i * kThreads, all - 1));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int v = v0 + i * kThreads;
-            if (kStaged && v < vecs) copy[v] = u[i];
-            top_here = fmaxf(top_here, max_of(u[i], T()));
+            for (int i = 0; i < 4; ++i)
+                if (v0 + i * kThreads < all) f(u[i], v0 + i * kThreads);
         }
-    }
+    };
+    from_memory(part, [&](const uint4 &u, int v) {
+        if (kStaged) copy[v] = u;
+        const float top = fmaxf(max_of(u, T()), kNegInf);
+        if (with_mass && top > kNegInf) {
+            if (top > top_here) mass *= top_here > kNegInf ? pow2((top_here - top) * c) : 0.0f;
+            top_here = fmaxf(top_here, top);
+            float e[kVec];
+            unpack(u, e, T());
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) mass += pow2(fmaxf((e[i] - top_here) * c, -200.0f));
+        }
+        top_here = fmaxf(top_here, top);
+    });
     // f(vector, index of its first element), and f(logit, index), of the part.
     auto each_vector = [&](auto f) {
+        if (kStaged) {
 #pragma unroll 2
-        for (int v = t; v < vecs; v += kThreads) f(kStaged ? copy[v] : part.load(v), part.index(v));
+            for (int v = t; v < vecs; v += kThreads) f(copy[v], part.index(v));
+        } else {
+            from_memory(part, [&](const uint4 &u, int v) { f(u, part.index(v)); });
+        }
     };
     auto each_of = [&](auto vectors, auto f) {
         vectors([&](const uint4 &u, int index) {
@@ -481,12 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
         return true;
     };
     const float m = key_logit(top_key);
-    const float temp = p.temperature ? p.temperature[row] : 1.0f;
-    const float min_p = p.min_p ? p.min_p[row] : 0.0f, top_p = p.top_p ? p.top_p[row] : 1.0f;
-    const int asked = p.top_k ? p.top_k[row] : 0;
-    const bool greedy = !(temp > 0.0f) || min_p > 1.0f || asked == 1 || m == kNegInf;
-    const bool by_k = asked > 0 && asked < V, by_p = top_p < 1.0f, by_min = min_p > 0.0f;
-    const float T_ = temp > 0.0f ? temp : 1.0f;
+    const bool greedy = first_only || m == kNegInf;
     Best best;
     auto race = [&](float l, int i) {
         best.offer(weight_of(l, m, T_) / fmaxf(__ldg(noise + i), 1.17549435e-38f), i);
@@ -512,50 +533,30 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
 
     // 2. The mass and the list, in powers of two.  The list's edge lies a little below min_p's; with
     // top-k and top-p it is the far one, since top-p's share is of all the top-k tokens' mass.
-    const float c = 1.44269504f / T_;
     const Scale scale = {m, c};
     const float far = -log2f(min_p) * 1.00001f + 1e-4f;
     const bool to_min = by_min && far < kListBits && !(by_k && by_p);   // nothing below the list is kept
     const float edge = to_min ? far : kListBits;
     const bool usable = m < __builtin_inff() && c < __builtin_inff();
     if (usable) {
-        float mass = 0.0f;
-        const int lane = t % 32;
-        const uint32_t none = neg_inf_bits(T()) * (sizeof(T) == 4 ? 1u : 0x10001u);
-#pragma unroll 1
-        for (int v0 = t - lane; v0 < vecs; v0 += kThreads) {
-            const int v = v0 + lane;
-            const uint4 u = v >= vecs ? make_uint4(none, none, none, none) : kStaged ? copy[v] : part.load(v);
+        each_vector([&](const uint4 &u, int index) {
+            if (!((max_of(u, T()) - m) * c >= -edge)) return;
             float e[kVec];
             unpack(u, e, T());
-            if (by_p) {
-#pragma unroll
-                for (int i = 0; i < kVec; ++i) mass += scale.mass(e[i]);
-            }
-            if (!__any_sync(0xffffffffu, (max_of(u, T()) - m) * c >= -edge)) continue;
-            // The warp's tokens go behind one another, with one addition to the count.
             int mine = 0;
 #pragma unroll
             for (int i = 0; i < kVec; ++i) mine += (e[i] - m) * c >= -edge;
-            int upto = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o *= 2) {
-                const int x = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += x;
-            }
-            int at = 0;
-            if (lane == 31) at = atomicAdd(&s.locals, upto);
-            at = __shfl_sync(0xffffffffu, at, 31) + upto - mine;
+            int at = atomicAdd(&s.locals, mine);
 #pragma unroll
             for (int i = 0; i < kVec; ++i)
                 if ((e[i] - m) * c >= -edge) {
-                    if (at < kLocalMax) s.local[at] = Listed{logit_key(e[i]), (uint32_t)(part.index(v) + i)};
+                    if (at < kLocalMax) s.local[at] = Listed{logit_key(e[i]), (uint32_t)(index + i)};
                     ++at;
                 }
-            __syncwarp();
-        }
+        });
         if (by_p) {
-            const u64 total = block_sum<kThreads>(fixed_of(mass), s.red);
+            const float share = top_here > kNegInf ? mass * pow2((top_here - m) * c) : 0.0f;
+            const u64 total = block_sum<kThreads>(fixed_of(share), s.red);
             if (t == 0) lead->totals[rank] = total;
         }
         // This block's tokens to the first block's list; one that has too many spoils the list.
@@ -626,20 +627,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
     __syncthreads();
     const Part<T> whole = part_of(0, V);
     auto whole_vectors = [&](auto f) {
-        if (kStaged && C == 1) {
+        if (C == 1)
             each_vector(f);
-            return;
-        }
-        const int all = whole.vecs();
-#pragma unroll 1
-        for (int v0 = t; v0 < all + t; v0 += 4 * kThreads) {
-            uint4 u[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) u[i] = whole.load(min(v0 + i * kThreads, all - 1));
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (v0 + i * kThreads < all) f(u[i], whole.index(v0 + i * kThreads));
-        }
+        else
+            from_memory(whole, [&](const uint4 &u, int v) { f(u, whole.index(v)); });
     };
     // A histogram over 30 powers of two; temperatures that overflow the scale take key histograms.
     finish([&](auto f) {
@@ -676,13 +667,12 @@ cudaError_t launch(const SampleParams &p, int rows, int cluster, cudaStream_t st
 
 template <typename T>
 cudaError_t launch(const ctr_sampler_s *pl, SampleParams p, cudaStream_t st) {
-    // Blocks a row: enough that a part fits shared memory, and that few rows fill the GPU, but
-    // at least 4096 elements each.
+    // Blocks a row: two an SM for few rows, but at least 4096 elements each.  A part that does not
+    // fit shared memory is read again from L2: 256 rows of 100003 16-bit logits, one block a row, take
+    // 30 us, and in clusters of four, whose parts fit but whose blocks wait for one another, 42.
     int cluster = 1;
     const int rows = (int)pl->rows;
-    while (cluster < kMaxCluster &&
-           ((int64_t)p.vocab * (int64_t)sizeof(T) > (int64_t)cluster * kStageBytes ||
-            (rows * cluster * 2 <= pl->num_sms && p.vocab >= 4096 * 2 * cluster)))
+    while (cluster < kMaxCluster && (int64_t)rows * cluster <= pl->num_sms && p.vocab >= 4096 * 2 * cluster)
         cluster *= 2;
     p.chunk = ((p.vocab + cluster - 1) / cluster + 15) / 16 * 16;
     if (p.chunk <= 4096) return launch<T, 256, true>(p, rows, cluster, st);
