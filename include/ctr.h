@@ -583,7 +583,8 @@ ctr_status ctr_attn_bind_workspace(ctr_attn_t plan, void *dev_ptr, size_t bytes)
  * ctr_attn_bind_workspace, before the first ctr_attn_forward (CTR_ERR_NOT_PREPARED
  * otherwise).  The calls themselves leave the counters cleared. */
 ctr_status ctr_attn_reset(ctr_attn_t plan, void *stream);
-/* Bind the caller-owned cache pages; they must stay allocated while bound. */
+/* Bind the caller-owned cache pages; they must stay allocated while bound.  At most 2^36 elements
+ * each (CTR_ERR_UNSUPPORTED beyond). */
 ctr_status ctr_attn_bind_cache(ctr_attn_t plan, void *k_pages, void *v_pages, int64_t num_pages);
 /* One decode step.  Asynchronous on stream; never allocates or synchronises.  weights_out is
  * required when weights are enabled and must be NULL (as weights_in) otherwise. */

@@ -624,7 +624,11 @@ __global__ void __launch_bounds__(32 * C::Shape::kWarps, C::Shape::kPerSm) atten
     const bool copies = row0 < kRows && col * kChunk < D;
     // With pages of whole sixteens a warp's slots lie in one page.
     const bool one_page = p.cache.page % 16 == 0;
-    const int64_t lane_off = row0 * p.cache.row_stride + col * kChunk;
+    // Offsets of rows in the pages, in sixteens of elements: a plan's pages have fewer than 2^32.
+    const uint32_t page16 = (uint32_t)(p.cache.page_stride / 16), head16 = (uint32_t)(p.cache.head_stride / 16),
+                   row16 = (uint32_t)(p.cache.row_stride / 16);
+    const T *const k_lane = static_cast<const T *>(p.k) + row0 * p.cache.row_stride + col * kChunk;
+    const T *const v_lane = static_cast<const T *>(p.v) + row0 * p.cache.row_stride + col * kChunk;
     const int64_t row_step = kRows * p.cache.row_stride;
     const uint32_t k_dst = ptx::smem_u32(ring) + row0 * k_pitch + col * 16;
     const uint32_t v_dst = ptx::smem_u32(ring) + 16 * k_pitch + row0 * v_pitch + col * 16;
@@ -650,16 +654,15 @@ __global__ void __launch_bounds__(32 * C::Shape::kWarps, C::Shape::kPerSm) atten
             const bool inside = j >= in.lo && j < in.n;
             const bool ok = inside && (unsigned)page_no < (unsigned)p.cache.num_pages;
             const unsigned mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-            int64_t off = page_no * p.cache.page_stride + hk * p.cache.head_stride +
-                          (j - page_index(j) * p.cache.page) * p.cache.row_stride;
+            const uint32_t off = page_no * page16 + hk * head16 + (j - page_index(j) * p.cache.page) * row16;
             if (lane == 0) slot_masks[warp][in_slot] = mask;
             if (inside && !ok)
                 atomicOr(p.cache.status, kStatusBadPage);
             const uint32_t kd = k_dst + in_slot * stage_bytes, vd = v_dst + in_slot * stage_bytes;
             const int newest = ntok[in.b];       // -n where slot n - 1 is the new token's
             if (mask == 0xffffu && one_page && !(newest < 0 && -newest - 1 < j0 + 16)) {
-                off = __shfl_sync(0xffffffffu, off, 0) + lane_off;
-                const T *ks = static_cast<const T *>(p.k) + off, *vs = static_cast<const T *>(p.v) + off;
+                const int64_t first = (int64_t)__shfl_sync(0xffffffffu, off, 0) * 16;
+                const T *ks = k_lane + first, *vs = v_lane + first;
                 if (kD && kAcross == 1 && p.cache.row_stride == kD) {
                     // Rows one behind the other: every offset is a constant.
 #pragma unroll
@@ -681,18 +684,18 @@ __global__ void __launch_bounds__(32 * C::Shape::kWarps, C::Shape::kPerSm) atten
                     }
                 }
             } else {
-#pragma unroll 1
+                const int64_t at_new = in.b * p.kv_stride + (int64_t)hk * D;
+                const T *const k_new = static_cast<const T *>(p.k_new) + at_new;
+                const T *const v_new = static_cast<const T *>(p.v_new) + at_new;
+#pragma unroll 4
                 for (int i = 0; i < kRounds; ++i) {
-                    const int row = i * kRows + row0;
-                    const int64_t o = __shfl_sync(0xffffffffu, off, row & 15);
-                    const bool on = mask >> (row & 15) & 1;
-                    const T *ks = static_cast<const T *>(p.k) + o, *vs = static_cast<const T *>(p.v) + o;
-                    if (on && newest == -(j0 + row + 1)) {
-                        // The new token's row comes from the arguments.
-                        const int64_t x = in.b * p.kv_stride + (int64_t)hk * D;
-                        ks = static_cast<const T *>(p.k_new) + x;
-                        vs = static_cast<const T *>(p.v_new) + x;
-                    }
+                    const int row = (i * kRows + row0) & 15;
+                    const int64_t o = (int64_t)__shfl_sync(0xffffffffu, off, row) * 16;
+                    const bool on = mask >> row & 1;
+                    // The new token's row comes from the arguments.
+                    const bool fresh = newest == -(j0 + row + 1);
+                    const T *ks = fresh ? k_new : static_cast<const T *>(p.k) + o;
+                    const T *vs = fresh ? v_new : static_cast<const T *>(p.v) + o;
                     // Hidden slots are filled with zeros: no probability is given to them, and
                     // what V holds there must be finite.  (The address is not read.)
 #pragma unroll

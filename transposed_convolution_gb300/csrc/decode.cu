@@ -132,7 +132,9 @@ ctr_status ctr_attn_reset(ctr_attn_t pl, void *stream) {
 
 ctr_status ctr_attn_bind_cache(ctr_attn_t pl, void *k_pages, void *v_pages, int64_t num_pages) {
     if (!pl || !k_pages || !v_pages || num_pages < 1) return CTR_ERR_INVALID_ARG;
-    if (num_pages > 0x7fffffff) return CTR_ERR_UNSUPPORTED;
+    // Kernels hold row offsets in sixteens of elements in 32 bits (2^37 bytes of 16-bit pages).
+    if (num_pages > 0x7fffffff || num_pages > (((int64_t)1 << 32) - 1) / (pl->Hkv * pl->page * (pl->D / 16)))
+        return CTR_ERR_UNSUPPORTED;
     if (!aligned(k_pages, 16) || !aligned(v_pages, 16)) return CTR_ERR_MISALIGNED;
     pl->k_pages = k_pages;
     pl->v_pages = v_pages;

@@ -210,28 +210,27 @@ class PagedAttention(_DecodePlan):
         budget = int(budget)
         if dst_tables.dim() != 2 or dst_tables.shape[0] != self.B:
             raise ValueError("dst_tables must be [%d, pages]" % self.B)
-        t_ptr = self._at(tables, "tables", self._table_shape, torch.int32)
-        l_ptr = self._at(lens, "lens", self._lens_shape, torch.int32)
-        w_ptr = self._at(weights, "weights", self._weights_shape, torch.float32)
-        d_ptr = self._at(dst_tables, "dst_tables", dst_tables.shape, torch.int32)
-        made = []
+        at, made = self._at, []
+        shape = (self.B, self.H_kv, max(budget, 0))
+        t_ptr = at(tables, "tables", self._table_shape, torch.int32)
+        l_ptr = at(lens, "lens", self._lens_shape, torch.int32)
+        w_ptr = at(weights, "weights", self._weights_shape, torch.float32)
+        d_ptr = at(dst_tables, "dst_tables", dst_tables.shape, torch.int32)
         if slots is None:
-            slots = torch.empty((self.B, self.H_kv, max(budget, 0)), dtype=torch.int32,
-                                device=self.device)
+            slots = torch.empty(shape, dtype=torch.int32, device=self.device)
             made.append(slots)
         if lens_out is None:
-            lens_out = torch.empty((self.B,), dtype=torch.int32, device=self.device)
+            lens_out = torch.empty(self._lens_shape, dtype=torch.int32, device=self.device)
             made.append(lens_out)
         if weights_out is None:
-            weights_out = torch.zeros((self.B, self.H_kv, max(budget, 0)), dtype=torch.float32,
-                                      device=self.device)
+            weights_out = torch.zeros(shape, dtype=torch.float32, device=self.device)
             made.append(weights_out)
         if weights_out.dim() != 3:
             raise ValueError("weights_out must be [%d, %d, >= %d]" % (self.B, self.H_kv, budget))
         pitch = weights_out.shape[2]
-        s_ptr = self._at(slots, "slots", (self.B, self.H_kv, budget), torch.int32)
-        lo_ptr = self._at(lens_out, "lens_out", (self.B,), torch.int32)
-        wo_ptr = self._at(weights_out, "weights_out", (self.B, self.H_kv, pitch), torch.float32)
+        s_ptr = at(slots, "slots", shape, torch.int32)
+        lo_ptr = at(lens_out, "lens_out", self._lens_shape, torch.int32)
+        wo_ptr = at(weights_out, "weights_out", (self.B, self.H_kv, pitch), torch.float32)
         st = self._evict(self.handle, t_ptr, l_ptr, w_ptr, d_ptr, dst_tables.shape[1], budget,
                          int(sinks), int(recent), s_ptr, lo_ptr, wo_ptr, pitch,
                          self._stream(stream, *made))
