@@ -169,6 +169,39 @@ def test_weights(shape, dtype):
     assert abs(zero[0, 0, :lens[0] + 1].sum().item() - G) < 1e-4 * G
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 96, 112, 128, 256])
+def test_many_sequences_and_units_split_anywhere(D, dtype):
+    """Hundreds of units whose tiles are cut at every place, with empty and idle rows between."""
+    lens = [(i * 37) % 200 if i % 9 else -1 for i in range(300)] + [3000, 0]
+    s = make(len(lens), 2, 1, D, 16, lens, dtype, seed=D)
+    before = s["k"].clone(), s["v"].clone()
+    plan = ctr.PagedAttention(len(lens), 2, 1, D, 16, s["tables"].shape[1], k_pages=s["k"],
+                              v_pages=s["v"])
+    out = plan.forward(s["q"], s["tables"], s["lens"], s["k_new"], s["v_new"])
+    plan.check()
+    s["k"], s["v"] = before
+    check(s, out, 16, "head", dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+def test_short_caches_are_cut_into_whole_units(dtype):
+    """More units than blocks, in caches of at most 256 slots a sequence."""
+    lens = [(i * 29) % 255 if i % 7 else 0 for i in range(200)]
+    s = make(200, 6, 3, 64, 16, lens, dtype, seed=2, max_pages=16)
+    before = s["k"].clone(), s["v"].clone()
+    plan = ctr.PagedAttention(200, 6, 3, 64, 16, 16, k_pages=s["k"], v_pages=s["v"], weights=True)
+    w = torch.zeros(200, 3, plan.capacity, device="cuda")
+    out = plan.forward(s["q"], s["tables"], s["lens"], s["k_new"], s["v_new"], weights=w)
+    plan.check()
+    s["k"], s["v"] = before
+    probs, ds = check(s, out, 16, "head", dtype)
+    for b, n in enumerate(lens):
+        want = probs[b].reshape(3, 2, n + 1).sum(1)
+        rel = (2 * ds[b].max() + (n / 16 + 64) * 2.0 ** -24) * 1.01 + 4 * 2.0 ** -24
+        assert (np.abs(f64(w[b, :, :n + 1]) - want) <= rel * want + 1e-30).all()
+
+
 def test_scale_and_huge_scores():
     """Scores of +-1e4: the running maximum keeps the exponentials in range; a scale of zero
     averages."""

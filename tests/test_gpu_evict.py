@@ -102,6 +102,25 @@ def test_ties_and_odd_weights(kind):
         run([n], 2, 16, 16, budget, sinks, recent, "f16", "head", w=w.clone())
 
 
+@pytest.mark.parametrize("kind", ["random", "equal", "few values", "heavy end"])
+@pytest.mark.parametrize("lens,cap_pages", [([20000], 0), ([8192, 100], 0), ([16385, -1], 40),
+                                            ([50000], 0), ([170000], 0)])
+def test_few_long_sequences(lens, cap_pages, kind):
+    """Several blocks a head, whose parts the ties cross, and parts that do not fit shared memory."""
+    g = torch.Generator().manual_seed(7)
+    page = 256
+    cap = (-(-max(lens) // page) + cap_pages) * page
+    w = torch.rand(len(lens), 1, cap, generator=g)
+    if kind == "equal":
+        w[:] = 1.0
+    elif kind == "few values":
+        w = torch.randint(0, 3, w.shape, generator=g).float()
+    elif kind == "heavy end":
+        w[:, :, max(lens) // 2:] += 1.0
+    for budget, sinks, recent in ((3000, 5, 70), (7, 0, 0)):
+        run(lens, 1, 16, page, budget, sinks, recent, "f16", "head", w=w, spare=cap_pages)
+
+
 def test_wider_tables_and_default_outputs():
     run([300, 200], 2, 64, 16, 100, 2, 20, spare=3)
     k = torch.randn(8, 2, 16, 64).cuda()

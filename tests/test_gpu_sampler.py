@@ -91,6 +91,21 @@ def test_odd_logits(kind, V):
         assert got[2] == -1 and got[5] == -1
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,V", [(1, 100001), (3, 50000), (20, 9000), (170, 6000), (160, 70001)])
+def test_flat_logits_by_blocks_a_row(rows, V, dtype):
+    """Logits so flat that the tokens near the maximum are too many to list, in clusters of 8, 4, 2 and
+    1 block, staged and not; and peaked ones in between."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    spread = torch.tensor([0.01, 0.3, 1.0, 4.0], device="cuda")[torch.arange(rows, device="cuda") % 4]
+    logits = (torch.randn(rows, V, generator=g, device="cuda") * spread[:, None]).to(DT[dtype])
+    noise = torch.empty(rows, V, device="cuda").exponential_(generator=g)
+    some = [(1.0, 0, 0.9, 0.0), (0.7, 0, 0.5, 0.001), (1.0, V // 2, 0.99, 0.0), (1.0, 5000, 1.0, 0.0),
+            (1.2, 3, 0.9, 0.5), (1.0, V - 1, 0.999, 0.0), (1.0, 0, 1.0, 1e-5)]
+    filters = [some[(i * 3) % len(some)] for i in range(rows)]
+    check(logits, noise, filters, tokens(logits, noise, filters, dtype))
+
+
 def test_equal_scores_take_the_lowest_index():
     x = torch.zeros(4, 5000, device="cuda")
     noise = torch.full((4, 5000), 0.5, device="cuda")

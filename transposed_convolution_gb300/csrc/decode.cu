@@ -230,6 +230,7 @@ ctr_status ctr_attn_evict(ctr_attn_t pl, const int32_t *tables, const int32_t *l
     p.B = (int)pl->B;
     p.Hkv = (int)pl->Hkv;
     p.esize = esize_of(pl);
+    p.num_sms = pl->num_sms;
     p.row_bytes = (int)pl->D * p.esize;
     return ctr::launch_evict(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CTR_OK
                                                                                  : CTR_ERR_CUDA;

@@ -66,7 +66,7 @@ struct EvictParams {
     int budget, sinks, recent;
     int32_t *slots, *lens_out;
     float *w_out;
-    int B, Hkv, row_bytes, esize;
+    int B, Hkv, row_bytes, esize, num_sms;
 };
 
 // Most blocks an SM that an attention launch has; the workspace holds two parts for each.

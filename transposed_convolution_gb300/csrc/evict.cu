@@ -3,21 +3,27 @@
 // Two kernels.  The first reads each (sequence, KV head)'s weights once, as order-preserving keys
 // in shared memory where they fit, finds the lowest key that stays by three histograms (11, 11
 // and 10 bits), and lists the kept slots in order: counts by warp, their sum, and the list, which
-// takes a ballot for each 32 slots.  The second copies the listed rows; it moves
+// takes a ballot for each 32 slots.  Few long sequences are spread over clusters of blocks, which add up
+// their histograms (32767 slots of 16 heads: 24 us in 16 blocks).  The second copies the listed rows; it moves
 // 4 D elements a row and is bound by the cache's memory, so its blocks are many and small, each
 // with the row addresses of 64 rows in shared memory and two 16-byte loads of K and V under way
 // for each thread at a time.  It is launched while the first still runs, and waits for its end.
 #include <algorithm>
+#include <cooperative_groups.h>
 
 #include "decode_device.cuh"
 #include "ptx.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace ctr {
 namespace {
 
 constexpr int kSelectThreads = 1024, kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kStageKeys = 40 * 1024;      // most keys kept in shared memory (160 KB)
+constexpr int kStageKeys = 40 * 1024;      // most keys a block keeps in shared memory (160 KB)
+// Clusters of eight such blocks leave too few free SMs a GPC for a second one everywhere.
+constexpr int kMaxCluster = 4, kPartSlots = 4096;
 constexpr int kCopyThreads = 256, kCopyRows = 64;
 
 // Order-preserving key: larger weight, larger key; NaN lowest, -0 as +0.
@@ -83,14 +89,18 @@ __device__ __noinline__ void find_bin(const int (&hist)[kBins], int target, int 
     __syncthreads();
 }
 
-// One block for each (sequence, KV head).
+// One cluster for each (sequence, KV head), each block a run of `part` slots.
 template <bool kStaged>
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(EvictParams p) {
+__global__ void __launch_bounds__(kSelectThreads) select_kernel(EvictParams p, int part) {
     extern __shared__ __align__(16) unsigned char staged[];
-    __shared__ int hist[kBins], warp_a[kSelectWarps], warp_b[kSelectWarps];
+    // A histogram a round, so that a block may go on while others still read its last one.
+    __shared__ int hists[3][kBins], sums[kBins], warp_a[kSelectWarps], warp_b[kSelectWarps];
+    __shared__ int counts[kMaxCluster][2];
     __shared__ Boundary found;
     uint32_t *const keys = reinterpret_cast<uint32_t *>(staged);
-    const int unit = blockIdx.x, b = unit / p.Hkv, t = threadIdx.x, lane = t % 32, warp = t / 32;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = cluster.num_blocks(), rank = cluster.block_rank();
+    const int unit = blockIdx.x / C, b = unit / p.Hkv, t = threadIdx.x, lane = t % 32, warp = t / 32;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int len = p.cache.lens[b];
@@ -99,36 +109,47 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(EvictParams p) {
         n = p.cache.cap;
         if (t == 0) atomicOr(p.cache.status, kStatusBadLength);
     }
+    const int first = min(rank * part, n), last = min(first + part, n);     // this block's slots
     const int keep = min(n, p.budget);
     const float *const w = p.w + (int64_t)unit * p.cache.cap;
     const int s0 = min(p.sinks, n), r0 = max(s0, n - p.recent);   // the others: s0 <= j < r0
     const int want = keep - s0 - (n - r0);                        // of the others
     const bool all = want >= r0 - s0;
-    auto key_at = [&](int j) { return kStaged ? keys[j] : weight_key(w[j]); };
+    auto key_at = [&](int j) { return kStaged ? keys[j - first] : weight_key(w[j]); };
 
     // The lowest key that stays, by histograms of its bits from the top.
     uint32_t cut = 0;
     int ties = 0;          // how many of the others with key == cut stay
     if (want > 0 && !all) {
         int target = want, above = 32;      // bits of the keys not yet decided
+        const int from = max(first, s0), to = min(last, r0);
         for (int round = 0; round < 3; ++round) {
+            int (&hist)[kBins] = hists[round];
             const int bits = round < 2 ? 11 : 10, shift = above - bits;
             for (int i = t; i < kBins; i += kSelectThreads) hist[i] = 0;
             __syncthreads();
 #pragma unroll 4
-            for (int j = s0 + t; j < r0; j += kSelectThreads) {
+            for (int j = from + t; j < to; j += kSelectThreads) {
                 uint32_t k;
                 if (round == 0) {
                     k = weight_key(w[j]);
-                    if (kStaged) keys[j] = k;
+                    if (kStaged) keys[j - first] = k;
                 } else {
                     k = key_at(j);
                 }
                 if (round == 0 || k >> above == cut >> above)
                     atomicAdd(&hist[k >> shift & ((1u << bits) - 1)], 1);
             }
+            if (C > 1) {
+                cluster.sync();
+                for (int i = t; i < kBins; i += kSelectThreads) {
+                    int sum = 0;
+                    for (int c = 0; c < C; ++c) sum += cluster.map_shared_rank(&hist[0], c)[i];
+                    sums[i] = sum;
+                }
+            }
             __syncthreads();
-            find_bin(hist, target, warp_a, &found);
+            find_bin(C > 1 ? sums : hist, target, warp_a, &found);
             cut |= (uint32_t)found.bin << shift;
             target -= found.before;
             above = shift;
@@ -144,9 +165,9 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(EvictParams p) {
     const bool whole_bin = ties == 0x7fffffff;     // every key >= cut stays
     __syncthreads();
 
-    // The list: each warp takes a run of the slots.
-    const int run = ((n + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
-    const int from = min(warp * run, n), to = min(from + run, n);
+    // The list: each warp takes a run of the block's slots.
+    const int run = ((last - first + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
+    const int from = min(first + warp * run, last), to = min(from + run, last);
     auto judge = [&](int j, bool *on, bool *eq) {
         *on = *eq = false;
         if (j >= to) return;
@@ -169,7 +190,21 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(EvictParams p) {
         warp_b[warp] = equal;
     }
     scan_warps(warp_a, warp_b);
-    int tie = warp_b[warp], at = warp_a[warp] + min(tie, ties);
+    int sure_before = warp_a[warp], tie = warp_b[warp];
+    if (C > 1) {
+        // The last warp has the block's totals: to every block.
+        if (warp == kSelectWarps - 1 && lane < C) {
+            int (*to_counts)[2] = cluster.map_shared_rank(&counts[0], lane);
+            to_counts[rank][0] = sure_before + sure;
+            to_counts[rank][1] = tie + equal;
+        }
+        cluster.sync();
+        for (int c = 0; c < rank; ++c) {
+            sure_before += counts[c][0];
+            tie += counts[c][1];
+        }
+    }
+    int at = sure_before + min(tie, ties);
     int32_t *const slots = p.slots + (int64_t)unit * p.budget;
     const unsigned below = (1u << lane) - 1;
     for (int base = from; base < to; base += 32) {
@@ -182,8 +217,10 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(EvictParams p) {
         if (on) slots[at + __popc(bo & below)] = base + lane;
         at += __popc(bo);
     }
-    for (int i = keep + t; i < p.budget; i += kSelectThreads) slots[i] = -1;
-    if (unit % p.Hkv == 0 && t == 0) p.lens_out[b] = len < 0 ? len : keep;
+    if (rank == 0) {
+        for (int i = keep + t; i < p.budget; i += kSelectThreads) slots[i] = -1;
+        if (unit % p.Hkv == 0 && t == 0) p.lens_out[b] = len < 0 ? len : keep;
+    }
 }
 
 // kCopyRows kept rows of one (sequence, KV head) a block: K, V and weights.
@@ -235,23 +272,42 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(EvictParams p, int b
     }
 }
 
+template <bool kStaged>
+cudaError_t launch_select(const EvictParams &p, int units, int cluster, int part, cudaStream_t st) {
+    static PerDeviceOnce once;
+    const cudaError_t e = once.run(current_device(), cudaSuccess, [] {
+        return cudaFuncSetAttribute(select_kernel<kStaged>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kStaged ? kStageKeys * (int)sizeof(uint32_t) : 0);
+    });
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * cluster));
+    cfg.blockDim = dim3(kSelectThreads);
+    cfg.dynamicSmemBytes = kStaged ? (size_t)part * sizeof(uint32_t) : 0;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, select_kernel<kStaged>, p, part);
+}
+
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t st) {
     const int units = p.B * p.Hkv;
-    cudaError_t e;
-    if (p.cache.cap <= kStageKeys) {
-        static PerDeviceOnce once;
-        e = once.run(current_device(), cudaSuccess, [] {
-            return cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kStageKeys * (int)sizeof(uint32_t));
-        });
-        if (e != cudaSuccess) return e;
-        e = launch_pdl(select_kernel<true>, dim3((unsigned)units), dim3(kSelectThreads),
-                       (size_t)p.cache.cap * sizeof(uint32_t), st, p);
-    } else {
-        e = launch_pdl(select_kernel<false>, dim3((unsigned)units), dim3(kSelectThreads), 0, st, p);
-    }
+    // Blocks a unit: two an SM for few units, but kPartSlots slots each at least.
+    int cluster = 1;
+    while (cluster < kMaxCluster && (int64_t)units * cluster <= p.num_sms &&
+           p.cache.cap >= 2 * cluster * kPartSlots)
+        cluster *= 2;
+    const int part = ((p.cache.cap + cluster - 1) / cluster + 31) / 32 * 32;
+    cudaError_t e = part <= kStageKeys ? launch_select<true>(p, units, cluster, part, st)
+                                       : launch_select<false>(p, units, cluster, part, st);
     if (e != cudaSuccess) return e;
     const int blocks = (int)((std::min<int64_t>(p.budget, p.cache.cap) + kCopyRows - 1) / kCopyRows);
     count_launches(2);

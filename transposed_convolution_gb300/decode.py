@@ -4,8 +4,9 @@ and given random numbers).
 
 Both only marshal arguments to the C ABI (``include/ctr.h``: ``ctr_attn_*``, ``ctr_sampler_*``)
 after checking them.  A call runs on ``stream`` (default: the current stream of the plan's
-device).  When ``stream`` is another stream than the current one, the caller orders the two, as
-for ``Plan``; tensors that the call itself allocates are then kept for that stream.
+device, which has to be the current device).  When ``stream`` is another stream than the current
+one, the caller orders the two, as for ``Plan``; the plan's own tensors and those that the call
+allocates are then kept for that stream.
 """
 from __future__ import annotations
 
@@ -33,13 +34,14 @@ class _DecodePlan:
 
     handle = None
     _destroy = None
+    _kept = ()              # tensors of the plan that its kernels use
 
     def _stream(self, stream, *made):
         """The raw stream of a call; tensors that the call made are kept for it."""
         current = torch._C._cuda_getCurrentRawStream(self._index)
         if stream is None or stream.cuda_stream == current:
             return current
-        for t in made:
+        for t in made + self._kept:
             t.record_stream(stream)
         return stream.cuda_stream
 
@@ -141,6 +143,7 @@ class PagedAttention(_DecodePlan):
             _ctr.ctr_attn_bind_cache(self.handle, k, v, self.num_pages)
             self.workspace_bytes = _ctr.ctr_attn_workspace_bytes(self.handle)
             self.workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=self.device)
+            self._kept = (self.workspace, self.k_pages, self.v_pages)
             _ctr.ctr_attn_bind_workspace(self.handle, self.workspace.data_ptr(),
                                          self.workspace_bytes)
             self._q_shape, self._kv_shape = (self.B, self.H_q, self.D), (self.B, self.H_kv, self.D)
