@@ -123,7 +123,7 @@ template <int kThreads> struct __align__(16) Shared {
     };
     // What a boundary search found: its bin and the counts and masses before and in it.
     uint32_t bin, before, inside;
-    u64 mass_before, mass_inside;
+    u64 mass_before, mass_inside, mass_sum;
     uint32_t rest, rest_low, rest_high;  // the last bin's count and keys
     u64 rest_mass;                       // and mass
     int locals;
@@ -248,7 +248,7 @@ template <int kThreads> __device__ __forceinline__ void add_to_bin(Shared<kThrea
 }
 
 // Finds the boundary bin of the histograms in `s`: the first whose counts (or masses) bring the
-// sum to `target`; target is at most the total.  Called by all threads.
+// sum to `target` (none where the total is less), and the total mass.  Called by all threads.
 template <int kThreads>
 __device__ __noinline__ void find_bin(Shared<kThreads> &s, bool by_mass, u64 target) {
     constexpr int kEach = kBins / kThreads;
@@ -296,7 +296,18 @@ __device__ __noinline__ void find_bin(Shared<kThreads> &s, bool by_mass, u64 tar
         cb += c[i];
         mb += m[i];
     }
+    if (t == kThreads - 1) s.mass_sum = mb;
     __syncthreads();
+}
+
+// The cut among `inside` elements of one key, of mass `in` together: the first so many of them.
+__device__ __forceinline__ Cut cut_of_one_key(uint32_t key, uint32_t inside, bool by_mass, u64 target, u64 before,
+                                              u64 above, u64 in, u64 *mass) {
+    const u64 w = in / inside;
+    u64 r = by_mass ? (w ? (target - above + w - 1) / w : inside) : target - before;
+    r = max((u64)1, min(r, (u64)inside));
+    *mass = above + r * w;
+    return Cut{key, r == inside ? 0xffffffffu : (uint32_t)r};
 }
 
 // Histograms of keys in [lo, hi], each of the bin of the last one that the boundary falls into, until
@@ -323,14 +334,7 @@ __device__ Cut cut_by_keys(Shared<kThreads> &s, uint32_t lo, uint32_t hi, bool b
             *mass = above + in;
             return Cut{low, 0xffffffffu};
         }
-        if (shift == 0) {
-            // All of one key: the first so many of them.
-            const u64 w = in / inside;
-            u64 r = by_mass ? (w ? (target - above + w - 1) / w : inside) : target - before;
-            r = max((u64)1, min(r, (u64)inside));
-            *mass = above + r * w;
-            return Cut{low, r == inside ? 0xffffffffu : (uint32_t)r};
-        }
+        if (shift == 0) return cut_of_one_key(low, inside, by_mass, target, before, above, in, mass);
         count0 = before;
         mass0 = above;
         hi = top;
@@ -338,13 +342,13 @@ __device__ Cut cut_by_keys(Shared<kThreads> &s, uint32_t lo, uint32_t hi, bool b
     }
 }
 
-// The cut at which the count (or, by_mass, the mass) of the prefix reaches `target` (at most the
-// total), over the elements that each(f) passes to f(logit), leaving out keys below `floor_key`.
-// *mass is the mass of the prefix, where `weigh`.  First a histogram of the distance to the maximum,
+// The cut at which the count (or, by_mass, the mass) of the prefix reaches `target`, over the elements
+// that each(f) passes to f(logit), leaving out keys below `floor_key`; *found is false where they have
+// less mass than that.  *mass is the mass of the prefix, where `weigh`.  First a histogram of the distance to the maximum,
 // in kBins - 1 steps over `range` powers of two and one for the rest.
 template <int kThreads, typename Each>
 __device__ Cut find_cut(Shared<kThreads> &s, const Scale &scale, float range, bool by_mass, bool weigh,
-                        u64 target, uint32_t floor_key, u64 *mass, Each each) {
+                        u64 target, uint32_t floor_key, u64 *mass, bool *found, Each each) {
     const float steps = (kBins - 1) / range;
     auto bin_of = [&](float l) { return min(kBins - 1, (int)(-scale.below(l) * steps)); };
     auto weight = [&](float l) { return weigh ? fixed_of(scale.mass(l)) : 0; };
@@ -394,11 +398,13 @@ __device__ Cut find_cut(Shared<kThreads> &s, const Scale &scale, float range, bo
     const int bin = s.bin;
     const uint32_t inside = s.inside, low = s.low[bin], high = s.high[bin];
     const u64 before = s.before, above = s.mass_before, in = s.mass_inside;
+    *found = !by_mass || target <= s.mass_sum;
     __syncthreads();
-    if (inside == 1 || (!by_mass && before + inside == target)) {
+    if (inside == 1 || !*found || (!by_mass && before + inside == target)) {
         *mass = above + in;
         return Cut{low, 0xffffffffu};
     }
+    if (low == high) return cut_of_one_key(low, inside, by_mass, target, before, above, in, mass);
     return cut_by_keys<kThreads>(s, low, high, by_mass, target, before, above, mass, [&](auto f) {
         each([&](float l) { f(logit_key(l), [&]() { return weight(l); }); });
     });
@@ -577,25 +583,23 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
     auto finish = [&](auto with_index, float range, u64 mass, u64 have) {
         auto each = [&](auto f) { with_index([&](float l, int) { f(l); }); };
         Cut cut = {0, 0xffffffffu};
+        bool found = true;
         if (by_k && have > (u64)asked)
-            cut = find_cut<kThreads>(s, scale, range, false, by_p, asked, 0, &mass, each);
+            cut = find_cut<kThreads>(s, scale, range, false, by_p, asked, 0, &mass, &found, each);
         if (by_p) {
-            // The mass that the elements at hand have: the cut lies among them, or not.
-            u64 all = mass;
-            if (!by_k || have <= (u64)asked) {
-                all = 0;
-                each([&](float l) { all += fixed_of(scale.mass(l)); });
-                all = block_sum<kThreads>(all, s.red);
-                if (by_k || mass == 0) mass = all;
+            if (mass == 0 || (by_k && have <= (u64)asked)) {
+                u64 mine = 0;
+                each([&](float l) { mine += fixed_of(scale.mass(l)); });
+                mass = block_sum<kThreads>(mine, s.red);
             }
             const u64 target = max((u64)1, (u64)fmax(ceil((double)top_p * (double)mass), 0.0));
-            if (target <= all) {
-                u64 unused;
-                const Cut at = find_cut<kThreads>(s, scale, range, true, true, target, cut.low, &unused, each);
+            u64 unused;
+            const Cut at = find_cut<kThreads>(s, scale, range, true, true, target, cut.low, &unused, &found, each);
+            // Less mass at hand: top-p's cut is below min_p's, or else below the list.
+            if (found)
                 cut = at.low == cut.low ? Cut{cut.low, min(cut.ties, at.ties)} : at;
-            } else if (!to_min) {
+            else if (!to_min)
                 return false;
-            }
         }
         // Of the ties at the cut the lowest indices: the highest complements.
         uint32_t low_index = 0;
