@@ -106,6 +106,21 @@ def test_flat_logits_by_blocks_a_row(rows, V, dtype):
     check(logits, noise, filters, tokens(logits, noise, filters, dtype))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("rows,V", [(1, 150001), (6, 20000), (40, 33333), (100, 9001), (260, 5003)])
+def test_cuts_below_the_list(rows, V, dtype):
+    """Cuts far from the maximum, where every block of a row searches its part, a mask in front, and
+    rows in between whose list will do."""
+    g = torch.Generator(device="cuda").manual_seed(V + 1)
+    logits = (torch.randn(rows, V, generator=g, device="cuda") * 3).to(DT[dtype])
+    logits[::3, :V // 3] = float("-inf")
+    noise = torch.empty(rows, V, device="cuda").exponential_(generator=g)
+    some = [(1.3, 0, 0.95, 0.0), (1.3, 999, 1.0, 0.0), (0.9, 3, 1.0, 0.0), (1.3, 3000, 0.9, 0.0),
+            (2.0, 0, 0.99, 1e-6), (2.5, 0, 1.0, 0.001), (1.5, V - 2, 1.0, 0.0), (1.1, 700, 0.8, 0.01)]
+    filters = [some[i % len(some)] if rows > 1 else some[0] for i in range(rows)]
+    check(logits, noise, filters, tokens(logits, noise, filters, dtype))
+
+
 def test_equal_scores_take_the_lowest_index():
     x = torch.zeros(4, 5000, device="cuda")
     noise = torch.full((4, 5000), 0.5, device="cuda")

@@ -12,8 +12,10 @@
 //   3. finds the cuts among the listed tokens, by a histogram of their distance to the maximum
 //      and, inside the bin that a cut falls into, histograms of their keys;
 //   4. races the kept ones: best w / noise, ties to the lowest index.
-// Where the list cannot hold the cuts (flat logits without min_p) the first block does 3 and 4 on
-// the whole row, which it reads again.
+// Where the list cannot hold the cuts (flat logits without min_p, or too many tokens near the maximum)
+// all blocks do 3 and 4 together, each on its part: every histogram is the sum of theirs, and each
+// races its own.  16 rows of 200000 fp32 logits, top-p 0.95 at temperature 1.3 (a fifth of the tokens stay):
+// 103 us, with 25000 logits a block read eight times; by one block of the row alone it took 420.
 //
 // Sums: a thread's masses are added in fp32 in a fixed order, everything beyond as integers in units of
 // 2^-35, and the list's order matters to nothing: equal inputs give equal tokens.  A bin's mass is
@@ -40,7 +42,7 @@ namespace {
 typedef unsigned long long u64;
 constexpr float kNegInf = -__builtin_inff();
 constexpr int kBins = 1024;
-constexpr int kListMax = 3072;
+constexpr int kListMax = 3000;
 constexpr float kListBits = 12.0f;    // tokens within 2^-12 of the maximum are listed
 constexpr int kMaxCluster = 8;
 constexpr int kStageBytes = 58 * 1024;  // most logits a block keeps in shared memory
@@ -110,6 +112,21 @@ struct Listed {
     uint32_t key, index;
 };
 constexpr int kLocalMax = 2048;      // tokens listed by one block
+constexpr uint32_t kSpoilt = 1u << 24;
+
+// The blocks that search together: one alone, or all of a cluster.
+struct Alone {
+    static constexpr int count = 1;
+    __device__ __forceinline__ void sync() const { __syncthreads(); }
+    template <typename S> __device__ __forceinline__ const S &of(S &s, int) const { return s; }
+};
+struct Together {
+    int count;
+    __device__ __forceinline__ void sync() const { cg::this_cluster().sync(); }
+    template <typename S> __device__ __forceinline__ const S &of(S &s, int r) const {
+        return *cg::this_cluster().map_shared_rank(&s, r);
+    }
+};
 
 // (A multiple of 16 bytes: the staged logits lie behind it.)
 template <int kThreads> struct __align__(16) Shared {
@@ -123,7 +140,7 @@ template <int kThreads> struct __align__(16) Shared {
     };
     // What a boundary search found: its bin and the counts and masses before and in it.
     uint32_t bin, before, inside;
-    u64 mass_before, mass_inside, mass_sum;
+    u64 mass_before, mass_inside, mass_sum, target;
     uint32_t rest, rest_low, rest_high;  // the last bin's count and keys
     u64 rest_mass;                       // and mass
     int locals;
@@ -131,7 +148,8 @@ template <int kThreads> struct __align__(16) Shared {
     uint32_t tops[kMaxCluster];
     u64 bests[kMaxCluster];
     u64 totals[kMaxCluster];             // mass of each part
-    int listed;                          // tokens listed
+    uint32_t listed;                     // tokens for the list, and kSpoilt for each block with too many
+    int wide;                            // the list does not do: all blocks go on
     Listed list[kListMax];
 };
 
@@ -247,22 +265,32 @@ template <int kThreads> __device__ __forceinline__ void add_to_bin(Shared<kThrea
     atomicAdd(&s.mass[2][bin], (uint32_t)(w >> 24));
 }
 
-// Finds the boundary bin of the histograms in `s`: the first whose counts (or masses) bring the
-// sum to `target` (none where the total is less), and the total mass.  Called by all threads.
-template <int kThreads>
-__device__ __noinline__ void find_bin(Shared<kThreads> &s, bool by_mass, u64 target) {
+// Finds the boundary bin of the peers' histograms together: the first whose counts (or masses)
+// bring the sum to `target`, or to that share of the total mass, and the total mass.  Without one (the
+// total is less) it is the last bin.  Called by all threads, whose histograms are complete.
+template <int kThreads, typename Peers>
+__device__ __noinline__ void find_bin(Shared<kThreads> &s, Peers peers, bool by_mass, bool weigh, u64 target,
+                                      float share) {
     constexpr int kEach = kBins / kThreads;
     static_assert(kBins % kThreads == 0, "bins");
     const int t = threadIdx.x, lane = t % 32, warp = t / 32;
-    u64 c[kEach], m[kEach], cs = 0, ms = 0;
+    u64 c[kEach] = {}, m[kEach] = {}, cs = 0, ms = 0;
+    for (int r = 0; r < peers.count; ++r) {
+        const Shared<kThreads> &o = peers.of(s, r);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            c[i] += o.count[t * kEach + i];
+            if (weigh)
+                m[i] += (u64)o.mass[0][t * kEach + i] + ((u64)o.mass[1][t * kEach + i] << 12) +
+                        ((u64)o.mass[2][t * kEach + i] << 24);
+        }
+    }
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-        c[i] = s.count[t * kEach + i];
-        m[i] = (u64)s.mass[0][t * kEach + i] + ((u64)s.mass[1][t * kEach + i] << 12) +
-               ((u64)s.mass[2][t * kEach + i] << 24);
         cs += c[i];
         ms += m[i];
     }
+    __syncwarp();
     u64 ci = cs, mi = ms;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
@@ -277,11 +305,17 @@ __device__ __noinline__ void find_bin(Shared<kThreads> &s, bool by_mass, u64 tar
         s.red[warp] = ci;
         s.red2[warp] = mi;
     }
+    if (t == 0) s.bin = kBins - 1;
     __syncthreads();
     u64 cb = ci - cs, mb = mi - ms;
     for (int i = 0; i < warp; ++i) {
         cb += s.red[i];
         mb += s.red2[i];
+    }
+    if (share > 0.0f) {
+        u64 all = 0;
+        for (int i = 0; i < kThreads / 32; ++i) all += s.red2[i];
+        target = max((u64)1, (u64)ceil((double)share * (double)all));
     }
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
@@ -296,7 +330,10 @@ __device__ __noinline__ void find_bin(Shared<kThreads> &s, bool by_mass, u64 tar
         cb += c[i];
         mb += m[i];
     }
-    if (t == kThreads - 1) s.mass_sum = mb;
+    if (t == kThreads - 1) {
+        s.mass_sum = mb;
+        s.target = target;
+    }
     __syncthreads();
 }
 
@@ -312,10 +349,10 @@ __device__ __forceinline__ Cut cut_of_one_key(uint32_t key, uint32_t inside, boo
 
 // Histograms of keys in [lo, hi], each of the bin of the last one that the boundary falls into, until
 // that holds one key, one element, or is kept whole.  each(f) calls f(key, weight()) of every
-// element; count0 and mass0 are of the elements above hi.
-template <int kThreads, typename Each>
-__device__ Cut cut_by_keys(Shared<kThreads> &s, uint32_t lo, uint32_t hi, bool by_mass, u64 target,
-                           u64 count0, u64 mass0, u64 *mass, Each each) {
+// element that this block has; count0 and mass0 are of the elements above hi.
+template <int kThreads, typename Peers, typename Each>
+__device__ Cut cut_by_keys(Shared<kThreads> &s, Peers peers, uint32_t lo, uint32_t hi, bool by_mass, bool weigh,
+                           u64 target, u64 count0, u64 mass0, u64 *mass, Each each) {
     for (;;) {
         const int shift = max(0, 32 - __clz(hi - lo) - 10);
         clear_bins(s);
@@ -323,11 +360,11 @@ __device__ Cut cut_by_keys(Shared<kThreads> &s, uint32_t lo, uint32_t hi, bool b
         each([&](uint32_t key, auto weight) {
             if (key >= lo && key <= hi) add_to_bin(s, (int)((hi - key) >> shift), weight());
         });
-        __syncthreads();
-        find_bin<kThreads>(s, by_mass, target - (by_mass ? mass0 : count0));
+        peers.sync();
+        find_bin<kThreads>(s, peers, by_mass, weigh, target - (by_mass ? mass0 : count0), 0.0f);
         const uint32_t bin = s.bin, inside = s.inside;
         const u64 before = count0 + s.before, above = mass0 + s.mass_before, in = s.mass_inside;
-        __syncthreads();
+        peers.sync();
         const uint32_t top = hi - (bin << shift);
         const uint32_t low = top - lo < (1u << shift) ? lo : top - ((1u << shift) - 1);
         if (inside == 1 || (!by_mass && before + inside == target)) {
@@ -342,13 +379,14 @@ __device__ Cut cut_by_keys(Shared<kThreads> &s, uint32_t lo, uint32_t hi, bool b
     }
 }
 
-// The cut at which the count (or, by_mass, the mass) of the prefix reaches `target`, over the elements
-// that each(f) passes to f(logit), leaving out keys below `floor_key`; *found is false where they have
-// less mass than that.  *mass is the mass of the prefix, where `weigh`.  First a histogram of the distance to the maximum,
-// in kBins - 1 steps over `range` powers of two and one for the rest.
-template <int kThreads, typename Each>
-__device__ Cut find_cut(Shared<kThreads> &s, const Scale &scale, float range, bool by_mass, bool weigh,
-                        u64 target, uint32_t floor_key, u64 *mass, bool *found, Each each) {
+// The cut at which the count (or, by_mass, the mass) of the prefix reaches `target`, or `share` of the
+// total mass, over the elements that each(key, f) passes to f(logit) in the peers' blocks (those below the key need not be), leaving out keys
+// below `floor_key`; *found is false where they have less mass than that.  *mass is the mass of the
+// prefix, where `weigh`.  First a histogram of the distance to the maximum, in kBins - 1 steps over
+// `range` powers of two and one for the rest.
+template <int kThreads, typename Peers, typename Each>
+__device__ Cut find_cut(Shared<kThreads> &s, Peers peers, const Scale &scale, float range, bool by_mass, bool weigh,
+                        u64 target, float share, uint32_t floor_key, u64 *mass, bool *found, Each each) {
     const float steps = (kBins - 1) / range;
     auto bin_of = [&](float l) { return min(kBins - 1, (int)(-scale.below(l) * steps)); };
     auto weight = [&](float l) { return weigh ? fixed_of(scale.mass(l)) : 0; };
@@ -361,7 +399,7 @@ __device__ Cut find_cut(Shared<kThreads> &s, const Scale &scale, float range, bo
     __syncthreads();
     uint32_t rest = 0, rest_low = 0xffffffffu, rest_high = 0;
     u64 rest_mass = 0;
-    each([&](float l) {
+    each(max(floor_key, logit_key(kNegInf)), [&](float l) {
         const uint32_t key = logit_key(l);
         if (key < floor_key) return;
         const int bin = bin_of(l);
@@ -393,21 +431,159 @@ __device__ Cut find_cut(Shared<kThreads> &s, const Scale &scale, float range, bo
         s.low[kBins - 1] = s.rest_low;
         s.high[kBins - 1] = s.rest_high;
     }
-    __syncthreads();
-    find_bin<kThreads>(s, by_mass, target);
+    peers.sync();
+    find_bin<kThreads>(s, peers, by_mass, weigh, target, share);
     const int bin = s.bin;
-    const uint32_t inside = s.inside, low = s.low[bin], high = s.high[bin];
+    uint32_t low = 0xffffffffu, high = 0;
+    for (int r = 0; r < peers.count; ++r) {
+        low = min(low, peers.of(s, r).low[bin]);
+        high = max(high, peers.of(s, r).high[bin]);
+    }
+    const uint32_t inside = s.inside;
     const u64 before = s.before, above = s.mass_before, in = s.mass_inside;
+    target = s.target;
     *found = !by_mass || target <= s.mass_sum;
-    __syncthreads();
-    if (inside == 1 || !*found || (!by_mass && before + inside == target)) {
+    peers.sync();
+    if (!*found) return Cut{0, 0xffffffffu};
+    if (inside == 1 || (!by_mass && before + inside == target)) {
         *mass = above + in;
         return Cut{low, 0xffffffffu};
     }
     if (low == high) return cut_of_one_key(low, inside, by_mass, target, before, above, in, mass);
-    return cut_by_keys<kThreads>(s, low, high, by_mass, target, before, above, mass, [&](auto f) {
-        each([&](float l) { f(logit_key(l), [&]() { return weight(l); }); });
+    return cut_by_keys<kThreads>(s, peers, low, high, by_mass, weigh, target, before, above, mass, [&](auto f) {
+        each(low, [&](float l) { f(logit_key(l), [&]() { return weight(l); }); });
     });
+}
+
+// What is asked of a row whose maximum is m: by_min holds by itself.
+struct Query {
+    const float *noise;
+    float m, c, T, min_p, top_p;
+    int asked, V;
+    bool by_k, by_p, to_min;
+    // N tokens race, those whose `keep` is set.  All numbers are asked for before the first is used
+    // (token 0's for those that are out: loads behind a condition would wait for one another).
+    template <int N>
+    __device__ __forceinline__ void race(Best &best, const float (&l)[N], const int (&index)[N],
+                                         const bool (&keep)[N]) const {
+        float e[N];
+#pragma unroll
+        for (int x = 0; x < N; ++x) e[x] = __ldg(noise + (keep[x] ? index[x] : 0));
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+            if (!keep[x]) continue;
+            const float w = weight_of(l[x], m, T);
+            if (w >= min_p) best.offer(w / fmaxf(e[x], 1.17549435e-38f), index[x]);
+        }
+    }
+};
+
+// The cuts and the race among the peers' `have` tokens, whose logits and indices with_index(least, f)
+// passes to f(logit, index); it may leave out logits below `least`.  mass: of which top-p takes its share, where that is not the mass of these tokens
+// (0).  race(least, keep) has those race for which keep(logit, index) holds.  False where they do not
+// hold top-p's cut, unless nothing below them is kept.
+template <int kThreads, typename Peers, typename WithIndex, typename Race>
+__device__ __forceinline__ bool choose(Shared<kThreads> &s, Peers peers, const Query &q, float range, u64 mass,
+                                       u64 have, WithIndex with_index, Race race) {
+    const Scale scale = {q.m, q.c};
+    auto each = [&](uint32_t least, auto f) { with_index(key_logit(least), [&](float l, int) { f(l); }); };
+    Cut cut = {0, 0xffffffffu};
+    bool found = true;
+    if (q.by_k && have > (u64)q.asked)
+        cut = find_cut<kThreads>(s, peers, scale, range, false, q.by_p, q.asked, 0.0f, 0, &mass, &found, each);
+    if (q.by_p) {
+        const u64 target = max((u64)1, (u64)fmax(ceil((double)q.top_p * (double)mass), 0.0));
+        u64 unused;
+        const Cut at = find_cut<kThreads>(s, peers, scale, range, true, true, target,
+                                          mass ? 0.0f : fmaxf(q.top_p, 1e-30f), cut.low, &unused, &found, each);
+        // Less mass at hand: top-p's cut is below min_p's, or else below the list.
+        if (found)
+            cut = at.low == cut.low ? Cut{cut.low, min(cut.ties, at.ties)} : at;
+        else if (!q.to_min)
+            return false;
+    }
+    // Of the ties at the cut the lowest indices: the highest complements.
+    uint32_t low_index = 0;
+    if (cut.ties != 0xffffffffu) {
+        u64 unused;
+        low_index = cut_by_keys<kThreads>(s, peers, ~(uint32_t)(q.V - 1), 0xffffffffu, false, false, cut.ties, 0, 0,
+                                          &unused, [&](auto f) {
+            with_index(key_logit(cut.low), [&](float l, int i) {
+                if (logit_key(l) == cut.low) f(~(uint32_t)i, []() { return (u64)0; });
+            });
+        }).low;
+    }
+    race(cut.low ? key_logit(cut.low) : kNegInf, [&](float l, int i) {
+        const uint32_t k = logit_key(l);
+        return l > kNegInf && (k > cut.low || (k == cut.low && ~(uint32_t)i >= low_index));
+    });
+    return true;
+}
+
+// f(vector, v) of a part's vectors in memory, four under way at a time.
+template <int kThreads, typename T, typename F>
+__device__ __forceinline__ void from_memory(const Part<T> &q, F f) {
+    const int t = threadIdx.x, all = q.vecs();
+#pragma unroll 1
+    for (int v0 = t; v0 < all + t; v0 += 4 * kThreads) {
+        uint4 u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[i] = q.load(min(v0 + i * kThreads, all - 1));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (v0 + i * kThreads < all) f(u[i], v0 + i * kThreads);
+    }
+}
+// f(vector, index of its first element) of the part, from shared memory where it is kept there.
+template <int kThreads, bool kStaged, typename T, typename F>
+__device__ __forceinline__ void each_vector(const Part<T> &part, const uint4 *copy, F f) {
+    if (kStaged) {
+        const int vecs = part.vecs();
+#pragma unroll 2
+        for (int v = threadIdx.x; v < vecs; v += kThreads) f(copy[v], part.index(v));
+    } else {
+        from_memory<kThreads>(part, [&](const uint4 &u, int v) { f(u, part.index(v)); });
+    }
+}
+
+// Every block's best in its part, where the list does not do: `near`, the cuts are known to be among
+// the tokens down to `edge`.  (Over 30 powers of two; scales that overflow take the histograms of
+// keys.)
+template <typename T, int kThreads, bool kStaged, typename Peers>
+__device__ __forceinline__ u64 choose_from_all(Shared<kThreads> &s, Peers peers, const Query &q, const Part<T> &part,
+                                               const uint4 *copy, bool near, float edge, u64 total, uint32_t n) {
+    Best best;
+    constexpr int kVec = Part<T>::kVec;
+    auto on = [&](float l) { return !near || (l - q.m) * q.c >= -edge; };
+    auto vectors = [&](float least, auto f) {
+        each_vector<kThreads, kStaged>(part, copy, [&](const uint4 &u, int index) {
+            const float top = max_of(u, T());
+            if (top < least || (near && !on(top))) return;
+            float e[kVec];
+            unpack(u, e, T());
+            f(e, index);
+        });
+    };
+    choose<kThreads>(s, peers, q, near ? edge * 1.001f : 30.0f, near && !q.by_k ? total : 0, near ? n : q.V,
+                     [&](float least, auto f) {
+        vectors(least, [&](const float (&e)[kVec], int index) {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+                if (on(e[i])) f(fmaxf(e[i], kNegInf), index + i);
+        });
+    }, [&](float least, auto keep) {
+        vectors(least, [&](const float (&e)[kVec], int index) {
+            int at[kVec];
+            bool in[kVec];
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                at[i] = index + i;
+                in[i] = e[i] >= least && on(e[i]) && keep(e[i], index + i);
+            }
+            q.race(best, e, at, in);
+        });
+    });
+    return best.packed();
 }
 
 // kStaged: a block's part of a row fits shared memory.
@@ -448,21 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
     uint4 *const copy = reinterpret_cast<uint4 *>(dynamic + sizeof(Shared<kThreads>));
     float top_here = kNegInf, mass = 0.0f;
     const bool with_mass = by_p && !first_only;
-    const int vecs = part.vecs();
-    // f(vector, v) of a part's vectors in memory, four under way at a time.
-    auto from_memory = [&](const Part<T> &q, auto f) {
-        const int all = q.vecs();
-#pragma unroll 1
-        for (int v0 = t; v0 < all + t; v0 += 4 * kThreads) {
-            uint4 u[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) u[i] = q.load(min(v0 + i * kThreads, all - 1));
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (v0 + i * kThreads < all) f(u[i], v0 + i * kThreads);
-        }
-    };
-    from_memory(part, [&](const uint4 &u, int v) {
+    from_memory<kThreads>(part, [&](const uint4 &u, int v) {
         if (kStaged) copy[v] = u;
         const float top = fmaxf(max_of(u, T()), kNegInf);
         if (with_mass && top > kNegInf) {
@@ -475,23 +637,6 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
         }
         top_here = fmaxf(top_here, top);
     });
-    // f(vector, index of its first element), and f(logit, index), of the part.
-    auto each_vector = [&](auto f) {
-        if (kStaged) {
-#pragma unroll 2
-            for (int v = t; v < vecs; v += kThreads) f(copy[v], part.index(v));
-        } else {
-            from_memory(part, [&](const uint4 &u, int v) { f(u, part.index(v)); });
-        }
-    };
-    auto each_of = [&](auto vectors, auto f) {
-        vectors([&](const uint4 &u, int index) {
-            float e[kVec];
-            unpack(u, e, T());
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) f(e[i], index + i);
-        });
-    };
     uint32_t top_key = (uint32_t)block_max<kThreads>(logit_key(top_here), s.red);
     if (C > 1) {
         if (t < C) cluster.map_shared_rank(&s, t)->tops[rank] = top_key;
@@ -514,19 +659,23 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
     };
     const float m = key_logit(top_key);
     const bool greedy = first_only || m == kNegInf;
+    Query q = {noise, m, c, T_, min_p, top_p, asked, V, by_k, by_p, false};
     Best best;
-    auto race = [&](float l, int i) {
-        best.offer(weight_of(l, m, T_) / fmaxf(__ldg(noise + i), 1.17549435e-38f), i);
-    };
     if (greedy || !(by_k || by_p || by_min)) {
-        if (greedy)
-            each_of(each_vector, [&](float l, int i) {
-                if (l == m) best.offer(0.0f, i);
-            });
-        else
-            each_of(each_vector, [&](float l, int i) {
-                if (l > kNegInf) race(l, i);
-            });
+        each_vector<kThreads, kStaged>(part, copy, [&](const uint4 &u, int index) {
+            if (greedy && !(max_of(u, T()) >= m)) return;
+            float e[kVec];
+            int at[kVec];
+            bool in[kVec];
+            unpack(u, e, T());
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                at[i] = index + i;
+                in[i] = e[i] > kNegInf;
+                if (greedy && e[i] == m) best.offer(0.0f, index + i);
+            }
+            if (!greedy) q.race(best, e, at, in);
+        });
         u64 mine = block_max<kThreads>(best.packed(), s.red);
         if (t == 0) lead->bests[rank] = mine;
         if (!hand_over()) return;
@@ -539,13 +688,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
 
     // 2. The mass and the list, in powers of two.  The list's edge lies a little below min_p's; with
     // top-k and top-p it is the far one, since top-p's share is of all the top-k tokens' mass.
-    const Scale scale = {m, c};
     const float far = -log2f(min_p) * 1.00001f + 1e-4f;
     const bool to_min = by_min && far < kListBits && !(by_k && by_p);   // nothing below the list is kept
     const float edge = to_min ? far : kListBits;
     const bool usable = m < __builtin_inff() && c < __builtin_inff();
     if (usable) {
-        each_vector([&](const uint4 &u, int index) {
+        each_vector<kThreads, kStaged>(part, copy, [&](const uint4 &u, int index) {
             if (!((max_of(u, T()) - m) * c >= -edge)) return;
             float e[kVec];
             unpack(u, e, T());
@@ -567,79 +715,60 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
         }
         // This block's tokens to the first block's list; one that has too many spoils the list.
         __syncthreads();
-        const int n = s.locals;
-        if (t == 0) s.bin = atomicAdd(&lead->listed, n > kLocalMax ? kListMax + 1 : n);
+        const uint32_t n = s.locals;
+        if (t == 0) s.bin = atomicAdd(&lead->listed, n + (n > kLocalMax ? kSpoilt : 0)) % kSpoilt;
         __syncthreads();
-        for (int i = t; i < min(n, kLocalMax); i += kThreads)
+        for (int i = t; i < min(n, (uint32_t)kLocalMax); i += kThreads)
             if (s.bin + i < kListMax) lead->list[s.bin + i] = s.local[i];
     }
-    if (!hand_over()) return;
+    if (C > 1) cluster.sync(); else __syncthreads();
 
-    // 3. The cuts.  `each` passes the logits of the list, or of the row, and with_index the indices
-    // too.
-    const int n = s.listed;
     u64 total = 0;
-    for (int i = 0; by_p && usable && i < C; ++i) total += s.totals[i];
-    auto finish = [&](auto with_index, float range, u64 mass, u64 have) {
-        auto each = [&](auto f) { with_index([&](float l, int) { f(l); }); };
-        Cut cut = {0, 0xffffffffu};
-        bool found = true;
-        if (by_k && have > (u64)asked)
-            cut = find_cut<kThreads>(s, scale, range, false, by_p, asked, 0, &mass, &found, each);
-        if (by_p) {
-            if (mass == 0 || (by_k && have <= (u64)asked)) {
-                u64 mine = 0;
-                each([&](float l) { mine += fixed_of(scale.mass(l)); });
-                mass = block_sum<kThreads>(mine, s.red);
-            }
-            const u64 target = max((u64)1, (u64)fmax(ceil((double)top_p * (double)mass), 0.0));
-            u64 unused;
-            const Cut at = find_cut<kThreads>(s, scale, range, true, true, target, cut.low, &unused, &found, each);
-            // Less mass at hand: top-p's cut is below min_p's, or else below the list.
-            if (found)
-                cut = at.low == cut.low ? Cut{cut.low, min(cut.ties, at.ties)} : at;
-            else if (!to_min)
-                return false;
-        }
-        // Of the ties at the cut the lowest indices: the highest complements.
-        uint32_t low_index = 0;
-        if (cut.ties != 0xffffffffu) {
-            u64 unused;
-            low_index = cut_by_keys<kThreads>(s, ~(uint32_t)(V - 1), 0xffffffffu, false, cut.ties, 0, 0, &unused,
-                                              [&](auto f) {
-                with_index([&](float l, int i) {
-                    if (logit_key(l) == cut.low) f(~(uint32_t)i, []() { return (u64)0; });
-                });
-            }).low;
-        }
-        // 4. The race.
-        with_index([&](float l, int i) {
-            const uint32_t k = logit_key(l);
-            if (k < cut.low || (k == cut.low && ~(uint32_t)i < low_index) || l == kNegInf) return;
-            if (weight_of(l, m, T_) >= min_p) race(l, i);
-        });
-        const u64 won = block_max<kThreads>(best.packed(), s.red);
-        if (t == 0) p.tokens[row] = (int64_t)(uint32_t)~(uint32_t)won;
-        return true;
-    };
-    // The list holds the cuts if top-k's is inside; top-p's is looked for.
-    if (usable && n <= kListMax && (by_k ? n >= asked || (to_min && !by_p) : by_p || to_min) &&
-        finish([&](auto f) {
+    const Shared<kThreads> &told = rank == 0 ? s : *lead;
+    for (int i = 0; by_p && usable && i < C; ++i) total += told.totals[i];
+    const uint32_t listed = told.listed, n = listed % kSpoilt;
+    // 3. and 4.  The list holds the cuts if top-k's is inside; top-p's is looked for.
+    q.to_min = to_min;
+    const bool near = usable && (by_k ? n >= asked || (to_min && !by_p) : to_min);
+    bool done = false;
+    if (rank == 0 && usable && listed <= kListMax && (near || (by_p && !by_k)))
+        done = choose<kThreads>(s, Alone(), q, edge * 1.001f, by_k ? 0 : total, n, [&](float, auto f) {
             for (int i = t; i < n; i += kThreads) f(key_logit(s.list[i].key), (int)s.list[i].index);
-        }, edge * 1.001f, total, n))
-        return;
-    __syncthreads();
-    const Part<T> whole = part_of(0, V);
-    auto whole_vectors = [&](auto f) {
-        if (C == 1)
-            each_vector(f);
-        else
-            from_memory(whole, [&](const uint4 &u, int v) { f(u, whole.index(v)); });
-    };
-    // A histogram over 30 powers of two; temperatures that overflow the scale take key histograms.
-    finish([&](auto f) {
-        each_of(whole_vectors, [&](float l, int i) { f(fmaxf(l, kNegInf), i); });
-    }, 30.0f, 0, V);
+        }, [&](float, auto keep) {
+            constexpr int kEach = 4;
+            for (int i0 = t; i0 < n; i0 += kEach * kThreads) {
+                float l[kEach];
+                int at[kEach];
+                bool in[kEach];
+#pragma unroll
+                for (int x = 0; x < kEach; ++x) {
+                    const Listed &item = s.list[min(i0 + x * kThreads, (int)n - 1)];
+                    l[x] = key_logit(item.key);
+                    at[x] = (int)item.index;
+                    in[x] = i0 + x * kThreads < n && keep(l[x], at[x]);
+                }
+                q.race(best, l, at, in);
+            }
+        });
+    if (C > 1) {
+        if (rank == 0 && t < C) cluster.map_shared_rank(&s, t)->wide = !done;
+        asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+        if (!done || rank != 0) {
+            asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+            if (!s.wide) return;
+        }
+    }
+    u64 won = best.packed();
+    if (!done)
+        won = C > 1 ? choose_from_all<T, kThreads, kStaged>(s, Together{C}, q, part, copy, near, edge, total, n)
+                    : choose_from_all<T, kThreads, kStaged>(s, Alone(), q, part, copy, near, edge, total, n);
+    won = block_max<kThreads>(won, s.red);
+    if (!done && C > 1) {
+        if (t == 0) lead->bests[rank] = won;
+        if (!hand_over()) return;
+        for (int i = 0; i < C; ++i) won = max(won, s.bests[i]);
+    }
+    if (t == 0) p.tokens[row] = (int64_t)(uint32_t)~(uint32_t)won;
 }
 
 template <typename T, int kThreads, bool kStaged>
