@@ -635,8 +635,8 @@ void ctr_attn_destroy(ctr_attn_t plan);
  * and the token is the kept one with the largest w_i / max(noise_i, FLT_MIN) (ties: the lowest
  * index).  With independent Exp(1) numbers as noise this is a draw from the kept tokens in
  * proportion to w (the exponential race).  A token with l_i = -inf is never drawn; a row
- * of nothing else gives -1.  Masses are summed in 64-bit fixed point, so the kept set does
- * not depend on the order of summation.
+ * of nothing else gives -1.  Masses are added in a fixed order in fp32 within a thread and as
+ * 64-bit integers (units of 2^-35) beyond it, so the kept set does not depend on timing.
  *
  *   logits   [rows][vocab] in the plan's dtype, row stride in elements (any, >= vocab)
  *   noise    [rows][vocab] fp32, row stride in elements

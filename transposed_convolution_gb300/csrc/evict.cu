@@ -4,7 +4,7 @@
 // in shared memory where they fit, finds the lowest key that stays by three histograms (11, 11
 // and 10 bits), and lists the kept slots in order: counts by warp, their sum, and the list, which
 // takes a ballot for each 32 slots.  Few long sequences are spread over clusters of blocks, which add up
-// their histograms (32767 slots of 16 heads: 24 us in 16 blocks).  The second copies the listed rows; it moves
+// their histograms (32767 slots of 16 heads: 24 us in 16 blocks, 16 in 64).  The second copies the listed rows; it moves
 // 4 D elements a row and is bound by the cache's memory, so its blocks are many and small, each
 // with the row addresses of 64 rows in shared memory and two 16-byte loads of K and V under way
 // for each thread at a time.  It is launched while the first still runs, and waits for its end.

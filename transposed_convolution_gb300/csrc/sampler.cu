@@ -802,7 +802,7 @@ template <typename T>
 cudaError_t launch(const ctr_sampler_s *pl, SampleParams p, cudaStream_t st) {
     // Blocks a row: two an SM for few rows, but at least 4096 elements each.  A part that does not
     // fit shared memory is read again from L2: 256 rows of 100003 16-bit logits, one block a row, take
-    // 30 us, and in clusters of four, whose parts fit but whose blocks wait for one another, 42.
+    // 33 us, and in clusters of four, whose parts fit but whose blocks wait for one another, 42.
     int cluster = 1;
     const int rows = (int)pl->rows;
     while (cluster < kMaxCluster && (int64_t)rows * cluster <= pl->num_sms && p.vocab >= 4096 * 2 * cluster)
