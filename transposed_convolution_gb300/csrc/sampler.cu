@@ -15,7 +15,7 @@
 // Where the list cannot hold the cuts (flat logits without min_p, or too many tokens near the maximum)
 // all blocks do 3 and 4 together, each on its part: every histogram is the sum of theirs, and each
 // races its own.  16 rows of 200000 fp32 logits, top-p 0.95 at temperature 1.3 (a fifth of the tokens stay):
-// 103 us, with 25000 logits a block read eight times; by one block of the row alone it took 420.
+// 108 us, with 25000 logits a block gone over eight times; by one block of the row alone 420.
 //
 // Sums: a thread's masses are added in fp32 in a fixed order, everything beyond as integers in units of
 // 2^-35, and the list's order matters to nothing: equal inputs give equal tokens.  A bin's mass is
@@ -45,7 +45,8 @@ constexpr int kBins = 1024;
 constexpr int kListMax = 3000;
 constexpr float kListBits = 12.0f;    // tokens within 2^-12 of the maximum are listed
 constexpr int kMaxCluster = 8;
-constexpr int kStageBytes = 58 * 1024;  // most logits a block keeps in shared memory
+// Most logits a block keeps in shared memory, two blocks an SM, and one.
+constexpr int kStageBytes = 58 * 1024, kStageBytesAlone = 160 * 1024;
 
 struct SampleParams {
     const void *logits;
@@ -275,6 +276,7 @@ __device__ __noinline__ void find_bin(Shared<kThreads> &s, Peers peers, bool by_
     static_assert(kBins % kThreads == 0, "bins");
     const int t = threadIdx.x, lane = t % 32, warp = t / 32;
     u64 c[kEach] = {}, m[kEach] = {}, cs = 0, ms = 0;
+#pragma unroll 4
     for (int r = 0; r < peers.count; ++r) {
         const Shared<kThreads> &o = peers.of(s, r);
 #pragma unroll
@@ -435,6 +437,7 @@ __device__ Cut find_cut(Shared<kThreads> &s, Peers peers, const Scale &scale, fl
     find_bin<kThreads>(s, peers, by_mass, weigh, target, share);
     const int bin = s.bin;
     uint32_t low = 0xffffffffu, high = 0;
+#pragma unroll 4
     for (int r = 0; r < peers.count; ++r) {
         low = min(low, peers.of(s, r).low[bin]);
         high = max(high, peers.of(s, r).high[bin]);
@@ -778,7 +781,7 @@ cudaError_t launch(const SampleParams &p, int rows, int cluster, cudaStream_t st
     static PerDeviceOnce once;
     const cudaError_t e = once.run(current_device(), cudaSuccess, [&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)sizeof(Shared<kThreads>) + kStageBytes + 32);
+                                    (int)sizeof(Shared<kThreads>) + kStageBytesAlone + 32);
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -809,8 +812,12 @@ cudaError_t launch(const ctr_sampler_s *pl, SampleParams p, cudaStream_t st) {
         cluster *= 2;
     p.chunk = ((p.vocab + cluster - 1) / cluster + 15) / 16 * 16;
     if (p.chunk <= 4096) return launch<T, 256, true>(p, rows, cluster, st);
-    return (size_t)p.chunk * sizeof(T) <= kStageBytes ? launch<T, 512, true>(p, rows, cluster, st)
-                                                      : launch<T, 512, false>(p, rows, cluster, st);
+    // Where every block has an SM to itself more of a row fits: 1 row of 131072 fp32 logits, top-k 50, takes
+    // 30 us so and 39 from L2.
+    const bool alone = (int64_t)rows * cluster <= pl->num_sms;
+    return (size_t)p.chunk * sizeof(T) <= (alone ? kStageBytesAlone : kStageBytes)
+               ? launch<T, 512, true>(p, rows, cluster, st)
+               : launch<T, 512, false>(p, rows, cluster, st);
 }
 
 }  // namespace
