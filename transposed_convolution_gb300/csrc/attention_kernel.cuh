@@ -627,8 +627,9 @@ __global__ void __launch_bounds__(32 * C::Shape::kWarps, C::Shape::kPerSm) atten
     // Offsets of rows in the pages, in sixteens of elements: a plan's pages have fewer than 2^32.
     const uint32_t page16 = (uint32_t)(p.cache.page_stride / 16), head16 = (uint32_t)(p.cache.head_stride / 16),
                    row16 = (uint32_t)(p.cache.row_stride / 16);
-    const T *const k_col = static_cast<const T *>(p.k) + col * kChunk, *const k_lane = k_col + row0 * p.cache.row_stride;
-    const T *const v_col = static_cast<const T *>(p.v) + col * kChunk, *const v_lane = v_col + row0 * p.cache.row_stride;
+    const T *const k_col = static_cast<const T *>(p.k) + col * kChunk;
+    const T *const v_col = static_cast<const T *>(p.v) + col * kChunk;
+    const T *const k_lane = k_col + row0 * p.cache.row_stride, *const v_lane = v_col + row0 * p.cache.row_stride;
     const int64_t row_step = kRows * p.cache.row_stride;
     const uint32_t k_dst = ptx::smem_u32(ring) + row0 * k_pitch + col * 16;
     const uint32_t v_dst = ptx::smem_u32(ring) + 16 * k_pitch + row0 * v_pitch + col * 16;

@@ -4,10 +4,11 @@
 // in shared memory where they fit, finds the lowest key that stays by three histograms (11, 11
 // and 10 bits), and lists the kept slots in order: counts by warp, their sum, and the list, which
 // takes a ballot for each 32 slots.  Few long sequences are spread over clusters of blocks, which add up
-// their histograms (32767 slots of 16 heads: 24 us in 16 blocks, 16 in 64).  The second copies the listed rows; it moves
-// 4 D elements a row and is bound by the cache's memory, so its blocks are many and small, each
-// with the row addresses of 64 rows in shared memory and two 16-byte loads of K and V under way
-// for each thread at a time.  It is launched while the first still runs, and waits for its end.
+// their histograms (32767 slots of 16 heads: 24 us in 16 blocks, 16 in 64).  The second copies the
+// listed rows; it moves 4 D elements a row and is bound by the cache's memory, so its blocks are many
+// and small, each with the row addresses of 64 rows in shared memory and two 16-byte loads of K and
+// V under way for each thread at a time.  It is launched while the first still runs, and waits for
+// its end.
 #include <algorithm>
 #include <cooperative_groups.h>
 
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(EvictParams p, i
     // The list: each warp takes a run of the block's slots.
     const int run = ((last - first + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
     const int from = min(first + warp * run, last), to = min(from + run, last);
-    auto judge = [&](int j, bool *on, bool *eq) {
+    auto decide = [&](int j, bool *on, bool *eq) {
         *on = *eq = false;
         if (j >= to) return;
         *on = j < s0 || j >= r0 || all;
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(EvictParams p, i
     int sure = 0, equal = 0;
     for (int base = from; base < to; base += 32) {
         bool on, eq;
-        judge(base + lane, &on, &eq);
+        decide(base + lane, &on, &eq);
         sure += __popc(__ballot_sync(0xffffffffu, on));
         equal += __popc(__ballot_sync(0xffffffffu, eq));
     }
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(EvictParams p, i
     const unsigned below = (1u << lane) - 1;
     for (int base = from; base < to; base += 32) {
         bool on, eq;
-        judge(base + lane, &on, &eq);
+        decide(base + lane, &on, &eq);
         const unsigned be = __ballot_sync(0xffffffffu, eq);
         if (eq && tie + __popc(be & below) < ties) on = true;
         tie += __popc(be);

@@ -8,14 +8,14 @@
 // exponential while the memory is busy.  A row's block (or cluster of blocks)
 //   1. reads its part into shared memory, where it fits, and takes the maximum and the mass;
 //   2. lists the tokens within 2^-kListBits of the maximum (or min_p of it: nothing below is kept
-//      then) at the cluster's first block; the others are done;
+//      then) at the cluster's first block; the others wait;
 //   3. finds the cuts among the listed tokens, by a histogram of their distance to the maximum
 //      and, inside the bin that a cut falls into, histograms of their keys;
 //   4. races the kept ones: best w / noise, ties to the lowest index.
 // Where the list cannot hold the cuts (flat logits without min_p, or too many tokens near the maximum)
 // all blocks do 3 and 4 together, each on its part: every histogram is the sum of theirs, and each
-// races its own.  16 rows of 200000 fp32 logits, top-p 0.95 at temperature 1.3 (a fifth of the tokens stay):
-// 108 us, with 25000 logits a block gone over eight times; by one block of the row alone 420.
+// races its own.  16 rows of 200000 fp32 logits, top-p 0.95 at temperature 1.3 (a fifth of the tokens
+// stays): 108 us, with 25000 logits a block gone over eight times; by one block of the row alone 420.
 //
 // Sums: a thread's masses are added in fp32 in a fixed order, everything beyond as integers in units of
 // 2^-35, and the list's order matters to nothing: equal inputs give equal tokens.  A bin's mass is
@@ -382,10 +382,10 @@ __device__ Cut cut_by_keys(Shared<kThreads> &s, Peers peers, uint32_t lo, uint32
 }
 
 // The cut at which the count (or, by_mass, the mass) of the prefix reaches `target`, or `share` of the
-// total mass, over the elements that each(key, f) passes to f(logit) in the peers' blocks (those below the key need not be), leaving out keys
-// below `floor_key`; *found is false where they have less mass than that.  *mass is the mass of the
-// prefix, where `weigh`.  First a histogram of the distance to the maximum, in kBins - 1 steps over
-// `range` powers of two and one for the rest.
+// total mass, over the elements that each(key, f) passes to f(logit) in the peers' blocks (it may leave
+// out those below the key), without those whose keys are below `floor_key`; *found is false where they
+// have less mass than that.  *mass is the mass of the prefix, where `weigh`.  First a histogram of the
+// distance to the maximum, in kBins - 1 steps over `range` powers of two and one for the rest.
 template <int kThreads, typename Peers, typename Each>
 __device__ Cut find_cut(Shared<kThreads> &s, Peers peers, const Scale &scale, float range, bool by_mass, bool weigh,
                         u64 target, float share, uint32_t floor_key, u64 *mass, bool *found, Each each) {
@@ -481,10 +481,11 @@ struct Query {
     }
 };
 
-// The cuts and the race among the peers' `have` tokens, whose logits and indices with_index(least, f)
-// passes to f(logit, index); it may leave out logits below `least`.  mass: of which top-p takes its share, where that is not the mass of these tokens
-// (0).  race(least, keep) has those race for which keep(logit, index) holds.  False where they do not
-// hold top-p's cut, unless nothing below them is kept.
+// The cuts and the race among the peers' `have` tokens.  with_index(least, f) passes their logits and
+// indices to f(logit, index), where it may leave out logits below `least`; race(least, keep) has
+// those race for which keep(logit, index) holds.  mass: of which top-p takes its share, where that is not
+// the mass of these tokens (0).  False where they do not hold top-p's cut, unless nothing below them
+// is kept.
 template <int kThreads, typename Peers, typename WithIndex, typename Race>
 __device__ __forceinline__ bool choose(Shared<kThreads> &s, Peers peers, const Query &q, float range, u64 mass,
                                        u64 have, WithIndex with_index, Race race) {
