@@ -598,6 +598,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
     cg::cluster_group cluster = cg::this_cluster();
     const int C = cluster.num_blocks(), rank = cluster.block_rank();
     const int row = blockIdx.x / C, t = threadIdx.x, V = p.vocab;
+    // The blocks of a cluster may start at different times, and shared memory of one that has not
+    // started may not be touched: the wait for this is before the first write to a peer's.
+    if (C > 1) ptx::cluster_arrive_relaxed();
     const T *logits = static_cast<const T *>(p.logits) + row * p.logits_stride;
     const float *noise = p.noise + row * p.noise_stride;
     if (t == 0) {
@@ -643,6 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
     });
     uint32_t top_key = (uint32_t)block_max<kThreads>(logit_key(top_here), s.red);
     if (C > 1) {
+        ptx::cluster_wait();
         if (t < C) cluster.map_shared_rank(&s, t)->tops[rank] = top_key;
         cluster.sync();
         for (int i = 0; i < C; ++i) top_key = max(top_key, s.tops[i]);
@@ -656,9 +660,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
             __syncthreads();
             return true;
         }
-        asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+        ptx::cluster_arrive();
         if (rank != 0) return false;
-        asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        ptx::cluster_wait();
         return true;
     };
     const float m = key_logit(top_key);
@@ -756,9 +760,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
         });
     if (C > 1) {
         if (rank == 0 && t < C) cluster.map_shared_rank(&s, t)->wide = !done;
-        asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+        ptx::cluster_arrive();
         if (!done || rank != 0) {
-            asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+            ptx::cluster_wait();
             if (!s.wide) return;
         }
     }
