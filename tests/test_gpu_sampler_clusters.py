@@ -48,3 +48,11 @@ def run(rows, V, some, seed):
 def test_unfiltered_and_greedy(rows, V):
     """Each block passes its maximum to its peers as soon as it has it, and its best token to the first."""
     run(rows, V, [(1.0, 0, 1.0, 0.0), (0.0, 0, 1.0, 0.0), (0.7, 0, 1.0, 0.0), (1.0, 1, 0.5, 0.0)], V)
+
+
+@pytest.mark.parametrize("rows,V", SHAPES)
+def test_listed_rows(rows, V):
+    """The first block has the list and decides alone, with little to do (min-p alone, small top-k)
+    while its peers still read its totals; rows that all blocks search lie in between."""
+    run(rows, V, [(1.0, 0, 1.0, 0.3), (0.7, 50, 0.95, 0.02), (0.5, 5, 1.0, 0.0), (1.3, 0, 0.95, 0.0),
+                  (0.6, 0, 0.5, 0.5), (1.0, 0, 0.9, 0.05)], V + 1)

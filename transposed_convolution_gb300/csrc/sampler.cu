@@ -758,10 +758,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
                 q.race(best, l, at, in);
             }
         });
+    // The others have read the first block's totals when they arrive: it may not end before that, but
+    // has its race to finish first where the list did.
+    const bool to_wait = C > 1 && done;
     if (C > 1) {
         if (rank == 0 && t < C) cluster.map_shared_rank(&s, t)->wide = !done;
         ptx::cluster_arrive();
-        if (!done || rank != 0) {
+        if (!to_wait) {
             ptx::cluster_wait();
             if (!s.wide) return;
         }
@@ -777,6 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
         for (int i = 0; i < C; ++i) won = max(won, s.bests[i]);
     }
     if (t == 0) p.tokens[row] = (int64_t)(uint32_t)~(uint32_t)won;
+    if (to_wait) ptx::cluster_wait();
 }
 
 template <typename T, int kThreads, bool kStaged>
