@@ -102,6 +102,9 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(EvictParams p, i
     cg::cluster_group cluster = cg::this_cluster();
     const int C = cluster.num_blocks(), rank = cluster.block_rank();
     const int unit = blockIdx.x / C, b = unit / p.Hkv, t = threadIdx.x, lane = t % 32, warp = t / 32;
+    // No block touches another's shared memory before all of the cluster have started: there may be
+    // nothing to choose, and the first access is then the counts'.
+    if (C > 1) ptx::cluster_arrive_relaxed();
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int len = p.cache.lens[b];
@@ -110,6 +113,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(EvictParams p, i
         n = p.cache.cap;
         if (t == 0) atomicOr(p.cache.status, kStatusBadLength);
     }
+    if (C > 1) ptx::cluster_wait();
     const int first = min(rank * part, n), last = min(first + part, n);     // this block's slots
     const int keep = min(n, p.budget);
     const float *const w = p.w + (int64_t)unit * p.cache.cap;
