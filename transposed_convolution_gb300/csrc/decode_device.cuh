@@ -19,13 +19,14 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float
 template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
 
 // Tokens of sequence b (slots 0 .. n - 1), with the new one if there is one and room for it.
-// Reports a length past the table's capacity.
+// Reports a length past the table's capacity, whichever thread asks; every block asks for all sequences,
+// so the first one does.
 __device__ __forceinline__ int tokens_of(const CacheView &c, int b, bool with_new, int *len) {
     int n = c.lens[b];
     *len = n;
     if (n < 0) return 0;
     if (n > c.cap - (with_new ? 1 : 0)) {
-        if (threadIdx.x == 0) atomicOr(c.status, kStatusBadLength);
+        if (blockIdx.x == 0) atomicOr(c.status, kStatusBadLength);
         *len = min(n, c.cap);
         return *len;
     }
