@@ -22,13 +22,16 @@
 // run ahead, gained less than its parts cost once the rings were as short as they are.
 //
 // Every warp streams its own slots through a ring of cp.async stages without block barriers,
-// and keeps a running maximum, sum and output of its own; the warps join once for each unit of
+// and keeps a running base, sum and output of its own; the warps join once for each unit of
 // a chunk.  (Bulk copies, one a row as the pages want them, issue from one lane at a time:
 // 655 instructions a step, and 532 us for the full batch.)
 //
 // Rounding: scores, statistics and outputs are fp32.  The probabilities enter the product with
 // V as two 16-bit terms (the rounded value and what rounding left), so they keep at least 15
-// bits; one term alone would add as much error as the rounding of the output does.
+// bits; one term alone would add as much error as the rounding of the output does.  fp16 terms end at
+// 2^-24, which the lift (below) makes 2^-37 of the largest weight: probabilities of less than 2^-22 of that
+// have fewer bits.  (Without the lift 2^-24 was all there was, and slots 17 nats under a warp's largest
+// were left out.  The ragged fp16 batch takes 32.0 us with it and 31.8 without.)
 #pragma once
 
 #include "decode_device.cuh"
@@ -55,6 +58,7 @@ template <> struct Shape<4, 256> { static constexpr int kWarps = 3, kStages = 2,
 
 template <typename T> struct Pair;
 template <> struct Pair<__nv_bfloat16> {
+    static constexpr float kLift = 0.0f, kSlack = 8.0f;
     static __device__ __forceinline__ uint32_t pack(float a, float b) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
         return *reinterpret_cast<const uint32_t *>(&v);
@@ -71,6 +75,7 @@ template <> struct Pair<__nv_bfloat16> {
     }
 };
 template <> struct Pair<__half> {
+    static constexpr float kLift = 13.0f, kSlack = 2.0f;
     static __device__ __forceinline__ uint32_t pack(float a, float b) {
         const __half2 v = __floats2half2_rn(a, b);
         return *reinterpret_cast<const uint32_t *>(&v);
@@ -140,9 +145,12 @@ struct Walk {
     int count;               // segments (whole units) so far
 };
 
-// A running maximum is raised only when a score exceeds it by 2^kSlack: until then the
-// probabilities may reach 2^kSlack, which changes no rounding, and the steps in between need no
-// reduction over the warp.
+// Weights are powers of two of a score's distance to its head's base, which follows the running maximum:
+// it is raised, to kLift below the maximum, only when a score exceeds that maximum by kSlack.  Until
+// then weights may reach 2^(kLift + kSlack), and the steps in between need no reduction over the warp.
+// fp32 and bf16 weights have exponents to spare on either side.  fp16 ones end at 2^-24, so they are
+// lifted to just below that type's largest: 2^15 for a slack of two, with the base rounded upwards, so that
+// they stay below it for scores so large that the lift itself is rounded.
 constexpr float kSlack = 8.0f;
 
 // The arithmetic of one warp on 16 slots and up to kHeads heads, 16-bit types: lane (r0 = lane / 4,
@@ -233,7 +241,7 @@ template <typename T, int DP, int NH, int kD_> struct Heads16 {
 #pragma unroll
         for (int h = 0; h < NH; ++h)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) grew |= fmaxf(s[h][e], s[h][e + 2]) > m[h][e] + kSlack;
+            for (int e = 0; e < 2; ++e) grew |= fmaxf(s[h][e], s[h][e + 2]) > __fadd_rd(m[h][e], P::kLift + P::kSlack);
         if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
             for (int h = 0; h < NH; ++h)
@@ -243,7 +251,7 @@ template <typename T, int DP, int NH, int kD_> struct Heads16 {
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                    v = fmaxf(v, m[h][e]);
+                    v = fmaxf(__fsub_ru(v, P::kLift), m[h][e]);
                     const float shrink = m[h][e] == kNegInf ? 0.0f : pow2(m[h][e] - v);
                     m[h][e] = v;
                     l[h][e] *= shrink;
@@ -257,7 +265,7 @@ template <typename T, int DP, int NH, int kD_> struct Heads16 {
         uint32_t hi[NH][2], lo[NH][2];
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-            // A head without any slot so far has no maximum yet: its weights are 0.
+            // A head without any slot so far has no base yet: its weights are 0.
             const float b0 = m[h][0] == kNegInf ? 0.0f : m[h][0];
             const float b1 = m[h][1] == kNegInf ? 0.0f : m[h][1];
 #pragma unroll
@@ -286,7 +294,7 @@ template <typename T, int DP, int NH, int kD_> struct Heads16 {
         }
     }
 
-    // The warp's maxima, sums and outputs [kHeads][pitch] to shared memory.
+    // The warp's bases, sums and outputs [kHeads][pitch] to shared memory.
     __device__ __forceinline__ void put(float *red_m, float *red_l, float *to, int pitch, int D) {
         const int lane = threadIdx.x % 32, r0 = lane / 4, quad = lane % 4;
 #pragma unroll
