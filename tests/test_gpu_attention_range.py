@@ -108,3 +108,35 @@ def test_rising_scores(dtype):
         if dtype == "f16":
             bound = bound + 2.0 ** -37 * np.abs(v).sum(0)
         assert (np.abs(out - want) <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("what", ["nan score", "inf score", "nan value"])
+@pytest.mark.parametrize("n,at,window", [(100, 40, 0), (700, 3, 0), (700, 699, 0), (9000, 5000, 0), (700, 600, 200)])
+def test_not_a_number_reaches_outputs_and_weights(n, at, window, what, dtype):
+    """A score that is NaN or infinite makes a head's softmax, and with it every weight of the step, NaN;
+    heads of the other group and slots before the window keep theirs."""
+    D, pages = 64, -(-n // PAGE)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    k, v = (torch.randn(pages, 2, PAGE, D, generator=g, device="cuda").to(DT[dtype]) for _ in range(2))
+    q = torch.randn(1, 4, D, generator=g, device="cuda").to(DT[dtype])
+    q[:, :, 0] = 1
+    if what == "nan value":
+        v[at // PAGE, 0, at % PAGE, 7] = float("nan")
+    else:
+        k[at // PAGE, 0, at % PAGE, 0] = float(what[:3])
+    plan = ctr.PagedAttention(1, 4, 2, D, PAGE, pages, k_pages=k, v_pages=v, weights=True, window=window)
+    tables = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    w = torch.full((1, 2, plan.capacity), 0.5, device="cuda")
+    out = plan.forward(q, tables, lens, weights=w)
+    plan.check()
+    first = max(0, n - window) if window else 0
+    assert torch.isfinite(out[0, 2:]).all() and torch.isfinite(w[0, 1]).all()
+    assert (w[0, :, :first] == 0.5).all() and (w[0, :, n:] == 0.5).all()
+    if what == "nan value":
+        assert torch.isnan(out[0, :2, 7]).all() and torch.isfinite(out[0, :2, :7]).all()
+        assert torch.isfinite(out[0, :2, 8:]).all() and torch.isfinite(w[0, 0]).all()
+    else:
+        assert torch.isnan(out[0, :2]).all()
+        assert torch.isnan(w[0, 0, first:n]).all()

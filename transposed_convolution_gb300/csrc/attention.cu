@@ -21,8 +21,9 @@ __global__ void __launch_bounds__(kWeightThreads) weights_kernel(AttnParams p, i
     const int64_t base = ((int64_t)b * p.Hkv + hk) * p.cache.cap + j0, h0 = (int64_t)b * p.Hq + hk * p.G;
     for (int g = t; g < p.G; g += kWeightThreads) {
         const float2 s = p.stats[h0 + g];
-        // A head that attends to nothing has no probabilities: 2^(x - inf) = 0.
-        stats[g] = s.y > 0.0f ? make_float2(s.x, 1.0f / s.y) : make_float2(__builtin_inff(), 0.0f);
+        // A head that attends to nothing has no probabilities: 2^(x - inf) = 0.  One whose sum is NaN has
+        // nothing but NaN.
+        stats[g] = s.y == 0.0f ? make_float2(__builtin_inff(), 0.0f) : make_float2(s.x, 1.0f / s.y);
     }
     // Slots before the window hold no scores of this call; those past the end stay as they are.
     float old[4], w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
