@@ -140,3 +140,33 @@ def test_not_a_number_reaches_outputs_and_weights(n, at, window, what, dtype):
     else:
         assert torch.isnan(out[0, :2]).all()
         assert torch.isnan(w[0, 0, first:n]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("Hq,D", [(1, 64), (5, 80), (8, 128), (16, 128), (2, 256)])
+@pytest.mark.parametrize("n,at", [(1, 0), (100, 40), (700, 3), (5000, 4999)])
+def test_infinite_values(n, at, Hq, D, dtype):
+    """An infinite value whose slot has a weight gives that infinity in its column, two of opposite
+    signs NaN, and the other columns are as without them."""
+    pages = -(-n // PAGE)
+    g = torch.Generator(device="cuda").manual_seed(n + D)
+    k, v = (torch.randn(pages, 1, PAGE, D, generator=g, device="cuda").to(DT[dtype]) for _ in range(2))
+    q = torch.randn(1, Hq, D, generator=g, device="cuda").to(DT[dtype])
+    plan = ctr.PagedAttention(1, Hq, 1, D, PAGE, pages, k_pages=k, v_pages=v)
+    tables = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    plain = plan.forward(q, tables, lens)
+    row = v[at // PAGE, 0, at % PAGE]
+    inf = float("inf")
+    row[3], row[D - 1], row[17] = inf, -inf, inf
+    other = (at * 7 + 11) % n
+    v[other // PAGE, 0, other % PAGE, 17] = -inf
+    out = plan.forward(q, tables, lens)
+    plan.check()
+    assert (out[:, :, 3] == inf).all() and (out[:, :, D - 1] == -inf).all()
+    if other == at:
+        assert (out[:, :, 17] == -inf).all()
+    else:
+        assert torch.isnan(out[:, :, 17]).all()
+    keep = [c for c in range(D) if c not in (3, 17, D - 1)]
+    assert torch.equal(out[:, :, keep], plain[:, :, keep])

@@ -27,11 +27,12 @@
 // 655 instructions a step, and 532 us for the full batch.)
 //
 // Rounding: scores, statistics and outputs are fp32.  The probabilities enter the product with
-// V as two 16-bit terms (the rounded value and what rounding left), so they keep at least 15
-// bits; one term alone would add as much error as the rounding of the output does.  fp16 terms end at
-// 2^-24, which the lift (below) makes 2^-37 of the largest weight: probabilities of less than 2^-22 of that
-// have fewer bits.  (Without the lift 2^-24 was all there was, and slots 17 nats under a warp's largest
-// were left out.  The ragged fp16 batch takes 32.0 us with it and 31.8 without.)
+// V as two 16-bit terms (the value rounded towards zero and what that left), so they keep at least 15
+// bits; one term alone would add as much error as the rounding of the output does.  Neither term is
+// negative or, unless the probability is, 0: an infinite value in V stays that infinity.
+// fp16 terms end at 2^-24, which the lift (below) makes 2^-37 of the largest weight: probabilities of less
+// than 2^-22 of that have fewer bits.  (Without the lift 2^-24 was all there was, and slots 17 nats under a
+// warp's largest were left out.  The ragged fp16 batch takes 32.0 us with it and 31.8 without.)
 #pragma once
 
 #include "decode_device.cuh"
@@ -59,6 +60,13 @@ template <> struct Shape<4, 256> { static constexpr int kWarps = 3, kStages = 2,
 template <typename T> struct Pair;
 template <> struct Pair<__nv_bfloat16> {
     static constexpr float kLift = 0.0f, kSlack = 8.0f;
+    static constexpr float kLeast = 1.17549435e-38f;      // smallest term (2^-126)
+    // Rounded towards zero.
+    static __device__ __forceinline__ uint32_t pack_down(float a, float b) {
+        uint32_t r;
+        asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+        return r;
+    }
     static __device__ __forceinline__ uint32_t pack(float a, float b) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
         return *reinterpret_cast<const uint32_t *>(&v);
@@ -76,6 +84,12 @@ template <> struct Pair<__nv_bfloat16> {
 };
 template <> struct Pair<__half> {
     static constexpr float kLift = 13.0f, kSlack = 2.0f;
+    static constexpr float kLeast = 5.96046448e-8f;       // smallest term (2^-24)
+    static __device__ __forceinline__ uint32_t pack_down(float a, float b) {
+        uint32_t r;
+        asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+        return r;
+    }
     static __device__ __forceinline__ uint32_t pack(float a, float b) {
         const __half2 v = __floats2half2_rn(a, b);
         return *reinterpret_cast<const uint32_t *>(&v);
@@ -273,10 +287,10 @@ template <typename T, int DP, int NH, int kD_> struct Heads16 {
                 const float x = pow2(s[h][2 * e] - b0), y = pow2(s[h][2 * e + 1] - b1);
                 l[h][0] += x;
                 l[h][1] += y;
-                const uint32_t r = P::pack(x, y);
+                const uint32_t r = P::pack_down(x, y);
                 const float2 f = P::unpack(r);
                 hi[h][e] = transpose8(r);
-                lo[h][e] = transpose8(P::pack(x - f.x, y - f.y));
+                lo[h][e] = transpose8(P::pack(fmaxf(x - f.x, P::kLeast), fmaxf(y - f.y, P::kLeast)));
             }
         }
         const uint32_t a = ptx::smem_u32(v_rows) + ((lane & 7) + (lane >> 4) * 8) * pitch +
@@ -905,7 +919,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(AttnParams p, int
         float M2 = M;
 #pragma unroll
         for (int y = 0; y < kDepth; ++y) {
-            if (c + y >= to) s[y] = make_float2(kNegInf, 0.0f);
+            if (c + y >= to) {
+                // (Infinite outputs would make 0 times them NaN.)
+                s[y] = make_float2(kNegInf, 0.0f);
+#pragma unroll
+                for (int i = 0; i < N; ++i) u[i][y] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
             M2 = fmaxf(M2, s[y].x);
         }
         const float shrink = M == kNegInf ? 0.0f : pow2(M - M2);
