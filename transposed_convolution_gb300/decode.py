@@ -225,8 +225,9 @@ class PagedAttention(_DecodePlan):
         if lens_out is None:
             lens_out = torch.empty(self._lens_shape, dtype=torch.int32, device=self.device)
             made.append(lens_out)
-        if weights_out is None:
-            weights_out = torch.zeros(shape, dtype=torch.float32, device=self.device)
+        clear = weights_out is None
+        if clear:
+            weights_out = torch.empty(shape, dtype=torch.float32, device=self.device)
             made.append(weights_out)
         if weights_out.dim() != 3:
             raise ValueError("weights_out must be [%d, %d, >= %d]" % (self.B, self.H_kv, budget))
@@ -234,9 +235,13 @@ class PagedAttention(_DecodePlan):
         s_ptr = at(slots, "slots", shape, torch.int32)
         lo_ptr = at(lens_out, "lens_out", self._lens_shape, torch.int32)
         wo_ptr = at(weights_out, "weights_out", (self.B, self.H_kv, pitch), torch.float32)
+        raw = self._stream(stream, *made)
+        if clear:
+            # On the call's own stream: on the current one it might run after the kernels.
+            with torch.cuda.stream(stream):
+                weights_out.zero_()
         st = self._evict(self.handle, t_ptr, l_ptr, w_ptr, d_ptr, dst_tables.shape[1], budget,
-                         int(sinks), int(recent), s_ptr, lo_ptr, wo_ptr, pitch,
-                         self._stream(stream, *made))
+                         int(sinks), int(recent), s_ptr, lo_ptr, wo_ptr, pitch, raw)
         if st:
             raise _ctr.CtrError(st, "ctr_attn_evict")
         return slots, lens_out, weights_out
