@@ -632,6 +632,7 @@ void ctr_attn_destroy(ctr_attn_t plan);
  *     top_p < 1     the tokens with (mass of the tokens before them) < top_p * (mass of the
  *                   top_k tokens)
  *     min_p > 0     the tokens with w_i >= min_p
+ * (a NaN top_p or min_p filters nothing, a NaN T is greedy)
  * and the token is the kept one with the largest w_i / max(noise_i, FLT_MIN) (ties: the lowest
  * index).  With independent Exp(1) numbers as noise this is a draw from the kept tokens in
  * proportion to w (the exponential race).  A token with l_i = -inf is never drawn; a row

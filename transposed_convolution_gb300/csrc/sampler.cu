@@ -608,7 +608,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) sample_kernel(Sampl
     }
     ptx::griddep_wait();
     const float temp = p.temperature ? p.temperature[row] : 1.0f;
-    const float min_p = p.min_p ? p.min_p[row] : 0.0f, top_p = p.top_p ? p.top_p[row] : 1.0f;
+    // (fmaxf: a NaN min-p keeps all, as 0 does.)
+    const float min_p = p.min_p ? fmaxf(p.min_p[row], 0.0f) : 0.0f, top_p = p.top_p ? p.top_p[row] : 1.0f;
     const int asked = p.top_k ? p.top_k[row] : 0;
     const bool first_only = !(temp > 0.0f) || min_p > 1.0f || asked == 1;
     const bool by_k = asked > 0 && asked < V, by_p = top_p < 1.0f, by_min = min_p > 0.0f;
