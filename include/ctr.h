@@ -545,7 +545,10 @@ void ctr_istft_destroy(ctr_istft_t plan);
  * Rows of stale pages past a sequence's end may hold anything, NaN included.
  *
  * Sums, softmax statistics and weights are fp32; out is rounded once to the dtype.  The
- * result does not depend on timing: partial results join in a fixed order.
+ * probabilities of 16-bit caches keep 15 bits or more in the product with V (fp16: down to 2^-22 of
+ * the largest; their last bit is at least 2^-37 of it).  The result does not depend on timing:
+ * partial results join in a fixed order.  A NaN or infinite score makes its head's outputs and weights
+ * NaN; a head whose scores are all -inf gives 0.
  * A page number outside [0, num_pages) hides its slots, and a length past the table's capacity
  * is cut to it (without room for the new row, which is then not put); ctr_attn_check reports
  * either as CTR_ERR_INVALID_ARG.  Two sequences may share pages that neither appends to.
@@ -579,9 +582,10 @@ ctr_status ctr_attn_set_weights(ctr_attn_t plan, int enable);
 size_t ctr_attn_workspace_bytes(ctr_attn_t plan);
 /* Bind a caller-owned workspace (256-byte aligned), as ctr_plan_bind_workspace. */
 ctr_status ctr_attn_bind_workspace(ctr_attn_t plan, void *dev_ptr, size_t bytes);
-/* Clear the workspace's counters and status word (asynchronous on stream): once after each
- * ctr_attn_bind_workspace, before the first ctr_attn_forward (CTR_ERR_NOT_PREPARED
- * otherwise).  The calls themselves leave the counters cleared. */
+/* Clear the workspace's status word (asynchronous on stream): once after each
+ * ctr_attn_bind_workspace, before the first ctr_attn_forward or ctr_attn_evict
+ * (CTR_ERR_NOT_PREPARED otherwise).  What a call reports there stays until ctr_attn_check or the
+ * next reset. */
 ctr_status ctr_attn_reset(ctr_attn_t plan, void *stream);
 /* Bind the caller-owned cache pages; they must stay allocated while bound.  At most 2^36 elements
  * each (CTR_ERR_UNSUPPORTED beyond). */

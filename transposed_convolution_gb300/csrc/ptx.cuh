@@ -118,7 +118,8 @@ __device__ __forceinline__ bool abort_warp(const volatile int *abort) {
 // ---------------------------------------------------------------- programmatic dependent launch
 // Wait until the grids this one depends on (the previous kernels of the stream, when this one
 // was launched with programmatic stream serialization) have completed and their memory is
-// visible; a no-op otherwise.  Every kernel calls it before its first global memory access.
+// visible; a no-op otherwise.  Every kernel calls it before its first global memory access, except
+// for inputs that the kernel before only reads, where that one waited before it let this one start.
 __device__ __forceinline__ void griddep_wait() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }

@@ -3,9 +3,10 @@
 // Every filter keeps a prefix of the order (logit descending, index ascending), so the kept set
 // is a lowest key, and how many of the tokens with that key stay.  The logits are read once, which
 // bounds the operator: V elements of 2 or 4 bytes a row, and the random numbers of the kept
-// tokens only.  25 million of them take the CUDA cores about as long as the memory, so the work on
-// each is kept to half a packed maximum, and for top-p a conversion, a scaled difference and an
-// exponential while the memory is busy.  A row's block (or cluster of blocks)
+// tokens only.  25 million of them take the CUDA cores longer than the memory (23 instructions a logit
+// in all with top-p and min-p: 33 us, 7.5 of them the memory's), so the work on each is kept to half a packed
+// maximum, and for top-p a conversion, a scaled difference and an exponential while the memory is busy.
+// A row's block (or cluster of blocks)
 //   1. reads its part into shared memory, where it fits, and takes the maximum and the mass;
 //   2. lists the tokens within 2^-kListBits of the maximum (or min_p of it: nothing below is kept
 //      then) at the cluster's first block; the others wait;
@@ -15,7 +16,8 @@
 // Where the list cannot hold the cuts (flat logits without min_p, or too many tokens near the maximum)
 // all blocks do 3 and 4 together, each on its part: every histogram is the sum of theirs, and each
 // races its own.  16 rows of 200000 fp32 logits, top-p 0.95 at temperature 1.3 (a fifth of the tokens
-// stays): 108 us, with 25000 logits a block gone over eight times; by one block of the row alone 420.
+// stays): 111 us from memory and 102 partly from L2, with 25000 logits a block gone over eight times; by
+// one block of the row alone 420.
 //
 // Sums: a thread's masses are added in fp32 in a fixed order, everything beyond as integers in units of
 // 2^-35, and the list's order matters to nothing: equal inputs give equal tokens.  A bin's mass is
