@@ -579,6 +579,9 @@ ctr_status ctr_attn_set_window(ctr_attn_t plan, int64_t window);
 /* Accumulate weights (default 0): the workspace then also holds one fp32 score per query head
  * and slot.  Unbinds the workspace. */
 ctr_status ctr_attn_set_weights(ctr_attn_t plan, int enable);
+/* Allow ctr_attn_forward_chunk (default 0): the workspace then also holds its partial results.
+ * Unbinds the workspace. */
+ctr_status ctr_attn_set_chunks(ctr_attn_t plan, int enable);
 size_t ctr_attn_workspace_bytes(ctr_attn_t plan);
 /* Bind a caller-owned workspace (256-byte aligned), as ctr_plan_bind_workspace. */
 ctr_status ctr_attn_bind_workspace(ctr_attn_t plan, void *dev_ptr, size_t bytes);
@@ -596,6 +599,37 @@ ctr_status ctr_attn_forward(ctr_attn_t plan, const void *q, int64_t q_stride, co
                             const void *v_new, int64_t kv_stride, const int32_t *tables,
                             const int32_t *lens, const float *weights_in, float *weights_out,
                             void *out, void *stream);
+/*
+ * Attention of a chunk of new tokens -- a prompt, a piece of one, drafted tokens -- whose K and V rows
+ * are in the cache already (ctr_attn_put).  Sequence b has the rows starts[b] .. starts[b + 1] - 1 of q;
+ * its token i, at slot lens[b] + i, attends to the slots up to its own:
+ *
+ *     end  = lens[b] + i + 1;   lo = window > 0 ? max(0, end - window) : 0
+ *     p[j] = softmax over lo <= j < end of  scale * (q[t, h] . K[j, h / (H_q / H_kv)])
+ *     out[t, h] = sum over j of p[j] * V[j, h / (H_q / H_kv)]
+ *
+ *   q       [T][H_q][D] in the plan's dtype, q_stride elements between rows (q, out and the stride
+ *           in bytes on 16-byte boundaries)
+ *   tables  [B][max_pages] int32; only the entries of slots that some row attends to are read
+ *   lens    [B] int32: tokens before the chunk; lens[b] < 0 marks an idle sequence, whose rows give 0
+ *   starts  [B + 1] int32, ascending, 0 <= starts[0], starts[B] <= T; rows of out outside
+ *           [starts[0], starts[B]) are left alone
+ *   out     [T][H_q][D]
+ * Needs ctr_attn_set_chunks(plan, 1) (CTR_ERR_NOT_PREPARED), T * H_q / H_kv <= 2^30 and T <= 2^24.  A plan
+ * with weights accumulates none here.
+ *
+ * Scores, softmax statistics and sums are fp32; the probabilities of 16-bit caches are rounded once to the
+ * dtype for the product with V (fp16: down to 2^-37 of the largest); out is rounded once.  The result does
+ * not depend on timing.  What a row does not attend to never reaches it, infinities and NaN in V and
+ * stale rows included; an infinite V that a row attends to makes that output infinite (a weight below
+ * 2^-126 of the row's largest counts as 0 and gives NaN), a NaN or +inf score makes the head's outputs NaN, and
+ * a row without slots or whose scores are all -inf gives 0.  Page numbers out of range hide their slots.
+ * starts out of order or range make their sequence empty, and tokens past the table's capacity
+ * attend to the slots below it; ctr_attn_check reports all three as CTR_ERR_INVALID_ARG.
+ */
+ctr_status ctr_attn_forward_chunk(ctr_attn_t plan, const void *q, int64_t q_stride, int64_t T,
+                                  const int32_t *tables, const int32_t *lens, const int32_t *starts,
+                                  void *out, void *stream);
 /*
  * Evict from the cache by accumulated attention weight: of the lens[b] slots of every
  * (sequence, KV head) keep n = min(lens[b], budget) -- the first `sinks`, the last `recent`,
@@ -620,10 +654,129 @@ ctr_status ctr_attn_evict(ctr_attn_t plan, const int32_t *tables, const int32_t 
                           int32_t *lens_out, float *weights_out, int64_t weights_pitch,
                           void *stream);
 /* Synchronise stream, then read and clear the status word: CTR_OK, CTR_ERR_INVALID_ARG when a
- * call since the last check met a page number or length out of range, or CTR_ERR_CUDA. */
+ * call since the last check met a page number, slot, length or start out of range,
+ * CTR_ERR_DEVICE_TIMEOUT when a kernel gave up waiting for its own copies or products (a defect;
+ * its outputs are not valid), or CTR_ERR_CUDA. */
 ctr_status ctr_attn_check(ctr_attn_t plan, void *stream);
 ctr_status ctr_attn_describe(ctr_attn_t plan, char *buf, size_t len);
 void ctr_attn_destroy(ctr_attn_t plan);
+
+/* ------------------------------------------------------------------------------------
+ * Rotary positions, alone or on the way into the cache.
+ *
+ * Pair i of the first R columns of a head's D -- columns (i, i + R/2) with CTR_ROPE_HALF (default), (2i,
+ * 2i + 1) with CTR_ROPE_INTERLEAVED -- is turned by the token's position; the other columns are copied:
+ *
+ *     x' = m (x cos a - y sin a),   y' = m (x sin a + y cos a),   a = position * f_i
+ *     f_i = base^(-2i/R)                                    (base 10000, m = magnitude = 1 by default)
+ *     CTR_ROPE_SCALE_LINEAR   f_i / factor
+ *     CTR_ROPE_SCALE_PARTS    (1 - g) f_i / factor + g f_i,  g = (original f_i / 2 pi - low) / (high - low),
+ *                             at least 0 and at most 1: pairs that turn fewer than `low` times over
+ *                             `original` positions are scaled, those of more than `high` turns are not
+ *
+ * or frequencies of the caller's own.  Angles are exact to 2^-32 turn plus the position times the 53-bit
+ * rounding of f_i; the products are fp32, rounded once to the dtype.  Positions are int32; a
+ * negative one turns backwards, so that a call with the negated positions is the transpose
+ * (the gradient of a call with respect to its input, from the gradient of its output).
+ * ------------------------------------------------------------------------------------ */
+typedef struct ctr_rope_s *ctr_rope_t;
+
+typedef enum {
+    CTR_ROPE_HALF = 0,
+    CTR_ROPE_INTERLEAVED = 1
+} ctr_rope_layout;
+
+typedef enum {
+    CTR_ROPE_SCALE_NONE = 0,
+    CTR_ROPE_SCALE_LINEAR = 1,
+    CTR_ROPE_SCALE_PARTS = 2
+} ctr_rope_scaling;
+
+/* 2 <= R <= D, R even (CTR_ERR_INVALID_ARG); D <= 512 (CTR_ERR_UNSUPPORTED).  Host only, as the calls
+ * down to ctr_rope_frequencies. */
+ctr_status ctr_rope_create(ctr_rope_t *out, int64_t D, int64_t R, int dtype);
+ctr_status ctr_rope_set_layout(ctr_rope_t plan, int layout);
+/* base >= 1, finite.  Drops the caller's own frequencies, as ctr_rope_set_scaling does. */
+ctr_status ctr_rope_set_base(ctr_rope_t plan, double base);
+/* factor > 0 (LINEAR, PARTS); original > 0 and 0 <= low < high (PARTS); all finite. */
+ctr_status ctr_rope_set_scaling(ctr_rope_t plan, int scaling, double factor, double original, double low,
+                                double high);
+ctr_status ctr_rope_set_magnitude(ctr_rope_t plan, float magnitude);
+/* The R/2 frequencies, in radians a position: set to the caller's (finite), or read. */
+ctr_status ctr_rope_set_frequencies(ctr_rope_t plan, const double *frequencies, int64_t n);
+ctr_status ctr_rope_frequencies(ctr_rope_t plan, double *frequencies, int64_t n);
+/*
+ * q [T][H_q][D] and k [T][H_k][D] (either may have no heads) to q_out and k_out, each in place or
+ * apart from every other buffer, any row strides (in elements, at least a row), aligned to their elements.
+ * positions [T] int32.  T <= 2^24, H_q, H_k <= 2^14.  Asynchronous on stream.
+ */
+ctr_status ctr_rope_forward(ctr_rope_t plan, const void *q, int64_t q_stride, int64_t H_q, const void *k,
+                            int64_t k_stride, int64_t H_k, const int32_t *positions, int64_t T, void *q_out,
+                            int64_t q_out_stride, void *k_out, int64_t k_out_stride, void *stream);
+/*
+ * Put T tokens' K and V rows into the cache of an attention plan, at slots[t] (row slots[t] %
+ * page_size of page slots[t] / page_size; < 0: nowhere), K turned by `rope` if one is given; with q (which
+ * needs rope) also turn q [T][H_q][D] to q_out (which may be q).  rope has the plan's D and dtype.
+ *   k, v   [T][H_kv][D], kv_stride elements between rows; slots [T] int64, no slot twice; positions [T]
+ *          int32, needed with rope
+ * q, k, v, q_out and the strides in bytes on 16-byte boundaries.  Slots past the cache are skipped and
+ * reported by ctr_attn_check.  Needs the bound cache and the workspace, as ctr_attn_forward.
+ */
+ctr_status ctr_attn_put(ctr_attn_t plan, ctr_rope_t rope, const void *q, int64_t q_stride, const void *k,
+                        const void *v, int64_t kv_stride, const int32_t *positions, const int64_t *slots,
+                        int64_t T, void *q_out, int64_t q_out_stride, void *stream);
+ctr_status ctr_rope_describe(ctr_rope_t plan, char *buf, size_t len);
+void ctr_rope_destroy(ctr_rope_t plan);
+
+/* ------------------------------------------------------------------------------------
+ * Pages of the cache for new tokens, and their slots and positions, on the GPU.
+ *
+ * The free list is two buffers of the caller's: free_pages [num_pages] int32, of which the first *count
+ * are free.  Sequence b has lens[b] tokens in the first ceil(lens[b] / page_size) pages of its row of
+ * tables [B][max_pages]; lens[b] < 0 marks an idle one.
+ *
+ * ctr_pages_reserve makes room for counts[b] more tokens in each sequence: pages from the end of the
+ * list into the table where the last page does not hold them, and for every new token, sequence by
+ * sequence, its slot page * page_size + row and its position.  Requests are served in order: one is
+ * granted, as a whole, if the rows of all requests up to it are at most `rows`, and if it needs no page
+ * or the pages that all requests up to it need are on the list.
+ *     granted [B]      counts[b], or 0
+ *     starts [B + 1]   first row of each sequence: sums of the granted counts
+ *     slots [rows] int64, positions [rows] int32; rows from starts[B] on get -1 and 0
+ *     lens_out [B]     lens[b] + granted[b]
+ * ctr_pages_release gives back the pages behind the first keep[b] tokens of each sequence (keep[b] <
+ * 0: all of them, and the sequence becomes idle), the last sequence's last page first, so that they come
+ * out again in the order they had, and sets their table entries to -1.
+ *     lens_out [B]     min(lens[b], keep[b]), -1 for keep[b] < 0; idle sequences stay as they are
+ * Neither changes lens.  A page is given back by one sequence only: pages that sequences share are the
+ * caller's to keep apart.
+ *
+ * A count < 0, a length out of range and a request past the table's capacity are refused (granted 0);
+ * they, page numbers out of range (their slots are -1) and a list that would hold more than num_pages pages
+ * are reported by ctr_pages_check as CTR_ERR_INVALID_ARG.
+ * ------------------------------------------------------------------------------------ */
+typedef struct ctr_pages_s *ctr_pages_t;
+
+/* 1 <= B <= 1024, page_size >= 1, max_pages >= 1, max_pages * page_size <= 2^28.  Host only. */
+ctr_status ctr_pages_create(ctr_pages_t *out, int64_t B, int64_t page_size, int64_t max_pages);
+/* Bind the caller's free list, 1 <= num_pages < 2^31. */
+ctr_status ctr_pages_bind_list(ctr_pages_t plan, int32_t *free_pages, int32_t *count, int64_t num_pages);
+size_t ctr_pages_workspace_bytes(ctr_pages_t plan);
+/* Bind a caller-owned workspace (256-byte aligned). */
+ctr_status ctr_pages_bind_workspace(ctr_pages_t plan, void *dev_ptr, size_t bytes);
+/* Clear the workspace (asynchronous on stream): once after each ctr_pages_bind_workspace.  refill = 1
+ * also puts all pages on the list, page 0 last. */
+ctr_status ctr_pages_reset(ctr_pages_t plan, int refill, void *stream);
+/* Asynchronous on stream; rows <= 2^30.  No output may be an input or another output. */
+ctr_status ctr_pages_reserve(ctr_pages_t plan, int32_t *tables, const int32_t *lens, const int32_t *counts,
+                             int64_t rows, int32_t *granted, int32_t *starts, int64_t *slots,
+                             int32_t *positions, int32_t *lens_out, void *stream);
+ctr_status ctr_pages_release(ctr_pages_t plan, int32_t *tables, const int32_t *lens, const int32_t *keep,
+                             int32_t *lens_out, void *stream);
+/* As ctr_attn_check. */
+ctr_status ctr_pages_check(ctr_pages_t plan, void *stream);
+ctr_status ctr_pages_describe(ctr_pages_t plan, char *buf, size_t len);
+void ctr_pages_destroy(ctr_pages_t plan);
 
 /* ------------------------------------------------------------------------------------
  * Sampling the next token (a code of the codec) from logits and given random numbers.

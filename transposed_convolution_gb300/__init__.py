@@ -28,9 +28,18 @@ Decode step of the model that writes a codec's frames (same names as the C ABI):
 ``ctr_attn_check``, ``ctr_attn_describe``, ``ctr_attn_destroy``, ``ctr_sampler_create``,
 ``ctr_sampler_forward``, ``ctr_sampler_describe``, ``ctr_sampler_destroy``.
 
+Chunks of new tokens (prompts, drafted tokens) on the same cache: ``ctr_attn_set_chunks``,
+``ctr_attn_forward_chunk``, ``ctr_attn_put``, ``ctr_rope_create``, ``ctr_rope_set_layout``,
+``ctr_rope_set_base``, ``ctr_rope_set_scaling``, ``ctr_rope_set_magnitude``, ``ctr_rope_set_frequencies``,
+``ctr_rope_frequencies``, ``ctr_rope_forward``, ``ctr_rope_describe``, ``ctr_rope_destroy``,
+``ctr_pages_create``, ``ctr_pages_bind_list``, ``ctr_pages_workspace_bytes``,
+``ctr_pages_bind_workspace``, ``ctr_pages_reset``, ``ctr_pages_reserve``, ``ctr_pages_release``,
+``ctr_pages_check``, ``ctr_pages_describe``, ``ctr_pages_destroy``.
+
 High level: ``Plan`` (a plan with its packed weight and workspace held as torch tensors),
 ``Istft`` (an inverse-STFT plan with its workspace), ``PagedAttention`` (attention of one new
-token over a paged cache, and eviction from it), ``Sampler`` (next-token sampling), and
+token or a chunk of them over a paged cache, and eviction from it), ``Sampler`` (next-token sampling),
+``Rotary`` (rotary positions), ``PagePool`` (pages for new tokens), and
 ``conv_transpose(x, w, bias, stride, padding, output_padding, negative_slope, groups)``.
 """
 from __future__ import annotations
@@ -52,6 +61,11 @@ CTR_ERR_NOT_PREPARED = 7
 CTR_F32 = 0
 CTR_BF16 = 1
 CTR_F16 = 2
+CTR_ROPE_HALF = 0
+CTR_ROPE_INTERLEAVED = 1
+CTR_ROPE_SCALE_NONE = 0
+CTR_ROPE_SCALE_LINEAR = 1
+CTR_ROPE_SCALE_PARTS = 2
 CTR_ACT_NONE = 0
 CTR_ACT_LEAKY_RELU = 1
 CTR_PATH_AUTO = 0
@@ -136,6 +150,33 @@ SIGNATURES = {
     "ctr_attn_check": (ctypes.c_int, [_vp, _vp]),
     "ctr_attn_describe": (ctypes.c_int, [_vp, ctypes.c_char_p, ctypes.c_size_t]),
     "ctr_attn_destroy": (None, [_vp]),
+    "ctr_attn_set_chunks": (ctypes.c_int, [_vp, ctypes.c_int]),
+    "ctr_attn_forward_chunk": (ctypes.c_int, [_vp, _vp, ctypes.c_int64, ctypes.c_int64, _vp, _vp, _vp, _vp,
+                                              _vp]),
+    "ctr_attn_put": (ctypes.c_int, [_vp, _vp, _vp, ctypes.c_int64, _vp, _vp, ctypes.c_int64, _vp, _vp,
+                                    ctypes.c_int64, _vp, ctypes.c_int64, _vp]),
+    "ctr_rope_create": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.c_int64, ctypes.c_int64, ctypes.c_int]),
+    "ctr_rope_set_layout": (ctypes.c_int, [_vp, ctypes.c_int]),
+    "ctr_rope_set_base": (ctypes.c_int, [_vp, ctypes.c_double]),
+    "ctr_rope_set_scaling": (ctypes.c_int, [_vp, ctypes.c_int] + [ctypes.c_double] * 4),
+    "ctr_rope_set_magnitude": (ctypes.c_int, [_vp, ctypes.c_float]),
+    "ctr_rope_set_frequencies": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_double), ctypes.c_int64]),
+    "ctr_rope_frequencies": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_double), ctypes.c_int64]),
+    "ctr_rope_forward": (ctypes.c_int, [_vp, _vp, ctypes.c_int64, ctypes.c_int64, _vp, ctypes.c_int64,
+                                        ctypes.c_int64, _vp, ctypes.c_int64, _vp, ctypes.c_int64, _vp,
+                                        ctypes.c_int64, _vp]),
+    "ctr_rope_describe": (ctypes.c_int, [_vp, ctypes.c_char_p, ctypes.c_size_t]),
+    "ctr_rope_destroy": (None, [_vp]),
+    "ctr_pages_create": (ctypes.c_int, [ctypes.POINTER(_vp)] + [ctypes.c_int64] * 3),
+    "ctr_pages_bind_list": (ctypes.c_int, [_vp, _vp, _vp, ctypes.c_int64]),
+    "ctr_pages_workspace_bytes": (ctypes.c_size_t, [_vp]),
+    "ctr_pages_bind_workspace": (ctypes.c_int, [_vp, _vp, ctypes.c_size_t]),
+    "ctr_pages_reset": (ctypes.c_int, [_vp, ctypes.c_int, _vp]),
+    "ctr_pages_reserve": (ctypes.c_int, [_vp, _vp, _vp, _vp, ctypes.c_int64] + [_vp] * 6),
+    "ctr_pages_release": (ctypes.c_int, [_vp] * 6),
+    "ctr_pages_check": (ctypes.c_int, [_vp, _vp]),
+    "ctr_pages_describe": (ctypes.c_int, [_vp, ctypes.c_char_p, ctypes.c_size_t]),
+    "ctr_pages_destroy": (None, [_vp]),
     "ctr_sampler_create": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.c_int64, ctypes.c_int64,
                                           ctypes.c_int]),
     "ctr_sampler_forward": (ctypes.c_int, [_vp, _vp, ctypes.c_int64, _vp, ctypes.c_int64, _vp, _vp, _vp,
@@ -404,6 +445,10 @@ def ctr_attn_set_weights(plan, enable):
     _check(lib.ctr_attn_set_weights(plan, int(enable)), "ctr_attn_set_weights")
 
 
+def ctr_attn_set_chunks(plan, enable):
+    _check(lib.ctr_attn_set_chunks(plan, int(enable)), "ctr_attn_set_chunks")
+
+
 def ctr_attn_workspace_bytes(plan) -> int:
     return int(lib.ctr_attn_workspace_bytes(plan))
 
@@ -435,6 +480,17 @@ def ctr_attn_evict(plan, tables_ptr, lens_ptr, weights_ptr, dst_tables_ptr, dst_
                               weights_pitch, stream), "ctr_attn_evict")
 
 
+def ctr_attn_forward_chunk(plan, q_ptr, q_stride, T, tables_ptr, lens_ptr, starts_ptr, out_ptr, stream):
+    _check(lib.ctr_attn_forward_chunk(plan, q_ptr, q_stride, int(T), tables_ptr, lens_ptr, starts_ptr,
+                                      out_ptr, stream), "ctr_attn_forward_chunk")
+
+
+def ctr_attn_put(plan, rope, q_ptr, q_stride, k_ptr, v_ptr, kv_stride, positions_ptr, slots_ptr, T,
+                 q_out_ptr, q_out_stride, stream):
+    _check(lib.ctr_attn_put(plan, rope, q_ptr, q_stride, k_ptr, v_ptr, kv_stride, positions_ptr,
+                            slots_ptr, int(T), q_out_ptr, q_out_stride, stream), "ctr_attn_put")
+
+
 def ctr_attn_check(plan, stream):
     _check(lib.ctr_attn_check(plan, stream), "ctr_attn_check")
 
@@ -447,6 +503,109 @@ def ctr_attn_describe(plan) -> str:
 
 def ctr_attn_destroy(plan):
     lib.ctr_attn_destroy(plan)
+
+
+def ctr_rope_create(D, rotary_dim, dtype):
+    """Returns a rotary plan handle (int).  Raises CtrError on a non-OK status."""
+    h = _vp()
+    _check(lib.ctr_rope_create(ctypes.byref(h), int(D), int(rotary_dim), int(dtype)), "ctr_rope_create")
+    return h.value
+
+
+def ctr_rope_set_layout(plan, layout):
+    _check(lib.ctr_rope_set_layout(plan, int(layout)), "ctr_rope_set_layout")
+
+
+def ctr_rope_set_base(plan, base):
+    _check(lib.ctr_rope_set_base(plan, float(base)), "ctr_rope_set_base")
+
+
+def ctr_rope_set_scaling(plan, scaling, factor=1.0, original=0.0, low=0.0, high=0.0):
+    _check(lib.ctr_rope_set_scaling(plan, int(scaling), float(factor), float(original), float(low),
+                                    float(high)), "ctr_rope_set_scaling")
+
+
+def ctr_rope_set_magnitude(plan, magnitude):
+    _check(lib.ctr_rope_set_magnitude(plan, float(magnitude)), "ctr_rope_set_magnitude")
+
+
+def ctr_rope_set_frequencies(plan, frequencies):
+    n = len(frequencies)
+    _check(lib.ctr_rope_set_frequencies(plan, (ctypes.c_double * n)(*frequencies), n),
+           "ctr_rope_set_frequencies")
+
+
+def ctr_rope_frequencies(plan, n):
+    out = (ctypes.c_double * n)()
+    _check(lib.ctr_rope_frequencies(plan, out, n), "ctr_rope_frequencies")
+    return list(out)
+
+
+def ctr_rope_forward(plan, q_ptr, q_stride, H_q, k_ptr, k_stride, H_k, positions_ptr, T, q_out_ptr,
+                     q_out_stride, k_out_ptr, k_out_stride, stream):
+    _check(lib.ctr_rope_forward(plan, q_ptr, q_stride, H_q, k_ptr, k_stride, H_k, positions_ptr, int(T),
+                                q_out_ptr, q_out_stride, k_out_ptr, k_out_stride, stream),
+           "ctr_rope_forward")
+
+
+def ctr_rope_describe(plan) -> str:
+    buf = ctypes.create_string_buffer(256)
+    _check(lib.ctr_rope_describe(plan, buf, 256), "ctr_rope_describe")
+    return buf.value.decode()
+
+
+def ctr_rope_destroy(plan):
+    lib.ctr_rope_destroy(plan)
+
+
+def ctr_pages_create(B, page_size, max_pages):
+    """Returns a page plan handle (int).  Raises CtrError on a non-OK status."""
+    h = _vp()
+    _check(lib.ctr_pages_create(ctypes.byref(h), int(B), int(page_size), int(max_pages)),
+           "ctr_pages_create")
+    return h.value
+
+
+def ctr_pages_bind_list(plan, free_ptr, count_ptr, num_pages):
+    _check(lib.ctr_pages_bind_list(plan, free_ptr, count_ptr, int(num_pages)), "ctr_pages_bind_list")
+
+
+def ctr_pages_workspace_bytes(plan) -> int:
+    return int(lib.ctr_pages_workspace_bytes(plan))
+
+
+def ctr_pages_bind_workspace(plan, ptr, nbytes):
+    _check(lib.ctr_pages_bind_workspace(plan, ptr, int(nbytes)), "ctr_pages_bind_workspace")
+
+
+def ctr_pages_reset(plan, refill, stream):
+    _check(lib.ctr_pages_reset(plan, int(refill), stream), "ctr_pages_reset")
+
+
+def ctr_pages_reserve(plan, tables_ptr, lens_ptr, counts_ptr, rows, granted_ptr, starts_ptr, slots_ptr,
+                      positions_ptr, lens_out_ptr, stream):
+    _check(lib.ctr_pages_reserve(plan, tables_ptr, lens_ptr, counts_ptr, int(rows), granted_ptr,
+                                 starts_ptr, slots_ptr, positions_ptr, lens_out_ptr, stream),
+           "ctr_pages_reserve")
+
+
+def ctr_pages_release(plan, tables_ptr, lens_ptr, keep_ptr, lens_out_ptr, stream):
+    _check(lib.ctr_pages_release(plan, tables_ptr, lens_ptr, keep_ptr, lens_out_ptr, stream),
+           "ctr_pages_release")
+
+
+def ctr_pages_check(plan, stream):
+    _check(lib.ctr_pages_check(plan, stream), "ctr_pages_check")
+
+
+def ctr_pages_describe(plan) -> str:
+    buf = ctypes.create_string_buffer(256)
+    _check(lib.ctr_pages_describe(plan, buf, 256), "ctr_pages_describe")
+    return buf.value.decode()
+
+
+def ctr_pages_destroy(plan):
+    lib.ctr_pages_destroy(plan)
 
 
 def ctr_sampler_create(rows, vocab, dtype=CTR_F32):
@@ -807,7 +966,10 @@ def conv_transpose(x, w, bias=None, stride=1, padding=0, output_padding=0, negat
 
 
 def __getattr__(name):
-    """PagedAttention and Sampler, imported when first used (their module imports torch)."""
+    """The plans of the decode step, imported when first used (their modules import torch)."""
+    if name in ("Rotary", "PagePool"):
+        from . import prompt
+        return getattr(prompt, name)
     if name in ("PagedAttention", "Sampler"):
         from . import decode
         return getattr(decode, name)

@@ -1,0 +1,98 @@
+// chunk_device.cuh -- device helpers shared by the chunk attention's kernels.
+#pragma once
+
+#include "chunk_schedule.cuh"
+
+namespace ctr {
+namespace chunk {
+
+constexpr float kNegInf = -__builtin_inff();
+
+// 2^x with a relative error of 2^-22; 0 at -inf.
+__device__ __forceinline__ float pow2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// What a sum whose maximum was m is worth under a larger base: never 0 unless it is empty, so that an infinite
+// output stays infinite.
+__device__ __forceinline__ float shrink_of(float m, float base) {
+    return m == kNegInf ? 0.0f : fmaxf(pow2(m - base), 1.17549435e-38f);
+}
+
+// Where row r of a unit is in q and in the output.
+template <typename U> __device__ __forceinline__ int64_t query_offset(const ChunkParams &p, const U &u, int r) {
+    const int row = u.r0 + r, tok = row / p.G;
+    return (u.s.row0 + (int64_t)tok) * p.q_stride + (int64_t)(u.hk * p.G + row - tok * p.G) * p.D;
+}
+template <typename U> __device__ __forceinline__ int64_t output_offset(const ChunkParams &p, const U &u, int r) {
+    const int row = u.r0 + r, tok = row / p.G;
+    return ((u.s.row0 + (int64_t)tok) * p.Hq + u.hk * p.G + row - tok * p.G) * p.D;
+}
+
+// First element of a unit's slot j, or -1 for slots that no row of it attends to (their pages may
+// be gone) and for pages out of range, which are reported.
+template <typename U> __device__ __forceinline__ int64_t cache_row(const ChunkParams &p, const U &u, int j) {
+    if (j < u.lo || j >= u.hi) return -1;
+    const int at = p.page_shift >= 0 ? j >> p.page_shift : j / p.cache.page;
+    const int pg = p.cache.tables[(int64_t)u.b * p.cache.table_pitch + at];
+    if ((unsigned)pg >= (unsigned)p.cache.num_pages) {
+        atomicOr(p.cache.status, kStatusBadPage);
+        return -1;
+    }
+    return pg * p.cache.page_stride + u.hk * p.cache.head_stride +
+           (int64_t)(j - at * p.cache.page) * p.cache.row_stride;
+}
+
+// Whether some row does not attend to all of the slots [j0, j0 + n).
+template <typename U> __device__ __forceinline__ bool is_edge(const U &u, int j0, int n) {
+    return j0 < u.lo_last || j0 + n > u.hi_first;
+}
+
+template <typename T> __device__ __forceinline__ float widen(T v);
+template <> __device__ __forceinline__ float widen(float v) { return v; }
+template <> __device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <> __device__ __forceinline__ float widen(__half v) { return __half2float(v); }
+template <typename T> __device__ __forceinline__ T round_to(float v);
+template <> __device__ __forceinline__ float round_to(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 round_to(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half round_to(float v) { return __float2half_rn(v); }
+
+__device__ __forceinline__ void store8(float *to, const float (&v)[8]) {
+    reinterpret_cast<float4 *>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4 *>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+template <typename T> __device__ __forceinline__ void store8(T *to, const float (&v)[8]) {
+    __align__(16) T x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = round_to<T>(v[i]);
+    *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<uint4 *>(x);
+}
+
+// A tile's products take all its slots for all its rows, and 0 times an infinity or NaN of a slot
+// that a row does not attend to would be NaN.  So infinities and NaN are taken out of V in the tiles that
+// some row attends to in part, and the unit is marked.  This is what they add to one output: the
+// infinities and NaN among the slots [lo, hi) of those tiles of the segment.
+template <typename T, int NT, typename U>
+__device__ __noinline__ float taint(const ChunkParams &p, const U &u, int t0, int t1, int lo, int hi, int d) {
+    float sum = 0.0f;
+    for (int tile = t0; tile < t1; ++tile) {
+        const int j0 = (u.first + tile) * NT;
+        if (!is_edge(u, j0, NT)) continue;
+        for (int j = max(lo, j0); j < min(hi, j0 + NT); ++j) {
+            const int64_t at = cache_row(p, u, j);
+            const float v = at < 0 ? 0.0f : widen(((const T *)p.v)[at + d]);
+            if (!isfinite(v)) sum += v;
+        }
+    }
+    return sum;
+}
+template <typename T, int MT, int NT>
+__device__ __forceinline__ float taint_of(const ChunkParams &p, const Unit<MT, NT> &u, int t0, int t1, int lo,
+                                          int hi, int d) {
+    return taint<T, NT>(p, u, t0, t1, lo, hi, d);
+}
+
+}  // namespace chunk
+}  // namespace ctr

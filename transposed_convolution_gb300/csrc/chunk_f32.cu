@@ -1,0 +1,305 @@
+// chunk_f32.cu -- attention of a chunk of new tokens over a paged fp32 cache, and the join of the
+// parts of units that several blocks share (all types).
+//
+// Two products of 64 rows by 64 slots by D a tile, as fp32 multiply-adds on the CUDA cores, which bound
+// it: a thread has 4 x 4 scores and 4 x D / 16 outputs, so that 64 multiply-adds go to eight 16-byte
+// loads from shared memory.  (The tensor pipe's accumulation, even of tf32 terms that add up to fp32,
+// truncates, which would cost the result digits.)
+#include <algorithm>
+
+#include "chunk_device.cuh"
+
+namespace ctr {
+namespace chunk {
+
+constexpr int kRows = 64, kSlots = 64, kThreads = 256;
+
+// Floats of shared memory: Q and K rows (16-byte reads of eight rows fall into different banks), V rows; P
+// takes K's place.
+__host__ __device__ constexpr int row_pitch(int D) { return D + 4; }
+constexpr int kPPitch = kSlots + 4;
+inline size_t smem_bytes(int D, int DP) {
+    return sizeof(float) * ((size_t)kRows * row_pitch(D) + std::max(kSlots * row_pitch(D), kRows * kPPitch) +
+                            (size_t)kSlots * DP);
+}
+
+template <typename T> __device__ __forceinline__ float4 load4(const T *from);
+template <> __device__ __forceinline__ float4 load4(const float *from) {
+    return *reinterpret_cast<const float4 *>(from);
+}
+template <> __device__ __forceinline__ float4 load4(const __nv_bfloat16 *from) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(from);
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
+template <> __device__ __forceinline__ float4 load4(const __half *from) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(from);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&u.x)),
+                 b = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// NC: columns a thread has, of up to 16 NC.  Thread (ty, tx) has rows 4 ty .. 4 ty + 3, slots tx + 16 j
+// and columns tx * 4 + 64 j .. + 3 (tx + 16 c where NC is no multiple of four).
+template <int NC> __device__ __forceinline__ int column(int tx, int c) {
+    return NC % 4 == 0 ? tx * 4 + c / 4 * 64 + c % 4 : tx + 16 * c;
+}
+
+template <typename T, int NC> __global__ void __launch_bounds__(kThreads) chunk_kernel(ChunkParams p) {
+    constexpr int DP = 16 * NC;
+    extern __shared__ __align__(16) float smem[];
+    __shared__ int64_t costs[kMaxB + 1];
+    __shared__ Start start;
+    __shared__ int visible[kSlots];
+    __shared__ int tainted;
+    const int D = p.D, pitch = row_pitch(D), t = threadIdx.x, tx = t % 16, ty = t / 16;
+    float *const sq = smem, *const sk = sq + kRows * pitch;
+    float *const sp = sk, *const sv = sk + max(kSlots * pitch, kRows * kPPitch);
+    ptx::griddep_wait();
+    find_start<kRows, kSlots>(p, costs, &start);
+    Walk<kRows, kSlots> walk;
+    walk.start(p, start);
+    int4 head = make_int4(0, 0, 0, 0);
+    // Columns past D stay zero in V.
+    for (int i = t; i < kSlots * (DP - D); i += kThreads) sv[i / (DP - D) * DP + D + i % (DP - D)] = 0.0f;
+    while (walk.next(p)) {
+        const Unit<kRows, kSlots> &u = walk.u;
+        __syncthreads();                 // the segment before is done with Q
+        for (int i = t; i < kRows * (D / 4); i += kThreads) {
+            const int r = i / (D / 4), d = i % (D / 4) * 4;
+            const float4 x = r < u.rows ? load4((const T *)p.q + query_offset(p, u, r) + d)
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+            *reinterpret_cast<float4 *>(sq + r * pitch + d) = x;
+        }
+        if (t == 0) tainted = 0;
+        int lo[4], hi[4];                // slots that this thread's rows attend to
+        float m[4], l[4], o[4][NC];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = ty * 4 + i;
+            hi[i] = r < u.rows ? end_slot(p, u.s, (u.r0 + r) / p.G) : 0;
+            lo[i] = first_slot(p, hi[i]);
+            m[i] = kNegInf;
+            l[i] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) o[i][c] = 0.0f;
+        }
+        for (int tile = walk.t0; tile < walk.t1; ++tile) {
+            const int j0 = (u.first + tile) * kSlots;
+            const bool edge = is_edge(u, j0, kSlots);
+            __syncthreads();             // the tile before is done with K, V and P
+            int hidden = 0;
+            {
+                // Four threads a slot.
+                const int r = t / 4, j = j0 + r;
+                const int64_t at = cache_row(p, u, j);
+                hidden = at < 0 && j >= u.lo && j < u.hi;
+                if (t % 4 == 0) visible[r] = at >= 0;
+                for (int d = t % 4 * 4; d < D; d += 16) {
+                    float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
+                    if (at >= 0) {
+                        k = load4((const T *)p.k + at + d);
+                        v = load4((const T *)p.v + at + d);
+                        if (edge && !(isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w))) {
+                            tainted = 1;
+                            v.x = isfinite(v.x) ? v.x : 0.0f;
+                            v.y = isfinite(v.y) ? v.y : 0.0f;
+                            v.z = isfinite(v.z) ? v.z : 0.0f;
+                            v.w = isfinite(v.w) ? v.w : 0.0f;
+                        }
+                    }
+                    *reinterpret_cast<float4 *>(sk + r * pitch + d) = k;
+                    *reinterpret_cast<float4 *>(sv + r * DP + d) = v;
+                }
+            }
+            const bool masked = __syncthreads_or(hidden) || edge;
+            float s[4][4] = {};
+            for (int d = 0; d < D; d += 4) {
+                float4 a[4], b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<float4 *>(sq + (ty * 4 + i) * pitch + d);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<float4 *>(sk + (tx + 16 * j) * pitch + d);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
+                        s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
+                        s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
+                        s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+                    }
+            }
+            float shrink[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float top = kNegInf;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[i][j] *= p.scale_log2;
+                    if (masked) {
+                        const int at = j0 + tx + 16 * j;
+                        if (at < lo[i] || at >= hi[i] || !visible[tx + 16 * j]) s[i][j] = kNegInf;
+                    }
+                    top = fmaxf(top, s[i][j]);
+                }
+#pragma unroll
+                for (int d = 8; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                top = fmaxf(top, m[i]);
+                const float base = top == kNegInf ? 0.0f : top;
+                shrink[i] = shrink_of(m[i], base);
+                m[i] = top;
+                float sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[i][j] = pow2(s[i][j] - base);
+                    sum += s[i][j];
+                }
+                l[i] = l[i] * shrink[i] + sum;
+            }
+            __syncthreads();             // all have read K
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sp[(ty * 4 + i) * kPPitch + tx + 16 * j] = s[i][j];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < NC; ++c) o[i][c] *= shrink[i];
+            __syncwarp();                // a warp reads the rows that it wrote
+            for (int j = 0; j < kSlots; j += 4) {
+                float4 a[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<float4 *>(sp + (ty * 4 + i) * kPPitch + j);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float b[NC];
+                    if (NC % 4 == 0) {
+#pragma unroll
+                        for (int c = 0; c < NC / 4; ++c)
+                            *reinterpret_cast<float4 *>(b + 4 * c) =
+                                *reinterpret_cast<float4 *>(sv + (j + e) * DP + tx * 4 + 64 * c);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) b[c] = sv[(j + e) * DP + tx + 16 * c];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float x = e == 0 ? a[i].x : e == 1 ? a[i].y : e == 2 ? a[i].z : a[i].w;
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) o[i][c] = fmaf(x, b[c], o[i][c]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int d = 8; d > 0; d /= 2) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+        if (tainted)
+            for (int i = 0; i < 4; ++i)
+                for (int c = 0; c < NC; ++c)
+                    if (column<NC>(tx, c) < D)
+                        o[i][c] += taint_of<T>(p, u, walk.t0, walk.t1, lo[i], hi[i], column<NC>(tx, c));
+        if (walk.part) {
+            const int64_t slot = walk.slot();
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                if (column<NC>(tx, c) < D)
+                    *reinterpret_cast<float4 *>(p.part_o + (slot * D + column<NC>(tx, c)) * kRows + ty * 4) =
+                        make_float4(o[0][c], o[1][c], o[2][c], o[3][c]);
+            if (tx == 0)
+                for (int i = 0; i < 4; ++i)
+                    p.part_ml[slot * kRows + ty * 4 + i] = make_float2(m[i], l[i]);
+            if (walk.begins) head = make_int4(u.b, u.hk, u.m, walk.parts());
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (ty * 4 + i >= u.rows) continue;
+                T *to = (T *)p.out + output_offset(p, u, ty * 4 + i);
+                const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    if (column<NC>(tx, c) < D) to[column<NC>(tx, c)] = round_to<T>(o[i][c] * inv);
+            }
+        }
+    }
+    if (t == 0 && !p.whole) p.heads[blockIdx.x] = head;
+}
+
+// Joins the parts of the unit that block x of the attention began, thirty-two rows a block: a thread
+// has a row and eight columns at a time.  What it reads is mostly in L2.
+template <typename T, int MT> __global__ void __launch_bounds__(256) join_kernel(ChunkParams p) {
+    ptx::griddep_wait();
+    const int4 head = p.heads[blockIdx.x];
+    if (head.w == 0) return;
+    Unit<MT, 64> u;
+    u.b = head.x;
+    u.hk = head.y;
+    u.m = head.z;
+    u.s = sequence_of(p, u.b, false);
+    u.tile(p);
+    const int r = blockIdx.y * 32 + threadIdx.x % 32;
+    if (r >= u.rows) return;
+    const int64_t first = 2 * (int64_t)blockIdx.x + 1;
+    float M = kNegInf, L = 0.0f;
+    for (int i = 0; i < head.w; ++i)
+        M = fmaxf(M, p.part_ml[(i == 0 ? first : first - 1 + 2 * i) * MT + r].x);
+    const float base = M == kNegInf ? 0.0f : M;
+    for (int i = 0; i < head.w; ++i) {
+        const float2 ml = p.part_ml[(i == 0 ? first : first - 1 + 2 * i) * MT + r];
+        L += ml.y * shrink_of(ml.x, base);
+    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    T *to = (T *)p.out + output_offset(p, u, r);
+    for (int d = threadIdx.x / 32 * 8; d < p.D; d += 64) {
+        float o[8] = {};
+        for (int i = 0; i < head.w; ++i) {
+            const int64_t slot = i == 0 ? first : first - 1 + 2 * i;
+            const float w = shrink_of(p.part_ml[slot * MT + r].x, base);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] += w * p.part_o[(slot * p.D + d + e) * MT + r];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= inv;
+        store8(to + d, o);
+    }
+}
+
+template <typename T, int NC> cudaError_t launch(const ctr_attn_s *pl, const ChunkParams &p, cudaStream_t st) {
+    static PerDeviceOnce once;
+    const auto kernel = chunk_kernel<T, NC>;
+    cudaError_t e = once.run(current_device(), cudaSuccess, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)smem_bytes(16 * NC, 16 * NC));
+    });
+    if (e != cudaSuccess) return e;
+    const int grid = pl->num_sms * chunk_shape(pl->dtype, pl->D).per_sm;
+    count_launches(1);
+    e = launch_pdl(kernel, dim3((unsigned)grid), dim3(kThreads), smem_bytes(p.D, 16 * NC), st, p);
+    if (e != cudaSuccess || p.whole) return e;
+    count_launches(1);
+    return launch_pdl(join_kernel<T, kRows>, dim3((unsigned)grid, kRows / 32), dim3(256), 0, st, p);
+}
+
+template <typename T> cudaError_t launch_any(const ctr_attn_s *pl, const ChunkParams &p, cudaStream_t st) {
+    if (p.D <= 64) return launch<T, 4>(pl, p, st);
+    if (p.D <= 80) return launch<T, 5>(pl, p, st);
+    if (p.D <= 96) return launch<T, 6>(pl, p, st);
+    if (p.D <= 128) return launch<T, 8>(pl, p, st);
+    return launch<T, 16>(pl, p, st);
+}
+
+}  // namespace chunk
+
+ChunkShape chunk_shape(int, int64_t D) {
+    return {chunk::kRows, chunk::kSlots, D <= 128 ? 2 : 1};
+}
+
+cudaError_t launch_chunk(const ctr_attn_s *pl, const ChunkParams &p, cudaStream_t st) {
+    return pl->dtype == CTR_F32    ? chunk::launch_any<float>(pl, p, st)
+           : pl->dtype == CTR_BF16 ? chunk::launch_any<__nv_bfloat16>(pl, p, st)
+                                   : chunk::launch_any<__half>(pl, p, st);
+}
+
+}  // namespace ctr

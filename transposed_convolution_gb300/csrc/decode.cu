@@ -30,24 +30,18 @@ void layout_workspace(ctr_attn_s *pl) {
         pl->ws_needed = pl->off_scores +
                         (size_t)(pl->B * pl->Hq) * (size_t)pl->score_pitch * sizeof(float);
     }
+    if (pl->chunks) {
+        // As for the decode step's parts: two to a block, and of each block the unit it begins.
+        const ctr::ChunkShape s = ctr::chunk_shape(pl->dtype, pl->D);
+        const int64_t blocks = (int64_t)pl->num_sms * s.per_sm;
+        pl->off_chunk_o = align256(pl->ws_needed);
+        pl->off_chunk_ml = pl->off_chunk_o + align256((size_t)(2 * blocks * s.rows * pl->D) * sizeof(float));
+        pl->off_chunk_heads = pl->off_chunk_ml + align256((size_t)(2 * blocks * s.rows) * sizeof(float2));
+        pl->ws_needed = pl->off_chunk_heads + align256((size_t)blocks * sizeof(int4));
+    }
     pl->ws = nullptr;
     pl->ws_bytes = 0;
     pl->ready = 0;
-}
-
-ctr::CacheView cache_view(const ctr_attn_s *pl, const int32_t *tables, const int32_t *lens) {
-    ctr::CacheView c = {};
-    c.tables = tables;
-    c.lens = lens;
-    c.page_stride = pl->Hkv * pl->page * pl->D;
-    c.head_stride = pl->layout == CTR_CACHE_HEAD_MAJOR ? pl->page * pl->D : pl->D;
-    c.row_stride = pl->layout == CTR_CACHE_HEAD_MAJOR ? pl->D : pl->Hkv * pl->D;
-    c.table_pitch = (int)pl->max_pages;
-    c.page = (int)pl->page;
-    c.num_pages = (int)pl->num_pages;
-    c.cap = (int)(pl->max_pages * pl->page);
-    c.status = static_cast<uint32_t *>(pl->ws);
-    return c;
 }
 
 }  // namespace
@@ -109,6 +103,13 @@ ctr_status ctr_attn_set_weights(ctr_attn_t pl, int enable) {
     return CTR_OK;
 }
 
+ctr_status ctr_attn_set_chunks(ctr_attn_t pl, int enable) {
+    if (!pl || (enable != 0 && enable != 1)) return CTR_ERR_INVALID_ARG;
+    pl->chunks = enable;
+    layout_workspace(pl);
+    return CTR_OK;
+}
+
 size_t ctr_attn_workspace_bytes(ctr_attn_t pl) { return pl ? pl->ws_needed : 0; }
 
 ctr_status ctr_attn_bind_workspace(ctr_attn_t pl, void *ws, size_t bytes) {
@@ -159,7 +160,7 @@ ctr_status ctr_attn_forward(ctr_attn_t pl, const void *q, int64_t q_stride, cons
     if (!pl->ws) return CTR_ERR_NO_WORKSPACE;
     if (!pl->ready) return CTR_ERR_NOT_PREPARED;
     ctr::AttnParams p = {};
-    p.cache = cache_view(pl, tables, lens);
+    p.cache = ctr::cache_view(pl, tables, lens);
     p.k = pl->k_pages;
     p.v = pl->v_pages;
     p.q = q;
@@ -178,9 +179,7 @@ ctr_status ctr_attn_forward(ctr_attn_t pl, const void *q, int64_t q_stride, cons
     }
     p.whole_units = pl->max_pages * pl->page <= ctr::kWholeSlots;
     p.score_pitch = pl->score_pitch;
-    p.page_shift = -1;
-    for (int s = 0; s < 29; ++s)
-        if (pl->page == (int64_t)1 << s) p.page_shift = s;
+    p.page_shift = ctr::page_shift(pl->page);
     p.w_in = weights_in;
     p.w_out = weights_out;
     p.B = (int)pl->B;
@@ -192,6 +191,44 @@ ctr_status ctr_attn_forward(ctr_attn_t pl, const void *q, int64_t q_stride, cons
     p.scale_log2 = (float)((double)pl->scale * 1.4426950408889634);
     return ctr::launch_attention(pl, p, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? CTR_OK : CTR_ERR_CUDA;
+}
+
+ctr_status ctr_attn_forward_chunk(ctr_attn_t pl, const void *q, int64_t q_stride, int64_t T,
+                                  const int32_t *tables, const int32_t *lens, const int32_t *starts,
+                                  void *out, void *stream) {
+    if (!pl || T < 0 || !tables || !lens || !starts || (T && (!q || !out || q_stride < pl->Hq * pl->D)))
+        return CTR_ERR_INVALID_ARG;
+    if (T > ((int64_t)1 << 24) || T * (pl->Hq / pl->Hkv) > ((int64_t)1 << 30)) return CTR_ERR_UNSUPPORTED;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(tables, 4) || !aligned(lens, 4) ||
+        !aligned(starts, 4) || (T && q_stride * esize_of(pl) % 16))
+        return CTR_ERR_MISALIGNED;
+    if (!pl->k_pages || !pl->chunks) return CTR_ERR_NOT_PREPARED;
+    if (!pl->ws) return CTR_ERR_NO_WORKSPACE;
+    if (!pl->ready) return CTR_ERR_NOT_PREPARED;
+    if (T == 0) return CTR_OK;
+    ctr::ChunkParams p = {};
+    p.cache = ctr::cache_view(pl, tables, lens);
+    p.k = pl->k_pages;
+    p.v = pl->v_pages;
+    p.q = q;
+    p.q_stride = q_stride;
+    p.T = T;
+    p.starts = starts;
+    p.out = out;
+    char *ws = static_cast<char *>(pl->ws);
+    p.part_o = reinterpret_cast<float *>(ws + pl->off_chunk_o);
+    p.part_ml = reinterpret_cast<float2 *>(ws + pl->off_chunk_ml);
+    p.heads = reinterpret_cast<int4 *>(ws + pl->off_chunk_heads);
+    p.B = (int)pl->B;
+    p.Hq = (int)pl->Hq;
+    p.Hkv = (int)pl->Hkv;
+    p.G = (int)(pl->Hq / pl->Hkv);
+    p.D = (int)pl->D;
+    p.window = pl->window;
+    p.scale_log2 = (float)((double)pl->scale * 1.4426950408889634);
+    p.page_shift = ctr::page_shift(pl->page);
+    p.whole = pl->max_pages * pl->page <= ctr::kWholeSlots;
+    return ctr::launch_chunk(pl, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CTR_OK : CTR_ERR_CUDA;
 }
 
 ctr_status ctr_attn_evict(ctr_attn_t pl, const int32_t *tables, const int32_t *lens,
@@ -214,7 +251,7 @@ ctr_status ctr_attn_evict(ctr_attn_t pl, const int32_t *tables, const int32_t *l
     if (!pl->ws) return CTR_ERR_NO_WORKSPACE;
     if (!pl->ready) return CTR_ERR_NOT_PREPARED;
     ctr::EvictParams p = {};
-    p.cache = cache_view(pl, tables, lens);
+    p.cache = ctr::cache_view(pl, tables, lens);
     p.k = pl->k_pages;
     p.v = pl->v_pages;
     p.w = weights;
@@ -240,26 +277,17 @@ ctr_status ctr_attn_check(ctr_attn_t pl, void *stream) {
     if (!pl) return CTR_ERR_INVALID_ARG;
     if (!pl->ws) return CTR_ERR_NO_WORKSPACE;
     if (!pl->ready) return CTR_ERR_NOT_PREPARED;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    uint32_t v = 0;
-    if (cudaMemcpyAsync(&v, pl->ws, sizeof v, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
-        cudaStreamSynchronize(st) != cudaSuccess)
-        return CTR_ERR_CUDA;
-    if (!v) return CTR_OK;
-    if (cudaMemsetAsync(pl->ws, 0, sizeof v, st) != cudaSuccess ||
-        cudaStreamSynchronize(st) != cudaSuccess)
-        return CTR_ERR_CUDA;
-    return CTR_ERR_INVALID_ARG;
+    return ctr::check_status(pl->ws, static_cast<cudaStream_t>(stream));
 }
 
 ctr_status ctr_attn_describe(ctr_attn_t pl, char *buf, size_t len) {
     if (!pl || !buf || len == 0) return CTR_ERR_INVALID_ARG;
     static const char *names[] = {"f32", "bf16", "f16"};
     snprintf(buf, len, "attention %s B=%lld Hq=%lld Hkv=%lld D=%lld page=%lld max_pages=%lld %s "
-             "window=%lld weights=%d ws=%zu", names[pl->dtype], (long long)pl->B, (long long)pl->Hq,
+             "window=%lld weights=%d%s ws=%zu", names[pl->dtype], (long long)pl->B, (long long)pl->Hq,
              (long long)pl->Hkv, (long long)pl->D, (long long)pl->page, (long long)pl->max_pages,
              pl->layout == CTR_CACHE_HEAD_MAJOR ? "head-major" : "token-major",
-             (long long)pl->window, pl->weights, pl->ws_needed);
+             (long long)pl->window, pl->weights, pl->chunks ? " chunks" : "", pl->ws_needed);
     return CTR_OK;
 }
 

@@ -1,6 +1,6 @@
-"""Torch-level plans of the decode step: ``PagedAttention`` (attention of one new token over a
-paged key-value cache, and eviction from that cache) and ``Sampler`` (the next token from logits
-and given random numbers).
+"""Torch-level plans of the decode step: ``PagedAttention`` (attention of one new token, or of a
+chunk of them, over a paged key-value cache, and eviction from that cache) and ``Sampler`` (the next
+token from logits and given random numbers).
 
 Both only marshal arguments to the C ABI (``include/ctr.h``: ``ctr_attn_*``, ``ctr_sampler_*``)
 after checking them.  A call runs on ``stream`` (default: the current stream of the plan's
@@ -98,12 +98,13 @@ class PagedAttention(_DecodePlan):
     "head") or [num_pages, page_size, H_kv, D] ("token"): given, or allocated (zeros) when only
     ``num_pages`` is.  Slot j of sequence b is row j % page_size of page
     ``tables[b, j // page_size]``.  ``window`` > 0 attends to the last that many slots;
-    ``weights`` accumulates every slot's attention weight, for ``evict``.
+    ``weights`` accumulates every slot's attention weight, for ``evict``; ``chunks`` makes room for
+    ``forward_chunk``.
     """
 
     def __init__(self, B, H_q, H_kv, D, page_size, max_pages, num_pages=None, k_pages=None,
                  v_pages=None, dtype=None, layout="head", window=0, scale=None, weights=False,
-                 device=None):
+                 device=None, chunks=False):
         if layout not in ("head", "token"):
             raise ValueError("layout must be 'head' or 'token'")
         if (k_pages is None) != (v_pages is None):
@@ -121,6 +122,7 @@ class PagedAttention(_DecodePlan):
         self.page_size, self.max_pages = int(page_size), int(max_pages)
         self.num_pages, self.capacity = int(num_pages), int(page_size) * int(max_pages)
         self.layout, self.window, self.weights = layout, int(window), bool(weights)
+        self.chunks = bool(chunks)
         shape = ((self.num_pages, self.H_kv, self.page_size, self.D) if layout == "head" else
                  (self.num_pages, self.page_size, self.H_kv, self.D))
         self.handle = _ctr.ctr_attn_create(B, H_q, H_kv, D, page_size, max_pages,
@@ -134,6 +136,8 @@ class PagedAttention(_DecodePlan):
                 _ctr.ctr_attn_set_scale(self.handle, scale)
             if self.weights:
                 _ctr.ctr_attn_set_weights(self.handle, 1)
+            if self.chunks:
+                _ctr.ctr_attn_set_chunks(self.handle, 1)
             if k_pages is None:
                 k_pages = torch.zeros(shape, dtype=self.dtype, device=self.device)
                 v_pages = torch.zeros(shape, dtype=self.dtype, device=self.device)
@@ -151,6 +155,9 @@ class PagedAttention(_DecodePlan):
             self._weights_shape = (self.B, self.H_kv, self.capacity)
             self._forward = _ctr.load_library().ctr_attn_forward
             self._evict = _ctr.load_library().ctr_attn_evict
+            self._forward_chunk = _ctr.load_library().ctr_attn_forward_chunk
+            self._put = _ctr.load_library().ctr_attn_put
+            self._starts_shape = (self.B + 1,)
             with torch.cuda.device(self.device):
                 _ctr.ctr_attn_reset(self.handle, self._stream(None))
                 # The plan may be used on any stream from here on.
@@ -203,6 +210,74 @@ class PagedAttention(_DecodePlan):
             raise _ctr.CtrError(st, "ctr_attn_forward")
         return out
 
+    def put(self, k, v, slots, q=None, positions=None, rotary=None, q_out=None, stream=None):
+        """Put the K and V rows of new tokens, k and v [T, H_kv, D], into the cache at slots [T]
+        (int64, page * page_size + row; negative: nowhere).  ``rotary`` (a ``Rotary`` plan of this D
+        and dtype) turns K by positions [T] (int32) on the way, and q [T, H_q, D], which the call then
+        returns turned (in q_out, which may be q).  k, v and q may be slices of a fused projection."""
+        T = k.shape[0] if k.dim() else 0
+        shape = (T, self.H_kv, self.D)
+        k_ptr, kv_stride = self._rows_at(k, "k", shape, self.dtype)
+        v_ptr, v_stride = self._rows_at(v, "v", shape, self.dtype)
+        if v_stride != kv_stride:
+            raise ValueError("k and v must have the same row stride")
+        s_ptr = self._at(slots, "slots", (T,), torch.int64)
+        p_ptr = r_ptr = q_ptr = o_ptr = None
+        q_stride = o_stride = 0
+        made = ()
+        if rotary is not None:
+            if positions is None:
+                raise ValueError("a rotary plan needs positions")
+            if rotary.D != self.D or rotary.dtype is not self.dtype:
+                raise ValueError("the rotary plan has D = %d, %s, the cache D = %d, %s"
+                                 % (rotary.D, rotary.dtype, self.D, self.dtype))
+            p_ptr = self._at(positions, "positions", (T,), torch.int32)
+            r_ptr = rotary.handle
+        elif positions is not None:
+            raise ValueError("positions without a rotary plan")
+        if q is not None:
+            if rotary is None:
+                raise ValueError("q without a rotary plan")
+            shape = (T, self.H_q, self.D)
+            q_ptr, q_stride = self._rows_at(q, "q", shape, self.dtype)
+            if q_out is None:
+                q_out = torch.empty(shape, dtype=self.dtype, device=self.device)
+                made = (q_out,)
+            o_ptr, o_stride = self._rows_at(q_out, "q_out", shape, self.dtype)
+            if not T:
+                q_ptr = o_ptr = None
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        st = self._put(self.handle, r_ptr, q_ptr, q_stride, k_ptr, v_ptr, kv_stride, p_ptr, s_ptr, T,
+                       o_ptr, o_stride, self._stream(stream, *made))
+        if st:
+            raise _ctr.CtrError(st, "ctr_attn_put")
+        return q_out
+
+    def forward_chunk(self, q, tables, lens, starts, out=None, stream=None):
+        """out [T, H_q, D] of q [T, H_q, D], whose rows starts[b] .. starts[b + 1] - 1 are the new tokens
+        of sequence b, at the slots from lens[b] on, where ``put`` has put their K and V: each attends
+        to the slots up to its own (the last ``window`` of them).  tables [B, max_pages], lens [B] and
+        starts [B + 1] are int32; lens[b] < 0 marks an idle sequence, whose rows give 0.  q may be a
+        slice of a fused projection.  Rows of ``out`` that no sequence has are left as they are (anything,
+        in a tensor that the call makes)."""
+        T = q.shape[0] if q.dim() else 0
+        shape = (T, self.H_q, self.D)
+        q_ptr, q_stride = self._rows_at(q, "q", shape, self.dtype)
+        t_ptr = self._at(tables, "tables", self._table_shape, torch.int32)
+        l_ptr = self._at(lens, "lens", self._lens_shape, torch.int32)
+        s_ptr = self._at(starts, "starts", self._starts_shape, torch.int32)
+        if out is None:
+            out = torch.empty(shape, dtype=self.dtype, device=self.device)
+            raw = self._stream(stream, out)
+        else:
+            raw = self._stream(stream)
+        st = self._forward_chunk(self.handle, q_ptr, q_stride, T, t_ptr, l_ptr, s_ptr,
+                                 self._at(out, "out", shape, self.dtype), raw)
+        if st:
+            raise _ctr.CtrError(st, "ctr_attn_forward_chunk")
+        return out
+
     def evict(self, tables, lens, weights, dst_tables, budget, sinks=0, recent=0, slots=None,
               lens_out=None, weights_out=None, stream=None):
         """Keep ``budget`` slots of every (sequence, head) -- the first ``sinks``, the last
@@ -247,8 +322,8 @@ class PagedAttention(_DecodePlan):
         return slots, lens_out, weights_out
 
     def check(self, stream=None):
-        """Wait for ``stream`` and raise CtrError when a call met a page number or a length out
-        of range."""
+        """Wait for ``stream`` and raise CtrError when a call met a page number, a slot, a length or
+        a start out of range."""
         _ctr.ctr_attn_check(self.handle, self._stream(stream))
 
     def describe(self) -> str:
