@@ -1,5 +1,4 @@
-// chunk_f32.cu -- attention of a chunk of new tokens over a paged fp32 cache, and the join of the
-// parts of units that several blocks share (all types).
+// chunk_f32.cu -- attention of a chunk of new tokens over a paged fp32 cache.
 //
 // Two products of 64 rows by 64 slots by D a tile, as fp32 multiply-adds on the CUDA cores, which bound
 // it: a thread has 4 x 4 scores and 4 x D / 16 outputs, so that 64 multiply-adds go to eight 16-byte
@@ -8,6 +7,7 @@
 #include <algorithm>
 
 #include "chunk_device.cuh"
+#include "chunk_join.cuh"
 
 namespace ctr {
 namespace chunk {
@@ -23,21 +23,7 @@ inline size_t smem_bytes(int D, int DP) {
                             (size_t)kSlots * DP);
 }
 
-template <typename T> __device__ __forceinline__ float4 load4(const T *from);
-template <> __device__ __forceinline__ float4 load4(const float *from) {
-    return *reinterpret_cast<const float4 *>(from);
-}
-template <> __device__ __forceinline__ float4 load4(const __nv_bfloat16 *from) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(from);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-}
-template <> __device__ __forceinline__ float4 load4(const __half *from) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(from);
-    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&u.x)),
-                 b = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
-    return make_float4(a.x, a.y, b.x, b.y);
-}
+__device__ __forceinline__ float4 load4(const float *from) { return *reinterpret_cast<const float4 *>(from); }
 
 // NC: columns a thread has, of up to 16 NC.  Thread (ty, tx) has rows 4 ty .. 4 ty + 3, slots tx + 16 j
 // and columns tx * 4 + 64 j .. + 3 (tx + 16 c where NC is no multiple of four).
@@ -45,7 +31,7 @@ template <int NC> __device__ __forceinline__ int column(int tx, int c) {
     return NC % 4 == 0 ? tx * 4 + c / 4 * 64 + c % 4 : tx + 16 * c;
 }
 
-template <typename T, int NC> __global__ void __launch_bounds__(kThreads) chunk_kernel(ChunkParams p) {
+template <int NC> __global__ void __launch_bounds__(kThreads) chunk_kernel(ChunkParams p) {
     constexpr int DP = 16 * NC;
     extern __shared__ __align__(16) float smem[];
     __shared__ int64_t costs[kMaxB + 1];
@@ -67,7 +53,7 @@ template <typename T, int NC> __global__ void __launch_bounds__(kThreads) chunk_
         __syncthreads();                 // the segment before is done with Q
         for (int i = t; i < kRows * (D / 4); i += kThreads) {
             const int r = i / (D / 4), d = i % (D / 4) * 4;
-            const float4 x = r < u.rows ? load4((const T *)p.q + query_offset(p, u, r) + d)
+            const float4 x = r < u.rows ? load4((const float *)p.q + query_offset(p, u, r) + d)
                                         : make_float4(0.f, 0.f, 0.f, 0.f);
             *reinterpret_cast<float4 *>(sq + r * pitch + d) = x;
         }
@@ -98,8 +84,8 @@ template <typename T, int NC> __global__ void __launch_bounds__(kThreads) chunk_
                 for (int d = t % 4 * 4; d < D; d += 16) {
                     float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
                     if (at >= 0) {
-                        k = load4((const T *)p.k + at + d);
-                        v = load4((const T *)p.v + at + d);
+                        k = load4((const float *)p.k + at + d);
+                        v = load4((const float *)p.v + at + d);
                         if (edge && !(isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w))) {
                             tainted = 1;
                             v.x = isfinite(v.x) ? v.x : 0.0f;
@@ -200,7 +186,7 @@ template <typename T, int NC> __global__ void __launch_bounds__(kThreads) chunk_
             for (int i = 0; i < 4; ++i)
                 for (int c = 0; c < NC; ++c)
                     if (column<NC>(tx, c) < D)
-                        o[i][c] += taint_of<T>(p, u, walk.t0, walk.t1, lo[i], hi[i], column<NC>(tx, c));
+                        o[i][c] += taint_of<float>(p, u, walk.t0, walk.t1, lo[i], hi[i], column<NC>(tx, c));
         if (walk.part) {
             const int64_t slot = walk.slot();
 #pragma unroll
@@ -216,90 +202,41 @@ template <typename T, int NC> __global__ void __launch_bounds__(kThreads) chunk_
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (ty * 4 + i >= u.rows) continue;
-                T *to = (T *)p.out + output_offset(p, u, ty * 4 + i);
+                float *to = (float *)p.out + output_offset(p, u, ty * 4 + i);
                 const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
-                    if (column<NC>(tx, c) < D) to[column<NC>(tx, c)] = round_to<T>(o[i][c] * inv);
+                    if (column<NC>(tx, c) < D) to[column<NC>(tx, c)] = o[i][c] * inv;
             }
         }
     }
     if (t == 0 && !p.whole) p.heads[blockIdx.x] = head;
 }
 
-// Joins the parts of the unit that block x of the attention began, thirty-two rows a block: a thread
-// has a row and eight columns at a time.  What it reads is mostly in L2.
-template <typename T, int MT> __global__ void __launch_bounds__(256) join_kernel(ChunkParams p) {
-    ptx::griddep_wait();
-    const int4 head = p.heads[blockIdx.x];
-    if (head.w == 0) return;
-    Unit<MT, 64> u;
-    u.b = head.x;
-    u.hk = head.y;
-    u.m = head.z;
-    u.s = sequence_of(p, u.b, false);
-    u.tile(p);
-    const int r = blockIdx.y * 32 + threadIdx.x % 32;
-    if (r >= u.rows) return;
-    const int64_t first = 2 * (int64_t)blockIdx.x + 1;
-    float M = kNegInf, L = 0.0f;
-    for (int i = 0; i < head.w; ++i)
-        M = fmaxf(M, p.part_ml[(i == 0 ? first : first - 1 + 2 * i) * MT + r].x);
-    const float base = M == kNegInf ? 0.0f : M;
-    for (int i = 0; i < head.w; ++i) {
-        const float2 ml = p.part_ml[(i == 0 ? first : first - 1 + 2 * i) * MT + r];
-        L += ml.y * shrink_of(ml.x, base);
-    }
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-    T *to = (T *)p.out + output_offset(p, u, r);
-    for (int d = threadIdx.x / 32 * 8; d < p.D; d += 64) {
-        float o[8] = {};
-        for (int i = 0; i < head.w; ++i) {
-            const int64_t slot = i == 0 ? first : first - 1 + 2 * i;
-            const float w = shrink_of(p.part_ml[slot * MT + r].x, base);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] += w * p.part_o[(slot * p.D + d + e) * MT + r];
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] *= inv;
-        store8(to + d, o);
-    }
-}
-
-template <typename T, int NC> cudaError_t launch(const ctr_attn_s *pl, const ChunkParams &p, cudaStream_t st) {
+template <int NC> cudaError_t launch(const ctr_attn_s *pl, const ChunkParams &p, cudaStream_t st) {
     static PerDeviceOnce once;
-    const auto kernel = chunk_kernel<T, NC>;
+    const auto kernel = chunk_kernel<NC>;
     cudaError_t e = once.run(current_device(), cudaSuccess, [&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)smem_bytes(16 * NC, 16 * NC));
     });
     if (e != cudaSuccess) return e;
-    const int grid = pl->num_sms * chunk_shape(pl->dtype, pl->D).per_sm;
+    const int grid = pl->num_sms * chunk_shape(CTR_F32, pl->D).per_sm;
     count_launches(1);
     e = launch_pdl(kernel, dim3((unsigned)grid), dim3(kThreads), smem_bytes(p.D, 16 * NC), st, p);
     if (e != cudaSuccess || p.whole) return e;
-    count_launches(1);
-    return launch_pdl(join_kernel<T, kRows>, dim3((unsigned)grid, kRows / 32), dim3(256), 0, st, p);
-}
-
-template <typename T> cudaError_t launch_any(const ctr_attn_s *pl, const ChunkParams &p, cudaStream_t st) {
-    if (p.D <= 64) return launch<T, 4>(pl, p, st);
-    if (p.D <= 80) return launch<T, 5>(pl, p, st);
-    if (p.D <= 96) return launch<T, 6>(pl, p, st);
-    if (p.D <= 128) return launch<T, 8>(pl, p, st);
-    return launch<T, 16>(pl, p, st);
+    return launch_join<float, kRows>(p, grid, st);
 }
 
 }  // namespace chunk
 
-ChunkShape chunk_shape(int, int64_t D) {
-    return {chunk::kRows, chunk::kSlots, D <= 128 ? 2 : 1};
-}
-
-cudaError_t launch_chunk(const ctr_attn_s *pl, const ChunkParams &p, cudaStream_t st) {
-    return pl->dtype == CTR_F32    ? chunk::launch_any<float>(pl, p, st)
-           : pl->dtype == CTR_BF16 ? chunk::launch_any<__nv_bfloat16>(pl, p, st)
-                                   : chunk::launch_any<__half>(pl, p, st);
+cudaError_t launch_chunk_f32(const ctr_attn_s *pl, const ChunkParams &p, cudaStream_t st) {
+    using namespace chunk;
+    if (p.D <= 64) return launch<4>(pl, p, st);
+    if (p.D <= 80) return launch<5>(pl, p, st);
+    if (p.D <= 96) return launch<6>(pl, p, st);
+    if (p.D <= 128) return launch<8>(pl, p, st);
+    return launch<16>(pl, p, st);
 }
 
 }  // namespace ctr

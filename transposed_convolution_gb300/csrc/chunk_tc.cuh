@@ -1,0 +1,698 @@
+// chunk_tc.cuh -- attention of a chunk of new tokens over a paged 16-bit cache, on the tensor cores.
+//
+// Two products a tile of 128 rows by NT slots, S = Q K^T and O += P V, 4 D operations a score against
+// one exponential, a maximum, a sum and a rounding: with many rows the tensor pipe bounds it, with few
+// the cache's bytes.  A block has two tiles of 128 rows on the same slots (one where D > 128), so that
+// K and V are read from L2 once for 256 rows and the tensor pipe works on one tile's products while
+// the other's softmax runs:
+//   warps 0-3, 4-7  the softmax of each tile, a thread a row: S from TMEM, P to TMEM over it;
+//   warps 8-11      copy K and V slots, wherever their pages are, and Q rows into shared memory, a
+//                   ring of stages of one K or V tile each (cp.async: 16 bytes from any page, zeros
+//                   for slots that are not there);
+//   warp 12         issues tcgen05.mma: per tile of slots PV0, QK0 of the next tile, PV1, QK1.
+// P stays in TMEM as the first operand of PV (half the shared-memory reads of one from there),
+// and V is read as it lies, [slots][columns], as a column-major operand.  With one tile of rows the
+// two S buffers alternate instead.
+//
+// Softmax: powers of two of a score's distance to the row's base, which follows the running maximum only when
+// that exceeds it by kSlack, because then O has to be rescaled in TMEM, which the tensor pipe waits
+// for.  Rows are independent of one another to the last bit.
+//
+// Rounding: scores, statistics and O are fp32; P is rounded once to the type (half the operations of two
+// terms; the error is that of one rounding of the output, and smaller where weights are many), the
+// sum is that of the unrounded ones.  fp16 has no exponents to spare below 2^-24: its P is lifted
+// by 2^13 and its slack is 2^2, so that weights keep eleven bits down to 2^-27 of the largest.
+#pragma once
+
+#include <algorithm>
+
+#include "chunk_device.cuh"
+#include "chunk_join.cuh"
+
+namespace ctr {
+namespace chunk {
+
+template <typename T> struct Half;
+template <> struct Half<__nv_bfloat16> {
+    static constexpr float kLift = 0.0f, kSlack = 8.0f;
+    static constexpr uint32_t kFormat = ptx::kFmtBF16, kExponent = 0x7f80u;
+    static __device__ __forceinline__ uint32_t pack(float a, float b) { return ptx::bf16x2_rn(a, b); }
+    // (bf16 has fp32's exponents: nothing to hold up.)
+    static __device__ __forceinline__ uint32_t hold_up(uint32_t v) { return v; }
+};
+template <> struct Half<__half> {
+    static constexpr float kLift = 13.0f, kSlack = 2.0f;
+    static constexpr uint32_t kFormat = ptx::kFmtF16, kExponent = 0x7c00u;
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        uint32_t r;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+        return r;
+    }
+    // At least 2^-24 (2^-37 of the largest), so that an infinite V stays infinite.
+    static __device__ __forceinline__ uint32_t hold_up(uint32_t v) {
+        uint32_t r;
+        asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x00010001u));
+        return r;
+    }
+};
+
+// Sizes by the largest head size.
+template <int DP> struct Sizes {
+    static constexpr int kTiles = DP <= 128 ? 2 : 1;           // of 128 rows
+    static constexpr int kRows = 128 * kTiles, kSlots = DP <= 128 ? 128 : 64;
+    static constexpr int kPanels = DP / 64;                    // of 128 bytes of every row
+    static constexpr int kQPanel = 128 * 128, kPanel = kSlots * 128;
+    static constexpr int kStage = kPanels * kPanel;
+    static constexpr int kStages = DP <= 64 ? 8 : 5;
+    static constexpr int kAhead = DP <= 64 ? 6 : 3;            // copies in flight before the oldest is waited for
+    static constexpr int kQ = kTiles * kPanels * kQPanel;
+    static constexpr int kSmem = 1024 + kQ + kStages * kStage;
+    // TMEM columns.
+    static constexpr int kS = 0, kO = 2 * kSlots, kOPitch = DP;
+    static_assert(kO + kTiles * kOPitch <= 512, "TMEM");
+};
+
+constexpr int kThreads = 512, kCopyWarp = 8, kMmaWarp = 12;
+constexpr int kRing = 8;                                        // tiles whose visible slots are kept
+constexpr int kSegments = 32;                                   // segments whose taint is kept
+constexpr uint64_t kWaitLimitNs = 2000000000;                   // of a block's waits for itself
+constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;              // 256 (192 + 64) = 512 * 128
+
+struct Shared {
+    // Whoever waits at a barrier waits for each of its phases in turn, or knows by what it has seen
+    // that the earlier ones are over: a wait tells only odd phases from even ones.  So where one tile of
+    // rows uses both S buffers, the second has barriers of its own ([2]).
+    uint64_t kv_full[8], kv_empty[8], q_full, q_empty, s_full[3], p_full[3], o_full[2], drained;
+    Start start;
+    uint32_t visible[kRing][4];
+    int taint[kSegments];
+    uint32_t tmem;
+    volatile int abort;
+};
+
+__device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+    return ptx::mbar_wait_warp(bar, parity, kWaitLimitNs, &sh.abort);
+}
+
+__device__ __forceinline__ void give_up(Shared &sh, const ChunkParams &p) {
+    sh.abort = 1;
+    if (threadIdx.x % 32 == 0) atomicOr(p.cache.status, kStatusTimeout);
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// D (+)= A[tmem] * B[smem], B column-major if the descriptor and idesc say so.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+// Operand [k][n] of 128-byte swizzled panels of 64 columns, `panel` bytes apart, whose rows are k: groups of
+// eight rows are 1024 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t smem_addr, uint32_t panel) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(panel >> 4) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+constexpr uint32_t kTransposeB = 1u << 16;
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+                   "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+                   "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]),
+                   "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]),
+                   "+r"(v[14]), "+r"(v[15])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+                 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+                 "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+                 : "memory");
+}
+
+// The slots [j0 + 32 w, + 32) that lie in [lo, hi), as bits.
+__device__ __forceinline__ uint32_t range_bits(int j, int lo, int hi) {
+    const int a = min(max(lo - j, 0), 32), b = min(max(hi - j, 0), 32);
+    return (uint32_t)((1ull << b) - (1ull << min(a, b)));
+}
+
+// ------------------------------------------------------------------------------------------------
+// Copies.  Each of the four warps has a quarter of a tile's slots: a lane looks one up, then eight
+// lanes copy 128 bytes of one.
+template <typename T, int DP> struct Copier {
+    typedef Sizes<DP> Z;
+    const ChunkParams &p;
+    Shared &sh;
+    uint32_t q_smem, kv_smem;
+    int items = 0, flying = 0;
+    // What is in flight, the last one first: the barrier to arrive at, and whether to look for values that
+    // are no numbers.
+    uint32_t queue[Z::kAhead + 1];
+    static constexpr uint32_t kIsQ = 1u << 31, kLook = 1u << 30;
+
+    __device__ __forceinline__ Copier(const ChunkParams &p, Shared &sh, uint32_t q, uint32_t kv)
+        : p(p), sh(sh), q_smem(q), kv_smem(kv) {}
+
+    // Waits for the oldest copy and passes it on.
+    __device__ __forceinline__ void retire() {
+        uint32_t e = 0;
+#pragma unroll
+        for (int i = 0; i <= Z::kAhead; ++i)
+            if (flying == i + 1) {
+                e = queue[i];
+                switch (i) {
+                case 0: copy_wait<0>(); break;
+                case 1: copy_wait<1>(); break;
+                case 2: copy_wait<2>(); break;
+                case 3: copy_wait<3>(); break;
+                case 4: copy_wait<4>(); break;
+                case 5: copy_wait<5>(); break;
+                default: copy_wait<6>(); break;
+                }
+            }
+        --flying;
+        const int stage = e & 15;
+        if (e & kLook) look(stage, (int)(e >> 4 & 0x3ffffff));
+        fence_async();
+        ptx::mbar_arrive(e & kIsQ ? &sh.q_full : &sh.kv_full[stage]);
+    }
+    __device__ __forceinline__ void push(uint32_t e) {
+        copy_commit();
+#pragma unroll
+        for (int i = Z::kAhead; i > 0; --i) queue[i] = queue[i - 1];
+        queue[0] = e;
+        if (++flying > Z::kAhead) retire();
+    }
+    // Waits until a barrier's phase is over; what is in flight is passed on meanwhile, because whoever
+    // completes that phase may be waiting for it.
+    __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity) {
+        while (!__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) {
+            if (flying == 0) return wait(sh, bar, parity);
+            retire();
+        }
+        return true;
+    }
+
+    // Takes values that are no numbers out of this thread's part of a V stage (see taint).
+    __device__ __noinline__ void look(int stage, int segment) {
+        const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 - kCopyWarp;
+        const uint32_t base = kv_smem + stage * Z::kStage;
+        bool found = false;
+        for (int panel = 0; panel * 64 < p.D; ++panel) {
+            if (panel * 64 + lane % 8 * 8 >= p.D) continue;
+            for (int r = lane / 8; r < Z::kSlots / 4; r += 4) {
+                const int row = warp * (Z::kSlots / 4) + r;
+                const uint32_t at = base + panel * Z::kPanel + row * 128 + ((lane ^ row) & 7) * 16;
+                uint32_t v[4];
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
+                bool bad = false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    constexpr uint32_t kE = Half<T>::kExponent;
+                    if ((v[i] & kE) == kE) v[i] &= 0xffff0000u, bad = true;
+                    if ((v[i] >> 16 & kE) == kE) v[i] &= 0x0000ffffu, bad = true;
+                }
+                if (bad) {
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]),
+                                 "r"(v[2]), "r"(v[3]) : "memory");
+                    found = true;
+                }
+            }
+        }
+        if (found) sh.taint[segment % kSegments] = segment;
+    }
+
+    // Rows of 128-byte panels: lane l's row is at `from` + `mine` elements of 16 (`on`: it is there).
+    __device__ __forceinline__ void copy_rows(uint32_t dst, int panel_bytes, int row0, int rows, const T *from,
+                                              uint32_t mine, bool on) {
+        const int lane = threadIdx.x % 32;
+        const unsigned there = __ballot_sync(0xffffffffu, on);
+#pragma unroll
+        for (int r0 = 0; r0 < rows; r0 += 4) {
+            const int r = r0 + lane / 8, row = row0 + r;
+            const T *src = from + (uint64_t)__shfl_sync(0xffffffffu, mine, r) * 16 + lane % 8 * 8;
+            const bool ok = there >> r & 1;
+            const uint32_t to = dst + row * 128 + ((lane ^ row) & 7) * 16;
+#pragma unroll
+            for (int panel = 0; panel < Z::kPanels; ++panel)
+                if (panel * 64 + lane % 8 * 8 < p.D)
+                    copy16(to + panel * panel_bytes, ok ? src + panel * 64 : from, ok);
+        }
+    }
+
+    __device__ __forceinline__ bool run(const Start &start) {
+        Walk<Z::kRows, Z::kSlots> walk;
+        walk.start(p, start);
+        const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 - kCopyWarp;
+        constexpr int kOwn = Z::kSlots / 4;
+        int segment = 0, tiles = 0;
+        while (walk.next(p)) {
+            const auto &u = walk.u;
+            ++segment;
+            for (int t = walk.t0; t < walk.t1; ++t, ++tiles) {
+                const int j0 = (u.first + t) * Z::kSlots;
+                const bool edge = is_edge(u, j0, Z::kSlots);
+                const int64_t at = lane < kOwn ? cache_row(p, u, j0 + warp * kOwn + lane) : -1;
+                const uint32_t mine = (uint32_t)(at >> 4);
+                for (int kv = 0; kv < 2; ++kv, ++items) {
+                    const int stage = items % Z::kStages;
+                    if (!wait_for(&sh.kv_empty[stage], (items / Z::kStages & 1) ^ 1)) return false;
+                    copy_rows(kv_smem + stage * Z::kStage, Z::kPanel, warp * kOwn, kOwn,
+                              (const T *)(kv ? p.v : p.k), mine, at >= 0);
+                    if (kv == 0) {
+                        const unsigned seen = __ballot_sync(0xffffffffu, at >= 0);
+                        if (lane == 0) {
+                            if (kOwn == 32) sh.visible[tiles % kRing][warp] = seen;
+                            else reinterpret_cast<uint16_t *>(sh.visible[tiles % kRing])[warp] = (uint16_t)seen;
+                        }
+                    }
+                    push(stage | (kv && edge ? kLook | (uint32_t)segment << 4 : 0u));
+                }
+                if (t == walk.t0) {
+                    // Q behind the first tile, which need not wait for the segment before.
+                    if (!wait_for(&sh.q_empty, (segment & 1))) return false;
+                    for (int tile = 0; tile < Z::kTiles && tile * 128 < u.rows; ++tile) {
+                        const int r = tile * 128 + warp * 32 + lane;
+                        const bool on = r < u.rows;
+                        copy_q(q_smem + tile * Z::kPanels * Z::kQPanel, warp * 32, on ? query_offset(p, u, r) : 0,
+                               on);
+                    }
+                    push(kIsQ);
+                }
+            }
+        }
+        while (flying > 0) retire();
+        return true;
+    }
+    __device__ __forceinline__ void copy_q(uint32_t dst, int row0, int64_t mine, bool on) {
+        const int lane = threadIdx.x % 32;
+        const unsigned there = __ballot_sync(0xffffffffu, on);
+        for (int r0 = 0; r0 < 32; r0 += 4) {
+            const int r = r0 + lane / 8, row = row0 + r;
+            const T *src = (const T *)p.q + __shfl_sync(0xffffffffu, mine, r) + lane % 8 * 8;
+            const bool ok = there >> r & 1;
+            const uint32_t to = dst + row * 128 + ((lane ^ row) & 7) * 16;
+            for (int panel = 0; panel < Z::kPanels; ++panel)
+                if (panel * 64 + lane % 8 * 8 < p.D)
+                    copy16(to + panel * Z::kQPanel, ok ? src + panel * 64 : (const T *)p.q, ok);
+        }
+    }
+};
+
+// ------------------------------------------------------------------------------------------------
+// Products.
+template <typename T, int DP> struct Multiplier {
+    typedef Sizes<DP> Z;
+    const ChunkParams &p;
+    Shared &sh;
+    uint32_t q_smem, kv_smem, tmem;
+
+    __device__ __forceinline__ void scores(int tile, int buffer, int stage) {
+        const uint32_t idesc = ptx::idesc_f32acc(Half<T>::kFormat, 128, Z::kSlots);
+        const uint32_t q = q_smem + tile * Z::kPanels * Z::kQPanel, k = kv_smem + stage * Z::kStage;
+        for (int i = 0; i < p.D / 16; ++i) {
+            const uint64_t a = ptx::sdesc_k<128>(q + i / 4 * Z::kQPanel + i % 4 * 32);
+            const uint64_t b = ptx::sdesc_k<128>(k + i / 4 * Z::kPanel + i % 4 * 32);
+            if (ptx::elect_one()) ptx::mma_f16(tmem + Z::kS + buffer * Z::kSlots, a, b, idesc, i > 0);
+        }
+    }
+    __device__ __forceinline__ void values(int tile, int buffer, int stage, bool first) {
+        const uint32_t idesc = ptx::idesc_f32acc(Half<T>::kFormat, 128, p.D) | kTransposeB;
+        const uint32_t v = kv_smem + stage * Z::kStage;
+#pragma unroll
+        for (int i = 0; i < Z::kSlots / 16; ++i) {
+            const uint64_t b = sdesc_mn(v + i * 2048, Z::kPanel);
+            if (ptx::elect_one())
+                mma_f16_ts(tmem + Z::kO + tile * Z::kOPitch, tmem + Z::kS + buffer * Z::kSlots + i * 8, b, idesc,
+                           i > 0 || !first);
+        }
+    }
+    // The barrier's phase ends when the products issued so far do; the plain arrival orders what this
+    // warp has seen before it for who waits there.
+    __device__ __forceinline__ void commit(uint64_t *bar) {
+        if (ptx::elect_one()) {
+            ptx::mma_commit(bar);
+            ptx::mbar_arrive(bar);
+        }
+    }
+    __device__ __forceinline__ void release(uint64_t *bar) {
+        if (ptx::elect_one()) ptx::mma_commit(bar);
+    }
+    __device__ __forceinline__ bool arrived(int item) {
+        return wait(sh, &sh.kv_full[item % Z::kStages], item / Z::kStages & 1);
+    }
+
+    __device__ __forceinline__ bool run(const Start &start) {
+        Walk<Z::kRows, Z::kSlots> walk;
+        walk.start(p, start);
+        int segment = 0, items = 0, p_count[3] = {0, 0, 0};
+        while (walk.next(p)) {
+            const int n = walk.t1 - walk.t0;
+            const bool dual = walk.u.rows > 128;
+            if (!wait(sh, &sh.q_full, segment & 1) || !arrived(items)) return false;
+            ptx::tc_fence_after();
+            scores(0, 0, items % Z::kStages);
+            commit(&sh.s_full[0]);
+            if (dual) {
+                scores(1, 1, items % Z::kStages);
+                commit(&sh.s_full[1]);
+            }
+            release(&sh.kv_empty[items % Z::kStages]);
+            if (n == 1) release(&sh.q_empty);
+            for (int t = 0; t < n; ++t, items += 2) {
+                const int v = (items + 1) % Z::kStages, k = (items + 2) % Z::kStages;
+                const bool more = t + 1 < n;
+                if (dual) {
+                    if (!arrived(items + 1) || !wait(sh, &sh.p_full[0], p_count[0]++ & 1)) return false;
+                    ptx::tc_fence_after();
+                    values(0, 0, v, t == 0);
+                    commit(&sh.o_full[0]);
+                    if (more) {
+                        if (!arrived(items + 2)) return false;
+                        ptx::tc_fence_after();
+                        scores(0, 0, k);
+                        commit(&sh.s_full[0]);
+                    }
+                    if (!wait(sh, &sh.p_full[1], p_count[1]++ & 1)) return false;
+                    ptx::tc_fence_after();
+                    values(1, 1, v, t == 0);
+                    commit(&sh.o_full[1]);
+                    release(&sh.kv_empty[v]);
+                    if (more) {
+                        scores(1, 1, k);
+                        commit(&sh.s_full[1]);
+                        release(&sh.kv_empty[k]);
+                        if (t + 2 == n) release(&sh.q_empty);
+                    }
+                } else {
+                    const int now = t & 1;
+                    if (more) {
+                        if (!arrived(items + 2)) return false;
+                        ptx::tc_fence_after();
+                        scores(0, now ^ 1, k);
+                        commit(&sh.s_full[now ? 0 : 2]);
+                        release(&sh.kv_empty[k]);
+                        if (t + 2 == n) release(&sh.q_empty);
+                    }
+                    const uint32_t parity = (now ? p_count[2]++ : p_count[0]++) & 1;
+                    if (!arrived(items + 1) || !wait(sh, &sh.p_full[now ? 2 : 0], parity)) return false;
+                    ptx::tc_fence_after();
+                    values(0, now, v, t == 0);
+                    commit(&sh.o_full[0]);
+                    release(&sh.kv_empty[v]);
+                }
+            }
+            ++segment;
+        }
+        return true;
+    }
+};
+
+// ------------------------------------------------------------------------------------------------
+// Softmax of one tile of rows, and its output.
+template <typename T, int DP> struct Softmax {
+    typedef Sizes<DP> Z;
+    typedef Half<T> H;
+    static constexpr int kN = Z::kSlots;
+    const ChunkParams &p;
+    Shared &sh;
+    uint32_t tmem;           // of this warp's lanes
+    int tile;                // of rows: 0 or 1
+
+    // Multiplies this warp's rows of O.
+    __device__ __forceinline__ void rescale(float factor) {
+        const uint32_t o = tmem + Z::kO + tile * Z::kOPitch;
+        for (int d = 0; d < p.D; d += 16) {
+            uint32_t v[16];
+            tmem_ld16(o + d, v);
+            tmem_wait_ld16(v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * factor);
+            tmem_st16(o + d, v);
+        }
+    }
+
+    __device__ __forceinline__ bool run(const Start &start) {
+        Walk<Z::kRows, Z::kSlots> walk;
+        walk.start(p, start);
+        const int r = tile * 128 + threadIdx.x % 128;
+        // Scores of a negative or zero scale are multiplied before they are compared.
+        const bool early = p.scale_log2 <= 0.0f;
+        const float scale = early ? 1.0f : p.scale_log2;
+        int segment = 0, tiles = 0, o_count = 0, s_count[2] = {0, 0};    // s_count: own barrier, and [2]
+        int4 head = make_int4(0, 0, 0, 0);
+        while (walk.next(p)) {
+            const auto &u = walk.u;
+            const int n = walk.t1 - walk.t0;
+            const bool dual = u.rows > 128;
+            ++segment;
+            if (tile == 1 && !dual) {
+                tiles += n;
+                continue;
+            }
+            const bool mine = r < u.rows;
+            const int hi = mine ? end_slot(p, u.s, (u.r0 + r) / p.G) : 0, lo = first_slot(p, hi);
+            float base = kNegInf, l = 0.0f;
+            for (int t = 0; t < n; ++t, ++tiles) {
+                const bool second = !dual && (t & 1);
+                const int buffer = dual ? tile : t & 1, bar = second ? 2 : tile;
+                const int j0 = (u.first + walk.t0 + t) * kN;
+                const uint32_t parity = (second ? s_count[1]++ : s_count[0]++) & 1;
+                if (!wait(sh, &sh.s_full[bar], parity)) return false;
+                ptx::tc_fence_after();
+                const uint32_t at = tmem + Z::kS + buffer * kN;
+                uint32_t s[kN / 32][32];
+#pragma unroll
+                for (int w = 0; w < kN / 32; ++w) ptx::tmem_ld_32x32b_x32(at + w * 32, s[w]);
+                uint32_t seen[kN / 32], all = ~0u;
+#pragma unroll
+                for (int w = 0; w < kN / 32; ++w) {
+                    seen[w] = *(volatile uint32_t *)&sh.visible[tiles % kRing][w];
+                    all &= seen[w];
+                }
+                const bool masked = is_edge(u, j0, kN) || all != ~0u;
+#pragma unroll
+                for (int w = 0; w < kN / 32; ++w) ptx::tmem_wait_ld_regs(s[w]);
+                if (early) {
+#pragma unroll
+                    for (int w = 0; w < kN / 32; ++w)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            s[w][i] = __float_as_uint(__uint_as_float(s[w][i]) * p.scale_log2);
+                }
+                if (masked) {
+#pragma unroll
+                    for (int w = 0; w < kN / 32; ++w) {
+                        const uint32_t bits = seen[w] & range_bits(j0 + w * 32, lo, hi);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            s[w][i] = bits >> i & 1 ? s[w][i] : 0xff800000u;
+                    }
+                }
+                float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+                for (int w = 0; w < kN / 32; ++w)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) top[i % 4] = fmaxf(top[i % 4], __uint_as_float(s[w][i]));
+                // Rounded upwards: no power of two below exceeds what the base allows it.
+                const float m = __fmul_ru(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), scale);
+                const bool raise = m > base + H::kSlack;
+                const float factor = raise && base > kNegInf ? shrink_of(base, m) : 1.0f;
+                const bool again = raise && base > kNegInf;
+                if (raise) base = m;
+                if (t > 0 && __any_sync(0xffffffffu, again)) {
+                    if (!wait(sh, &sh.o_full[tile], (o_count + t - 1) & 1)) return false;
+                    ptx::tc_fence_after();
+                    rescale(factor);
+                }
+                const float sub = base == kNegInf ? 0.0f : __fsub_ru(base, H::kLift);
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int w = 0; w < kN / 64; ++w) {
+                    uint32_t out[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float a = pow2(fmaf(__uint_as_float(s[2 * w + i / 16][i % 16 * 2]), scale, -sub));
+                        const float b = pow2(fmaf(__uint_as_float(s[2 * w + i / 16][i % 16 * 2 + 1]), scale, -sub));
+                        sum[i % 2 * 2] += a;
+                        sum[i % 2 * 2 + 1] += b;
+                        out[i] = H::pack(a, b);
+                    }
+                    if (!masked) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) out[i] = H::hold_up(out[i]);
+                    }
+                    ptx::tmem_st_32x32b_x32(at + w * 32, out);
+                }
+                l = l * factor + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(&sh.p_full[bar]);
+            }
+            o_count += n;
+            // (The last scores were ready when all products with V but the last two were.)
+            if (n > 1 && !wait(sh, &sh.o_full[tile], (o_count - 2) & 1)) return false;
+            if (!wait(sh, &sh.o_full[tile], (o_count - 1) & 1)) return false;
+            ptx::tc_fence_after();
+            const bool tainted = *(volatile int *)&sh.taint[segment % kSegments] == segment;
+            output(walk, r, mine, lo, hi, base, l, tainted);
+            if (walk.part && walk.begins && tile == 0) head = make_int4(u.b, u.hk, u.m, walk.parts());
+        }
+        if (threadIdx.x == 0 && !p.whole) p.heads[blockIdx.x] = head;
+        return true;
+    }
+
+    template <typename W>
+    __device__ __forceinline__ void output(const W &walk, int r, bool mine, int lo, int hi, float base, float l,
+                                           bool tainted) {
+        const auto &u = walk.u;
+        const uint32_t o = tmem + Z::kO + tile * Z::kOPitch;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int64_t slot = walk.slot();
+        T *to = (T *)p.out + (mine ? output_offset(p, u, r) : 0);
+        if (walk.part && mine) p.part_ml[slot * Z::kRows + r] = make_float2(base, l);
+        for (int d = 0; d < p.D; d += 16) {
+            uint32_t v[16];
+            __syncwarp();
+            tmem_ld16(o + d, v);
+            tmem_wait_ld16(v);
+            if (!mine) continue;
+            if (tainted)
+                for (int i = 0; i < 16; ++i)
+                    v[i] = __float_as_uint(__uint_as_float(v[i]) +
+                                           taint_of<T>(p, u, walk.t0, walk.t1, lo, hi, d + i));
+            if (walk.part) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    p.part_o[(slot * p.D + d + i) * Z::kRows + r] = __uint_as_float(v[i]);
+            } else {
+                float x[8];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        x[i] = l == 0.0f ? 0.0f : __uint_as_float(v[h * 8 + i]) * inv;
+                    store8(to + d + h * 8, x);
+                }
+            }
+        }
+        __syncwarp();
+        // (O has been read when this warp arrives at p_full next.)
+    }
+};
+
+template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(ChunkParams p) {
+    typedef Sizes<DP> Z;
+    extern __shared__ unsigned char dynamic[];
+    __shared__ Shared sh;
+    const uint32_t raw = ptx::smem_u32(dynamic), smem = (raw + 1023) & ~1023u;
+    const int warp = threadIdx.x / 32;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Z::kStages; ++i) {
+            ptx::mbar_init(&sh.kv_full[i], 128);
+            ptx::mbar_init(&sh.kv_empty[i], 1);
+        }
+        ptx::mbar_init(&sh.q_full, 128);
+        ptx::mbar_init(&sh.q_empty, 1);
+        ptx::mbar_init(&sh.drained, 1);
+        for (int i = 0; i < 3; ++i) {
+            ptx::mbar_init(&sh.s_full[i], 2);
+            ptx::mbar_init(&sh.p_full[i], 128);
+        }
+        ptx::mbar_init(&sh.o_full[0], 2);
+        ptx::mbar_init(&sh.o_full[1], 2);
+        ptx::fence_mbar_init();
+        sh.abort = 0;
+    }
+    if (threadIdx.x < kSegments) sh.taint[threadIdx.x] = 0;
+    if (warp == kMmaWarp) {
+        ptx::tmem_alloc(&sh.tmem, 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    find_start<Z::kRows, Z::kSlots>(p, reinterpret_cast<int64_t *>(dynamic + (smem - raw)), &sh.start);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = sh.tmem, q_smem = smem, kv_smem = smem + Z::kQ;
+    bool ok = true;
+    if (warp < kCopyWarp) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        if (warp / 4 < Z::kTiles) {
+            Softmax<T, DP> softmax{p, sh, tmem + ((uint32_t)(warp % 4 * 32) << 16), warp / 4};
+            ok = softmax.run(sh.start);
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp < kMmaWarp) {
+            Copier<T, DP> copier(p, sh, q_smem, kv_smem);
+            ok = copier.run(sh.start);
+            if (!ok) copy_wait<0>();
+        } else if (warp == kMmaWarp) {
+            Multiplier<T, DP> multiplier{p, sh, q_smem, kv_smem, tmem};
+            ok = multiplier.run(sh.start);
+        }
+    }
+    if (!ok) give_up(sh, p);
+    if (warp == kMmaWarp) {
+        // Products that nobody waits for any more.
+        if (ptx::elect_one()) ptx::mma_commit(&sh.drained);
+        ptx::mbar_wait_warp(&sh.drained, 0, kWaitLimitNs, nullptr);
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, 512);
+}
+
+template <typename T, int DP> cudaError_t launch_tc(const ctr_attn_s *pl, const ChunkParams &p, cudaStream_t st) {
+    typedef Sizes<DP> Z;
+    static_assert(Z::kSmem + sizeof(Shared) <= 227 * 1024, "shared memory");
+    static_assert(kMaxB * sizeof(int64_t) <= Z::kQ, "costs");
+    static PerDeviceOnce once;
+    const auto kernel = tc_kernel<T, DP>;
+    cudaError_t e = once.run(current_device(), cudaSuccess, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::kSmem);
+    });
+    if (e != cudaSuccess) return e;
+    count_launches(1);
+    e = launch_pdl(kernel, dim3((unsigned)pl->num_sms), dim3(kThreads), Z::kSmem, st, p);
+    if (e != cudaSuccess || p.whole) return e;
+    return launch_join<T, Z::kRows>(p, pl->num_sms, st);
+}
+
+template <typename T> cudaError_t launch_16(const ctr_attn_s *pl, const ChunkParams &p, cudaStream_t st) {
+    return p.D <= 64 ? launch_tc<T, 64>(pl, p, st) : p.D <= 128 ? launch_tc<T, 128>(pl, p, st)
+                                                                : launch_tc<T, 256>(pl, p, st);
+}
+
+}  // namespace chunk
+}  // namespace ctr

@@ -90,9 +90,9 @@ struct ChunkParams {
     int whole;               // units are not cut
 };
 
-// A chunk attention's launch: rows and slots of a tile, and blocks an SM.
+// A chunk attention's launch: rows of a tile, and blocks an SM.
 struct ChunkShape {
-    int rows, slots, per_sm;
+    int rows, per_sm;
 };
 ChunkShape chunk_shape(int dtype, int64_t D);
 
@@ -153,6 +153,9 @@ cudaError_t launch_attention_f32(const ctr_attn_s *pl, const AttnParams &p, cuda
 cudaError_t launch_attention_bf16(const ctr_attn_s *pl, const AttnParams &p, cudaStream_t st);
 cudaError_t launch_attention_f16(const ctr_attn_s *pl, const AttnParams &p, cudaStream_t st);
 cudaError_t launch_attention(const ctr_attn_s *pl, const AttnParams &p, cudaStream_t st);
+cudaError_t launch_chunk_f32(const ctr_attn_s *pl, const ChunkParams &p, cudaStream_t st);
+cudaError_t launch_chunk_bf16(const ctr_attn_s *pl, const ChunkParams &p, cudaStream_t st);
+cudaError_t launch_chunk_f16(const ctr_attn_s *pl, const ChunkParams &p, cudaStream_t st);
 cudaError_t launch_chunk(const ctr_attn_s *pl, const ChunkParams &p, cudaStream_t st);
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t st);
 
