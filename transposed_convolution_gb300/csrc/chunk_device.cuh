@@ -74,8 +74,12 @@ template <typename T> __device__ __forceinline__ void store8(T *to, const float 
 // that a row does not attend to would be NaN.  So infinities and NaN are taken out of V in the tiles that
 // some row attends to in part, and the unit is marked.  This is what they add to one output: the
 // infinities and NaN among the slots [lo, hi) of those tiles of the segment.
-template <typename T, int NT, typename U>
-__device__ __noinline__ float taint(const ChunkParams &p, const U &u, int t0, int t1, int lo, int hi, int d) {
+// (By value: a unit whose address is taken would live in local memory.)
+struct Edges {
+    int b, hk, lo, hi, lo_last, hi_first, first;
+};
+template <typename T, int NT>
+__device__ __noinline__ float taint(const ChunkParams &p, Edges u, int t0, int t1, int lo, int hi, int d) {
     float sum = 0.0f;
     for (int tile = t0; tile < t1; ++tile) {
         const int j0 = (u.first + tile) * NT;
@@ -88,10 +92,11 @@ __device__ __noinline__ float taint(const ChunkParams &p, const U &u, int t0, in
     }
     return sum;
 }
-template <typename T, int MT, int NT>
-__device__ __forceinline__ float taint_of(const ChunkParams &p, const Unit<MT, NT> &u, int t0, int t1, int lo,
+template <typename T, int NT, typename U>
+__device__ __forceinline__ float taint_of(const ChunkParams &p, const U &u, int t0, int t1, int lo,
                                           int hi, int d) {
-    return taint<T, NT>(p, u, t0, t1, lo, hi, d);
+    const Edges e = {u.b, u.hk, u.lo, u.hi, u.lo_last, u.hi_first, u.first};
+    return taint<T, NT>(p, e, t0, t1, lo, hi, d);
 }
 
 }  // namespace chunk

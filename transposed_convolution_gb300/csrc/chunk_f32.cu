@@ -31,7 +31,7 @@ template <int NC> __device__ __forceinline__ int column(int tx, int c) {
     return NC % 4 == 0 ? tx * 4 + c / 4 * 64 + c % 4 : tx + 16 * c;
 }
 
-template <int NC> __global__ void __launch_bounds__(kThreads) chunk_kernel(ChunkParams p) {
+template <int NC> __global__ void __launch_bounds__(kThreads) chunk_kernel(const __grid_constant__ ChunkParams p) {
     constexpr int DP = 16 * NC;
     extern __shared__ __align__(16) float smem[];
     __shared__ int64_t costs[kMaxB + 1];
@@ -42,7 +42,13 @@ template <int NC> __global__ void __launch_bounds__(kThreads) chunk_kernel(Chunk
     float *const sq = smem, *const sk = sq + kRows * pitch;
     float *const sp = sk, *const sv = sk + max(kSlots * pitch, kRows * kPPitch);
     ptx::griddep_wait();
-    find_start<kRows, kSlots>(p, costs, &start);
+    sum_costs<kRows, kSlots>(p, costs);
+    __syncthreads();
+    if (t < 32) {
+        const Start s = find_start<kRows, kSlots>(p, costs);
+        if (t == 0) start = s;
+    }
+    __syncthreads();
     Walk<kRows, kSlots> walk;
     walk.start(p, start);
     int4 head = make_int4(0, 0, 0, 0);
@@ -186,7 +192,7 @@ template <int NC> __global__ void __launch_bounds__(kThreads) chunk_kernel(Chunk
             for (int i = 0; i < 4; ++i)
                 for (int c = 0; c < NC; ++c)
                     if (column<NC>(tx, c) < D)
-                        o[i][c] += taint_of<float>(p, u, walk.t0, walk.t1, lo[i], hi[i], column<NC>(tx, c));
+                        o[i][c] += taint_of<float, kSlots>(p, u, walk.t0, walk.t1, lo[i], hi[i], column<NC>(tx, c));
         if (walk.part) {
             const int64_t slot = walk.slot();
 #pragma unroll

@@ -84,7 +84,7 @@ template <int MT, int NT> __device__ __forceinline__ int64_t sequence_cost(const
     return sum;
 }
 
-// Where a block begins: found by its first warp, then in shared memory for all of them.
+// Where a block begins.
 struct Start {
     int64_t x, x1;           // this block's stretch of all units' tiles and entries
     int64_t unit;            // where the first unit lies
@@ -170,81 +170,80 @@ template <int MT, int NT> struct Walk {
     }
 };
 
-// Finds a block's start; every thread of the block calls it.  costs: kMaxB + 1 numbers in shared memory.
-template <int MT, int NT>
-__device__ __forceinline__ void find_start(const ChunkParams &p, int64_t *costs, Start *start) {
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    for (int b = warp; b < p.B; b += blockDim.x / 32) {
+// The sequences' costs (of one KV head), by all warps of the block; for a barrier to follow.
+template <int MT, int NT> __device__ __forceinline__ void sum_costs(const ChunkParams &p, int64_t *costs) {
+    for (int b = threadIdx.x / 32; b < p.B; b += blockDim.x / 32) {
         const int64_t c = sequence_cost<MT, NT>(p, b);
-        if (lane == 0) costs[b] = c;
+        if (threadIdx.x % 32 == 0) costs[b] = c;
     }
-    __syncthreads();
-    if (warp == 0) {
-        int64_t all = 0;
-        for (int b = lane; b < p.B; b += 32) all += costs[b];
+}
+
+// Finds the block's start; one warp calls it.
+template <int MT, int NT> __device__ __forceinline__ Start find_start(const ChunkParams &p, const int64_t *costs) {
+    const int lane = threadIdx.x % 32;
+    int64_t all = 0;
+    for (int b = lane; b < p.B; b += 32) all += costs[b];
 #pragma unroll
-        for (int d = 16; d > 0; d /= 2) all += __shfl_xor_sync(0xffffffffu, all, d);
-        all *= p.Hkv;
-        Start s;
-        s.chunk = (all + gridDim.x - 1) / gridDim.x;
-        s.x = min(all, s.chunk * blockIdx.x);
-        s.x1 = min(all, s.x + s.chunk);
-        s.unit = s.b = s.hk = s.m = 0;
-        if (s.x < s.x1) {
-            // The sequence: thirty-two at a time.
-            int64_t before = 0;
-            for (int b0 = 0;; b0 += 32) {
-                const int64_t c = b0 + lane < p.B ? costs[b0 + lane] * p.Hkv : 0;
-                int64_t up = c;
+    for (int d = 16; d > 0; d /= 2) all += __shfl_xor_sync(0xffffffffu, all, d);
+    all *= p.Hkv;
+    Start s;
+    s.chunk = (all + gridDim.x - 1) / gridDim.x;
+    s.x = min(all, s.chunk * blockIdx.x);
+    s.x1 = min(all, s.x + s.chunk);
+    s.unit = s.b = s.hk = s.m = 0;
+    if (s.x < s.x1) {
+        // The sequence: thirty-two at a time.
+        int64_t before = 0;
+        for (int b0 = 0;; b0 += 32) {
+            const int64_t c = b0 + lane < p.B ? costs[b0 + lane] * p.Hkv : 0;
+            int64_t up = c;
 #pragma unroll
-                for (int d = 1; d < 32; d *= 2) {
-                    const int64_t v = __shfl_up_sync(0xffffffffu, up, d);
-                    if (lane >= d) up += v;
-                }
-                const unsigned here = __ballot_sync(0xffffffffu, before + up > s.x);
-                const int at = here ? __ffs(here) - 1 : 31;
-                const int64_t own = __shfl_sync(0xffffffffu, c, at), upto = __shfl_sync(0xffffffffu, up, at);
-                if (here) {
-                    s.b = b0 + at;
-                    before += upto - own;
-                    break;
-                }
-                before += upto;
+            for (int d = 1; d < 32; d *= 2) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, up, d);
+                if (lane >= d) up += v;
             }
-            const int64_t cost = costs[s.b];
-            s.hk = (int)((s.x - before) / cost);
-            before += s.hk * cost;
-            // The tile of rows.
-            Unit<MT, NT> u;
-            u.s = sequence_of(p, s.b, false);
-            u.units = (int)(((int64_t)u.s.n * p.G + MT - 1) / MT);
-            for (int m0 = 0; m0 < u.units; m0 += 32) {
-                int64_t c = 0;
-                u.m = m0 + lane;
-                if (u.m < u.units) {
-                    u.tile(p);
-                    c = u.tiles + 1;
-                }
-                int64_t up = c;
-#pragma unroll
-                for (int d = 1; d < 32; d *= 2) {
-                    const int64_t v = __shfl_up_sync(0xffffffffu, up, d);
-                    if (lane >= d) up += v;
-                }
-                const unsigned here = __ballot_sync(0xffffffffu, before + up > s.x);
-                const int at = here ? __ffs(here) - 1 : 31;
-                const int64_t own = __shfl_sync(0xffffffffu, c, at), upto = __shfl_sync(0xffffffffu, up, at);
-                if (here) {
-                    s.m = m0 + at;
-                    s.unit = before + upto - own;
-                    break;
-                }
-                before += upto;
+            const unsigned here = __ballot_sync(0xffffffffu, before + up > s.x);
+            const int at = here ? __ffs(here) - 1 : 31;
+            const int64_t own = __shfl_sync(0xffffffffu, c, at), upto = __shfl_sync(0xffffffffu, up, at);
+            if (here) {
+                s.b = b0 + at;
+                before += upto - own;
+                break;
             }
+            before += upto;
         }
-        if (lane == 0) *start = s;
+        const int64_t cost = costs[s.b];
+        s.hk = (int)((s.x - before) / cost);
+        before += s.hk * cost;
+        // The tile of rows.
+        Unit<MT, NT> u;
+        u.s = sequence_of(p, s.b, false);
+        u.units = (int)(((int64_t)u.s.n * p.G + MT - 1) / MT);
+        for (int m0 = 0; m0 < u.units; m0 += 32) {
+            int64_t c = 0;
+            u.m = m0 + lane;
+            if (u.m < u.units) {
+                u.tile(p);
+                c = u.tiles + 1;
+            }
+            int64_t up = c;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, up, d);
+                if (lane >= d) up += v;
+            }
+            const unsigned here = __ballot_sync(0xffffffffu, before + up > s.x);
+            const int at = here ? __ffs(here) - 1 : 31;
+            const int64_t own = __shfl_sync(0xffffffffu, c, at), upto = __shfl_sync(0xffffffffu, up, at);
+            if (here) {
+                s.m = m0 + at;
+                s.unit = before + upto - own;
+                break;
+            }
+            before += upto;
+        }
     }
-    __syncthreads();
+    return s;
 }
 
 }  // namespace chunk

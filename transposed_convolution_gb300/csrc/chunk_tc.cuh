@@ -64,7 +64,6 @@ template <int DP> struct Sizes {
     static constexpr int kQPanel = 128 * 128, kPanel = kSlots * 128;
     static constexpr int kStage = kPanels * kPanel;
     static constexpr int kStages = DP <= 64 ? 8 : 5;
-    static constexpr int kAhead = DP <= 64 ? 6 : 3;            // copies in flight before the oldest is waited for
     static constexpr int kQ = kTiles * kPanels * kQPanel;
     static constexpr int kSmem = 1024 + kQ + kStages * kStage;
     // TMEM columns.
@@ -72,20 +71,29 @@ template <int DP> struct Sizes {
     static_assert(kO + kTiles * kOPitch <= 512, "TMEM");
 };
 
-constexpr int kThreads = 512, kCopyWarp = 8, kMmaWarp = 12;
+constexpr int kThreads = 512, kCopyWarp = 8, kMmaWarp = 12, kScheduleWarp = 13;
 constexpr int kRing = 8;                                        // tiles whose visible slots are kept
-constexpr int kSegments = 32;                                   // segments whose taint is kept
+constexpr int kSegments = 8;                                    // segments that the schedule is ahead
 constexpr uint64_t kWaitLimitNs = 2000000000;                   // of a block's waits for itself
-constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;              // 256 (192 + 64) = 512 * 128
+constexpr int kSoftmaxRegs = 192, kCopyRegs = 80, kMmaRegs = 48;  // 256 * 192 + 128 (80 + 48) = 512 * 128
+
+// What the roles know of a segment: the unit (as in Unit) and its tiles [t0, t1); none: the end.
+struct Segment {
+    Sequence s;
+    int b, hk, m, r0, rows, lo, hi, lo_last, hi_first, first;
+    int t0, t1;
+    int part, begins, parts; // as in Walk
+    int taint;               // values that are no numbers were taken out of V
+};
 
 struct Shared {
     // Whoever waits at a barrier waits for each of its phases in turn, or knows by what it has seen
     // that the earlier ones are over: a wait tells only odd phases from even ones.  So where one tile of
     // rows uses both S buffers, the second has barriers of its own ([2]).
     uint64_t kv_full[8], kv_empty[8], q_full, q_empty, s_full[3], p_full[3], o_full[2], drained;
-    Start start;
+    uint64_t segment_full[kSegments], segment_empty[kSegments];
+    Segment segments[kSegments];
     uint32_t visible[kRing][4];
-    int taint[kSegments];
     uint32_t tmem;
     volatile int abort;
 };
@@ -98,6 +106,55 @@ __device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity)
 __device__ __forceinline__ void give_up(Shared &sh, const ChunkParams &p) {
     sh.abort = 1;
     if (threadIdx.x % 32 == 0) atomicOr(p.cache.status, kStatusTimeout);
+}
+
+// The next segment's description, or null at the end (ok stays) or when a wait fails; and done with one.
+__device__ __forceinline__ Segment *next_segment(Shared &sh, int no, bool &ok) {
+    ok = wait(sh, &sh.segment_full[no % kSegments], no / kSegments & 1);
+    Segment *s = &sh.segments[no % kSegments];
+    return ok && s->t1 > s->t0 ? s : nullptr;
+}
+__device__ __forceinline__ void segment_done(Shared &sh, int no) {
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) ptx::mbar_arrive(&sh.segment_empty[no % kSegments]);
+}
+
+// Describes the block's segments, ahead of the roles that work on them.
+template <int MT, int NT>
+__device__ __forceinline__ bool schedule(const ChunkParams &p, Shared &sh, const int64_t *costs) {
+    Walk<MT, NT> walk;
+    walk.start(p, find_start<MT, NT>(p, costs));
+    for (int no = 0;; ++no) {
+        const bool more = walk.next(p);
+        if (!wait(sh, &sh.segment_empty[no % kSegments], (no / kSegments & 1) ^ 1)) return false;
+        if (threadIdx.x % 32 == 0) {
+            const Unit<MT, NT> &u = walk.u;
+            Segment &s = sh.segments[no % kSegments];
+            s.t0 = s.t1 = 0;
+            if (more) {
+                s.s = u.s;
+                s.b = u.b;
+                s.hk = u.hk;
+                s.m = u.m;
+                s.r0 = u.r0;
+                s.rows = u.rows;
+                s.lo = u.lo;
+                s.hi = u.hi;
+                s.lo_last = u.lo_last;
+                s.hi_first = u.hi_first;
+                s.first = u.first;
+                s.t0 = walk.t0;
+                s.t1 = walk.t1;
+                s.part = walk.part;
+                s.begins = walk.begins;
+                s.parts = walk.parts();
+                s.taint = 0;
+            }
+            ptx::mbar_arrive(&sh.segment_full[no % kSegments]);
+        }
+        __syncwarp();
+        if (!more) return true;
+    }
 }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool on) {
@@ -162,6 +219,37 @@ __device__ __forceinline__ uint32_t range_bits(int j, int lo, int hi) {
     return (uint32_t)((1ull << b) - (1ull << min(a, b)));
 }
 
+// Takes values that are no numbers out of this thread's part of a V stage (see taint); whether there
+// were any.
+template <typename T, int DP> __device__ __noinline__ bool take_out(uint32_t stage, int D) {
+    typedef Sizes<DP> Z;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 - kCopyWarp;
+    bool found = false;
+    for (int panel = 0; panel * 64 < D; ++panel) {
+        if (panel * 64 + lane % 8 * 8 >= D) continue;
+        for (int r = lane / 8; r < Z::kSlots / 4; r += 4) {
+            const int row = warp * (Z::kSlots / 4) + r;
+            const uint32_t at = stage + panel * Z::kPanel + row * 128 + ((lane ^ row) & 7) * 16;
+            uint32_t v[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
+            bool bad = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                constexpr uint32_t kE = Half<T>::kExponent;
+                if ((v[i] & kE) == kE) v[i] &= 0xffff0000u, bad = true;
+                if ((v[i] >> 16 & kE) == kE) v[i] &= 0x0000ffffu, bad = true;
+            }
+            if (bad) {
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]),
+                             "r"(v[2]), "r"(v[3]) : "memory");
+                found = true;
+            }
+        }
+    }
+    return found;
+}
+
 // ------------------------------------------------------------------------------------------------
 // Copies.  Each of the four warps has a quarter of a tile's slots: a lane looks one up, then eight
 // lanes copy 128 bytes of one.
@@ -170,159 +258,119 @@ template <typename T, int DP> struct Copier {
     const ChunkParams &p;
     Shared &sh;
     uint32_t q_smem, kv_smem;
-    int items = 0, flying = 0;
-    // What is in flight, the last one first: the barrier to arrive at, and whether to look for values that
-    // are no numbers.
-    uint32_t queue[Z::kAhead + 1];
-    static constexpr uint32_t kIsQ = 1u << 31, kLook = 1u << 30;
+    int items;
+    int looked;              // the stage of a V tile that is still to be looked through, or -1,
+    int looked_in;           // its segment,
+    bool left;               // and whether that is done but for this
 
-    __device__ __forceinline__ Copier(const ChunkParams &p, Shared &sh, uint32_t q, uint32_t kv)
-        : p(p), sh(sh), q_smem(q), kv_smem(kv) {}
-
-    // Waits for the oldest copy and passes it on.
-    __device__ __forceinline__ void retire() {
-        uint32_t e = 0;
-#pragma unroll
-        for (int i = 0; i <= Z::kAhead; ++i)
-            if (flying == i + 1) {
-                e = queue[i];
-                switch (i) {
-                case 0: copy_wait<0>(); break;
-                case 1: copy_wait<1>(); break;
-                case 2: copy_wait<2>(); break;
-                case 3: copy_wait<3>(); break;
-                case 4: copy_wait<4>(); break;
-                case 5: copy_wait<5>(); break;
-                default: copy_wait<6>(); break;
-                }
-            }
-        --flying;
-        const int stage = e & 15;
-        if (e & kLook) look(stage, (int)(e >> 4 & 0x3ffffff));
+    // The barrier's phase ends when this thread's copies, and those of all others, have arrived.
+    __device__ __forceinline__ void arrive(uint64_t *bar) {
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
+    }
+    // Looks a V tile through (see taint) once its copies, all but the last kLater groups, have arrived.
+    template <int kLater> __device__ __forceinline__ void look() {
+        if (looked < 0) return;
+        copy_wait<kLater>();
+        if (take_out<T, DP>(kv_smem + looked * Z::kStage, p.D))
+            sh.segments[looked_in % kSegments].taint = 1;
         fence_async();
-        ptx::mbar_arrive(e & kIsQ ? &sh.q_full : &sh.kv_full[stage]);
+        ptx::mbar_arrive(&sh.kv_full[looked]);
+        looked = -1;
+        if (left) segment_done(sh, looked_in);
+        left = false;
     }
-    __device__ __forceinline__ void push(uint32_t e) {
-        copy_commit();
-#pragma unroll
-        for (int i = Z::kAhead; i > 0; --i) queue[i] = queue[i - 1];
-        queue[0] = e;
-        if (++flying > Z::kAhead) retire();
-    }
-    // Waits until a barrier's phase is over; what is in flight is passed on meanwhile, because whoever
-    // completes that phase may be waiting for it.
+    // Waits for a phase; whoever completes it may be waiting for the tile that is to be looked through.
     __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity) {
-        while (!__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) {
-            if (flying == 0) return wait(sh, bar, parity);
-            retire();
-        }
-        return true;
+        if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+        look<0>();
+        return wait(sh, bar, parity);
     }
 
-    // Takes values that are no numbers out of this thread's part of a V stage (see taint).
-    __device__ __noinline__ void look(int stage, int segment) {
-        const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 - kCopyWarp;
-        const uint32_t base = kv_smem + stage * Z::kStage;
-        bool found = false;
-        for (int panel = 0; panel * 64 < p.D; ++panel) {
-            if (panel * 64 + lane % 8 * 8 >= p.D) continue;
-            for (int r = lane / 8; r < Z::kSlots / 4; r += 4) {
-                const int row = warp * (Z::kSlots / 4) + r;
-                const uint32_t at = base + panel * Z::kPanel + row * 128 + ((lane ^ row) & 7) * 16;
-                uint32_t v[4];
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at) : "memory");
-                bool bad = false;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    constexpr uint32_t kE = Half<T>::kExponent;
-                    if ((v[i] & kE) == kE) v[i] &= 0xffff0000u, bad = true;
-                    if ((v[i] >> 16 & kE) == kE) v[i] &= 0x0000ffffu, bad = true;
-                }
-                if (bad) {
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]),
-                                 "r"(v[2]), "r"(v[3]) : "memory");
-                    found = true;
-                }
-            }
-        }
-        if (found) sh.taint[segment % kSegments] = segment;
-    }
-
-    // Rows of 128-byte panels: lane l's row is at `from` + `mine` elements of 16 (`on`: it is there).
-    __device__ __forceinline__ void copy_rows(uint32_t dst, int panel_bytes, int row0, int rows, const T *from,
-                                              uint32_t mine, bool on) {
-        const int lane = threadIdx.x % 32;
+    // kRows rows of a warp, panels of 128 bytes: lane l's row is at `from` + `mine` elements, if there is one.
+    template <int kRows, int kPanel, typename Offset>
+    __device__ __forceinline__ void copy_rows(uint32_t dst, const T *from, Offset mine, bool on, int unit) {
+        const int lane = threadIdx.x % 32, column = lane % 8 * 8;
         const unsigned there = __ballot_sync(0xffffffffu, on);
+        const uint32_t to = dst + lane / 8 * 128 + ((lane ^ lane / 8) & 7) * 16;
+        from += column;
 #pragma unroll
-        for (int r0 = 0; r0 < rows; r0 += 4) {
-            const int r = r0 + lane / 8, row = row0 + r;
-            const T *src = from + (uint64_t)__shfl_sync(0xffffffffu, mine, r) * 16 + lane % 8 * 8;
+        for (int r0 = 0; r0 < kRows; r0 += 4) {
+            const int r = r0 + lane / 8;
+            const T *src = from + (int64_t)__shfl_sync(0xffffffffu, mine, r) * unit;
             const bool ok = there >> r & 1;
-            const uint32_t to = dst + row * 128 + ((lane ^ row) & 7) * 16;
+            // (The swizzle is the row's last three bits; every other step changes the third.)
+            const uint32_t at = (to ^ (r0 % 8 ? 64 : 0)) + r0 * 128;
 #pragma unroll
             for (int panel = 0; panel < Z::kPanels; ++panel)
-                if (panel * 64 + lane % 8 * 8 < p.D)
-                    copy16(to + panel * panel_bytes, ok ? src + panel * 64 : from, ok);
+                if (panel * 64 + column < p.D) copy16(at + panel * kPanel, src + panel * 64, ok);
         }
     }
 
-    __device__ __forceinline__ bool run(const Start &start) {
-        Walk<Z::kRows, Z::kSlots> walk;
-        walk.start(p, start);
+    __device__ __forceinline__ bool run() {
         const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 - kCopyWarp;
         constexpr int kOwn = Z::kSlots / 4;
-        int segment = 0, tiles = 0;
-        while (walk.next(p)) {
-            const auto &u = walk.u;
-            ++segment;
-            for (int t = walk.t0; t < walk.t1; ++t, ++tiles) {
+        int tiles = 0;
+        bool ok;
+        items = 0;
+        looked = -1;
+        left = false;
+        for (int no = 0;; ++no) {
+            const Segment *const next = next_segment(sh, no, ok);
+            if (!next) {
+                look<0>();
+                return ok;
+            }
+            const Segment &u = *next;
+            const int t0 = u.t0, t1 = u.t1;
+            for (int t = t0; t < t1; ++t, ++tiles) {
                 const int j0 = (u.first + t) * Z::kSlots;
                 const bool edge = is_edge(u, j0, Z::kSlots);
                 const int64_t at = lane < kOwn ? cache_row(p, u, j0 + warp * kOwn + lane) : -1;
-                const uint32_t mine = (uint32_t)(at >> 4);
+                const bool on = at >= 0;
+                const uint32_t mine = on ? (uint32_t)(at >> 4) : 0u;
+                const unsigned seen = __ballot_sync(0xffffffffu, on);
+                // K, on the first tile Q, and V.
                 for (int kv = 0; kv < 2; ++kv, ++items) {
                     const int stage = items % Z::kStages;
                     if (!wait_for(&sh.kv_empty[stage], (items / Z::kStages & 1) ^ 1)) return false;
-                    copy_rows(kv_smem + stage * Z::kStage, Z::kPanel, warp * kOwn, kOwn,
-                              (const T *)(kv ? p.v : p.k), mine, at >= 0);
+                    copy_rows<kOwn, Z::kPanel>(kv_smem + stage * Z::kStage + warp * kOwn * 128,
+                                               (const T *)(kv ? p.v : p.k), mine, on, 16);
+                    copy_commit();
                     if (kv == 0) {
-                        const unsigned seen = __ballot_sync(0xffffffffu, at >= 0);
                         if (lane == 0) {
                             if (kOwn == 32) sh.visible[tiles % kRing][warp] = seen;
                             else reinterpret_cast<uint16_t *>(sh.visible[tiles % kRing])[warp] = (uint16_t)seen;
                         }
+                        arrive(&sh.kv_full[stage]);
+                        look<1>();
+                        if (t == t0 && !queries(u, no)) return false;
+                    } else if (edge) {
+                        looked = stage;
+                        looked_in = no;
+                    } else {
+                        arrive(&sh.kv_full[stage]);
                     }
-                    push(stage | (kv && edge ? kLook | (uint32_t)segment << 4 : 0u));
-                }
-                if (t == walk.t0) {
-                    // Q behind the first tile, which need not wait for the segment before.
-                    if (!wait_for(&sh.q_empty, (segment & 1))) return false;
-                    for (int tile = 0; tile < Z::kTiles && tile * 128 < u.rows; ++tile) {
-                        const int r = tile * 128 + warp * 32 + lane;
-                        const bool on = r < u.rows;
-                        copy_q(q_smem + tile * Z::kPanels * Z::kQPanel, warp * 32, on ? query_offset(p, u, r) : 0,
-                               on);
-                    }
-                    push(kIsQ);
                 }
             }
+            // The last tile is looked through behind the next segment's first copies.
+            left = looked >= 0;
+            if (!left) segment_done(sh, no);
         }
-        while (flying > 0) retire();
-        return true;
     }
-    __device__ __forceinline__ void copy_q(uint32_t dst, int row0, int64_t mine, bool on) {
-        const int lane = threadIdx.x % 32;
-        const unsigned there = __ballot_sync(0xffffffffu, on);
-        for (int r0 = 0; r0 < 32; r0 += 4) {
-            const int r = r0 + lane / 8, row = row0 + r;
-            const T *src = (const T *)p.q + __shfl_sync(0xffffffffu, mine, r) + lane % 8 * 8;
-            const bool ok = there >> r & 1;
-            const uint32_t to = dst + row * 128 + ((lane ^ row) & 7) * 16;
-            for (int panel = 0; panel < Z::kPanels; ++panel)
-                if (panel * 64 + lane % 8 * 8 < p.D)
-                    copy16(to + panel * Z::kQPanel, ok ? src + panel * 64 : (const T *)p.q, ok);
+    __device__ __forceinline__ bool queries(const Segment &u, int no) {
+        const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 - kCopyWarp;
+        if (!wait_for(&sh.q_empty, (no & 1) ^ 1)) return false;
+#pragma unroll
+        for (int tile = 0; tile < Z::kTiles; ++tile) {
+            if (tile * 128 >= u.rows) break;
+            const int r = tile * 128 + warp * 32 + lane;
+            const bool on = r < u.rows;
+            const int64_t mine = on ? query_offset(p, u, r) : 0;
+            copy_rows<32, Z::kQPanel>(q_smem + tile * Z::kPanels * Z::kQPanel + warp * 32 * 128, (const T *)p.q,
+                                      mine, on, 1);
         }
+        arrive(&sh.q_full);
+        return true;
     }
 };
 
@@ -365,18 +413,26 @@ template <typename T, int DP> struct Multiplier {
     __device__ __forceinline__ void release(uint64_t *bar) {
         if (ptx::elect_one()) ptx::mma_commit(bar);
     }
+    // Waits for copies, whose writes the products then see.
+    __device__ __forceinline__ bool arrived(uint64_t *bar, uint32_t parity) {
+        const bool ok = wait(sh, bar, parity);
+        fence_async();
+        return ok;
+    }
     __device__ __forceinline__ bool arrived(int item) {
-        return wait(sh, &sh.kv_full[item % Z::kStages], item / Z::kStages & 1);
+        return arrived(&sh.kv_full[item % Z::kStages], item / Z::kStages & 1);
     }
 
-    __device__ __forceinline__ bool run(const Start &start) {
-        Walk<Z::kRows, Z::kSlots> walk;
-        walk.start(p, start);
-        int segment = 0, items = 0, p_count[3] = {0, 0, 0};
-        while (walk.next(p)) {
-            const int n = walk.t1 - walk.t0;
-            const bool dual = walk.u.rows > 128;
-            if (!wait(sh, &sh.q_full, segment & 1) || !arrived(items)) return false;
+    __device__ __forceinline__ bool run() {
+        int items = 0, p_count[3] = {0, 0, 0};
+        bool ok;
+        for (int no = 0;; ++no) {
+            const Segment *const u = next_segment(sh, no, ok);
+            if (!u) return ok;
+            const int n = u->t1 - u->t0;
+            const bool dual = u->rows > 128;
+            segment_done(sh, no);
+            if (!arrived(&sh.q_full, no & 1) || !arrived(items)) return false;
             ptx::tc_fence_after();
             scores(0, 0, items % Z::kStages);
             commit(&sh.s_full[0]);
@@ -429,9 +485,7 @@ template <typename T, int DP> struct Multiplier {
                     release(&sh.kv_empty[v]);
                 }
             }
-            ++segment;
         }
-        return true;
     }
 };
 
@@ -459,22 +513,23 @@ template <typename T, int DP> struct Softmax {
         }
     }
 
-    __device__ __forceinline__ bool run(const Start &start) {
-        Walk<Z::kRows, Z::kSlots> walk;
-        walk.start(p, start);
+    __device__ __forceinline__ bool run() {
         const int r = tile * 128 + threadIdx.x % 128;
         // Scores of a negative or zero scale are multiplied before they are compared.
         const bool early = p.scale_log2 <= 0.0f;
         const float scale = early ? 1.0f : p.scale_log2;
-        int segment = 0, tiles = 0, o_count = 0, s_count[2] = {0, 0};    // s_count: own barrier, and [2]
+        int tiles = 0, o_count = 0, s_count[2] = {0, 0};    // s_count: own barrier, and [2]
         int4 head = make_int4(0, 0, 0, 0);
-        while (walk.next(p)) {
-            const auto &u = walk.u;
-            const int n = walk.t1 - walk.t0;
+        bool ok;
+        for (int no = 0;; ++no) {
+            const Segment *const next = next_segment(sh, no, ok);
+            if (!next) break;
+            const Segment &u = *next;
+            const int n = u.t1 - u.t0, from = (u.first + u.t0) * kN;
             const bool dual = u.rows > 128;
-            ++segment;
             if (tile == 1 && !dual) {
                 tiles += n;
+                segment_done(sh, no);
                 continue;
             }
             const bool mine = r < u.rows;
@@ -483,7 +538,7 @@ template <typename T, int DP> struct Softmax {
             for (int t = 0; t < n; ++t, ++tiles) {
                 const bool second = !dual && (t & 1);
                 const int buffer = dual ? tile : t & 1, bar = second ? 2 : tile;
-                const int j0 = (u.first + walk.t0 + t) * kN;
+                const int j0 = from + t * kN;
                 const uint32_t parity = (second ? s_count[1]++ : s_count[0]++) & 1;
                 if (!wait(sh, &sh.s_full[bar], parity)) return false;
                 ptx::tc_fence_after();
@@ -553,31 +608,31 @@ template <typename T, int DP> struct Softmax {
                 }
                 l = l * factor + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
                 ptx::tmem_wait_st();
+                // The product before the last has to be over before the last can be: the wait behind the
+                // loop would take the one's end for the other's.
+                if (t == n - 1 && t > 0 && !wait(sh, &sh.o_full[tile], (o_count + t - 1) & 1)) return false;
                 ptx::tc_fence_before();
                 ptx::mbar_arrive(&sh.p_full[bar]);
             }
             o_count += n;
-            // (The last scores were ready when all products with V but the last two were.)
-            if (n > 1 && !wait(sh, &sh.o_full[tile], (o_count - 2) & 1)) return false;
             if (!wait(sh, &sh.o_full[tile], (o_count - 1) & 1)) return false;
             ptx::tc_fence_after();
-            const bool tainted = *(volatile int *)&sh.taint[segment % kSegments] == segment;
-            output(walk, r, mine, lo, hi, base, l, tainted);
-            if (walk.part && walk.begins && tile == 0) head = make_int4(u.b, u.hk, u.m, walk.parts());
+            output(u, r, mine, lo, hi, base, l);
+            if (u.part && u.begins) head = make_int4(u.b, u.hk, u.m, u.parts);
+            segment_done(sh, no);
         }
         if (threadIdx.x == 0 && !p.whole) p.heads[blockIdx.x] = head;
-        return true;
+        return ok;
     }
 
-    template <typename W>
-    __device__ __forceinline__ void output(const W &walk, int r, bool mine, int lo, int hi, float base, float l,
-                                           bool tainted) {
-        const auto &u = walk.u;
+    __device__ __forceinline__ void output(const Segment &u, int r, bool mine, int lo, int hi, float base,
+                                           float l) {
+        const bool part = u.part, tainted = *(const volatile int *)&u.taint;
         const uint32_t o = tmem + Z::kO + tile * Z::kOPitch;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const int64_t slot = walk.slot();
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (u.begins ? 1 : 0);    // as in Walk
         T *to = (T *)p.out + (mine ? output_offset(p, u, r) : 0);
-        if (walk.part && mine) p.part_ml[slot * Z::kRows + r] = make_float2(base, l);
+        if (part && mine) p.part_ml[slot * Z::kRows + r] = make_float2(base, l);
         for (int d = 0; d < p.D; d += 16) {
             uint32_t v[16];
             __syncwarp();
@@ -587,8 +642,8 @@ template <typename T, int DP> struct Softmax {
             if (tainted)
                 for (int i = 0; i < 16; ++i)
                     v[i] = __float_as_uint(__uint_as_float(v[i]) +
-                                           taint_of<T>(p, u, walk.t0, walk.t1, lo, hi, d + i));
-            if (walk.part) {
+                                           taint_of<T, kN>(p, u, u.t0, u.t1, lo, hi, d + i));
+            if (part) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     p.part_o[(slot * p.D + d + i) * Z::kRows + r] = __uint_as_float(v[i]);
@@ -608,7 +663,7 @@ template <typename T, int DP> struct Softmax {
     }
 };
 
-template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(ChunkParams p) {
+template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__ ChunkParams p) {
     typedef Sizes<DP> Z;
     extern __shared__ unsigned char dynamic[];
     __shared__ Shared sh;
@@ -622,6 +677,10 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 1) tc_
         ptx::mbar_init(&sh.q_full, 128);
         ptx::mbar_init(&sh.q_empty, 1);
         ptx::mbar_init(&sh.drained, 1);
+        for (int i = 0; i < kSegments; ++i) {
+            ptx::mbar_init(&sh.segment_full[i], 1);
+            ptx::mbar_init(&sh.segment_empty[i], 4 * Z::kTiles + 5);     // warps
+        }
         for (int i = 0; i < 3; ++i) {
             ptx::mbar_init(&sh.s_full[i], 2);
             ptx::mbar_init(&sh.p_full[i], 128);
@@ -631,14 +690,14 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 1) tc_
         ptx::fence_mbar_init();
         sh.abort = 0;
     }
-    if (threadIdx.x < kSegments) sh.taint[threadIdx.x] = 0;
     if (warp == kMmaWarp) {
         ptx::tmem_alloc(&sh.tmem, 512);
         ptx::tmem_relinquish();
     }
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    find_start<Z::kRows, Z::kSlots>(p, reinterpret_cast<int64_t *>(dynamic + (smem - raw)), &sh.start);
+    int64_t *const costs = reinterpret_cast<int64_t *>(dynamic + (smem - raw));    // where Q will be
+    sum_costs<Z::kRows, Z::kSlots>(p, costs);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -648,17 +707,22 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 1) tc_
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         if (warp / 4 < Z::kTiles) {
             Softmax<T, DP> softmax{p, sh, tmem + ((uint32_t)(warp % 4 * 32) << 16), warp / 4};
-            ok = softmax.run(sh.start);
+            ok = softmax.run();
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp < kMmaWarp) {
-            Copier<T, DP> copier(p, sh, q_smem, kv_smem);
-            ok = copier.run(sh.start);
-            if (!ok) copy_wait<0>();
-        } else if (warp == kMmaWarp) {
-            Multiplier<T, DP> multiplier{p, sh, q_smem, kv_smem, tmem};
-            ok = multiplier.run(sh.start);
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
+            Copier<T, DP> copier{p, sh, q_smem, kv_smem};
+            ok = copier.run();
+            copy_wait<0>();
+        } else {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+            if (warp == kMmaWarp) {
+                Multiplier<T, DP> multiplier{p, sh, q_smem, kv_smem, tmem};
+                ok = multiplier.run();
+            } else if (warp == kScheduleWarp) {
+                ok = schedule<Z::kRows, Z::kSlots>(p, sh, costs);
+            }
         }
     }
     if (!ok) give_up(sh, p);
