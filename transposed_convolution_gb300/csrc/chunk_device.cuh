@@ -33,16 +33,16 @@ template <typename U> __device__ __forceinline__ int64_t output_offset(const Chu
 
 // First element of a unit's slot j, or -1 for slots that no row of it attends to (their pages may
 // be gone) and for pages out of range, which are reported.
-template <typename U> __device__ __forceinline__ int64_t cache_row(const ChunkParams &p, const U &u, int j) {
+template <typename U>
+__device__ __forceinline__ int64_t cache_row(const CacheView &c, int page_shift, const U &u, int j) {
     if (j < u.lo || j >= u.hi) return -1;
-    const int at = p.page_shift >= 0 ? j >> p.page_shift : j / p.cache.page;
-    const int pg = p.cache.tables[(int64_t)u.b * p.cache.table_pitch + at];
-    if ((unsigned)pg >= (unsigned)p.cache.num_pages) {
-        atomicOr(p.cache.status, kStatusBadPage);
+    const int at = page_shift >= 0 ? j >> page_shift : j / c.page;
+    const int pg = c.tables[(int64_t)u.b * c.table_pitch + at];
+    if ((unsigned)pg >= (unsigned)c.num_pages) {
+        atomicOr(c.status, kStatusBadPage);
         return -1;
     }
-    return pg * p.cache.page_stride + u.hk * p.cache.head_stride +
-           (int64_t)(j - at * p.cache.page) * p.cache.row_stride;
+    return pg * c.page_stride + u.hk * c.head_stride + (int64_t)(j - at * c.page) * c.row_stride;
 }
 
 // Whether some row does not attend to all of the slots [j0, j0 + n).
@@ -74,19 +74,20 @@ template <typename T> __device__ __forceinline__ void store8(T *to, const float 
 // that a row does not attend to would be NaN.  So infinities and NaN are taken out of V in the tiles that
 // some row attends to in part, and the unit is marked.  This is what they add to one output: the
 // infinities and NaN among the slots [lo, hi) of those tiles of the segment.
-// (By value: a unit whose address is taken would live in local memory.)
+// (By value: what has its address taken is in memory from then on.)
 struct Edges {
-    int b, hk, lo, hi, lo_last, hi_first, first;
+    CacheView cache;
+    const void *v;
+    int page_shift, b, hk, lo, hi, lo_last, hi_first, first;
 };
-template <typename T, int NT>
-__device__ __noinline__ float taint(const ChunkParams &p, Edges u, int t0, int t1, int lo, int hi, int d) {
+template <typename T, int NT> __device__ __noinline__ float taint(Edges u, int t0, int t1, int lo, int hi, int d) {
     float sum = 0.0f;
     for (int tile = t0; tile < t1; ++tile) {
         const int j0 = (u.first + tile) * NT;
         if (!is_edge(u, j0, NT)) continue;
         for (int j = max(lo, j0); j < min(hi, j0 + NT); ++j) {
-            const int64_t at = cache_row(p, u, j);
-            const float v = at < 0 ? 0.0f : widen(((const T *)p.v)[at + d]);
+            const int64_t at = cache_row(u.cache, u.page_shift, u, j);
+            const float v = at < 0 ? 0.0f : widen(((const T *)u.v)[at + d]);
             if (!isfinite(v)) sum += v;
         }
     }
@@ -95,8 +96,8 @@ __device__ __noinline__ float taint(const ChunkParams &p, Edges u, int t0, int t
 template <typename T, int NT, typename U>
 __device__ __forceinline__ float taint_of(const ChunkParams &p, const U &u, int t0, int t1, int lo,
                                           int hi, int d) {
-    const Edges e = {u.b, u.hk, u.lo, u.hi, u.lo_last, u.hi_first, u.first};
-    return taint<T, NT>(p, e, t0, t1, lo, hi, d);
+    const Edges e = {p.cache, p.v, p.page_shift, u.b, u.hk, u.lo, u.hi, u.lo_last, u.hi_first, u.first};
+    return taint<T, NT>(e, t0, t1, lo, hi, d);
 }
 
 }  // namespace chunk

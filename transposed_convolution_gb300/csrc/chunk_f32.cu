@@ -31,7 +31,7 @@ template <int NC> __device__ __forceinline__ int column(int tx, int c) {
     return NC % 4 == 0 ? tx * 4 + c / 4 * 64 + c % 4 : tx + 16 * c;
 }
 
-template <int NC> __global__ void __launch_bounds__(kThreads) chunk_kernel(const __grid_constant__ ChunkParams p) {
+template <int NC> __global__ void __launch_bounds__(kThreads) chunk_kernel(ChunkParams p) {
     constexpr int DP = 16 * NC;
     extern __shared__ __align__(16) float smem[];
     __shared__ int64_t costs[kMaxB + 1];
@@ -84,7 +84,7 @@ template <int NC> __global__ void __launch_bounds__(kThreads) chunk_kernel(const
             {
                 // Four threads a slot.
                 const int r = t / 4, j = j0 + r;
-                const int64_t at = cache_row(p, u, j);
+                const int64_t at = cache_row(p.cache, p.page_shift, u, j);
                 hidden = at < 0 && j >= u.lo && j < u.hi;
                 if (t % 4 == 0) visible[r] = at >= 0;
                 for (int d = t % 4 * 4; d < D; d += 16) {

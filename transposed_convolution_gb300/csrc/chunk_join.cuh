@@ -8,7 +8,7 @@ namespace chunk {
 
 // Joins the parts of the unit that block x of the attention began: a warp has thirty-two rows and eight
 // columns, and takes the parts four at a time, so that it has 32 loads in flight.  What it reads is in L2.
-template <typename T, int MT> __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ ChunkParams p) {
+template <typename T, int MT> __global__ void __launch_bounds__(256) join_kernel(ChunkParams p) {
     ptx::griddep_wait();
     const int4 head = p.heads[blockIdx.x];
     if (head.w == 0) return;

@@ -84,6 +84,11 @@ template <int MT, int NT> __device__ __forceinline__ int64_t sequence_cost(const
     return sum;
 }
 
+// a / b, a >= 0 and b > 0: mostly both have 32 bits, whose division takes a fifth of the time.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // Where a block begins.
 struct Start {
     int64_t x, x1;           // this block's stretch of all units' tiles and entries
@@ -166,7 +171,7 @@ template <int MT, int NT> struct Walk {
     __device__ __forceinline__ int64_t slot() const { return 2 * (int64_t)blockIdx.x + (begins ? 1 : 0); }
     // Parts of the unit whose first one this is.
     __device__ __forceinline__ int parts() const {
-        return (int)((unit + u.tiles) / chunk) - (int)blockIdx.x + 1;
+        return (int)divide(unit + u.tiles, chunk) - (int)blockIdx.x + 1;
     }
 };
 
@@ -187,7 +192,7 @@ template <int MT, int NT> __device__ __forceinline__ Start find_start(const Chun
     for (int d = 16; d > 0; d /= 2) all += __shfl_xor_sync(0xffffffffu, all, d);
     all *= p.Hkv;
     Start s;
-    s.chunk = (all + gridDim.x - 1) / gridDim.x;
+    s.chunk = divide(all + gridDim.x - 1, gridDim.x);
     s.x = min(all, s.chunk * blockIdx.x);
     s.x1 = min(all, s.x + s.chunk);
     s.unit = s.b = s.hk = s.m = 0;
@@ -213,7 +218,7 @@ template <int MT, int NT> __device__ __forceinline__ Start find_start(const Chun
             before += upto;
         }
         const int64_t cost = costs[s.b];
-        s.hk = (int)((s.x - before) / cost);
+        s.hk = (int)divide(s.x - before, cost);
         before += s.hk * cost;
         // The tile of rows.
         Unit<MT, NT> u;

@@ -98,11 +98,15 @@ struct Shared {
     volatile int abort;
 };
 
+// Bounded; every lane asks, and the answer is a vote: behind a branch the compiler takes the warp for
+// divided, and its products and TMEM accesses for many (which took twice the time).
+__device__ __forceinline__ bool tested(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity));
+}
 __device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity) {
-    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+    if (tested(bar, parity)) return true;
     return ptx::mbar_wait_warp(bar, parity, kWaitLimitNs, &sh.abort);
 }
-
 __device__ __forceinline__ void give_up(Shared &sh, const ChunkParams &p) {
     sh.abort = 1;
     if (threadIdx.x % 32 == 0) atomicOr(p.cache.status, kStatusTimeout);
@@ -117,6 +121,7 @@ __device__ __forceinline__ Segment *next_segment(Shared &sh, int no, bool &ok) {
 __device__ __forceinline__ void segment_done(Shared &sh, int no) {
     __syncwarp();
     if (threadIdx.x % 32 == 0) ptx::mbar_arrive(&sh.segment_empty[no % kSegments]);
+    __syncwarp();
 }
 
 // Describes the block's segments, ahead of the roles that work on them.
@@ -213,6 +218,31 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
                  : "memory");
 }
 
+// Two fp32 operations an instruction, which halves what a score costs to issue.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // The slots [j0 + 32 w, + 32) that lie in [lo, hi), as bits.
 __device__ __forceinline__ uint32_t range_bits(int j, int lo, int hi) {
     const int a = min(max(lo - j, 0), 32), b = min(max(hi - j, 0), 32);
@@ -273,27 +303,30 @@ template <typename T, int DP> struct Copier {
         copy_wait<kLater>();
         if (take_out<T, DP>(kv_smem + looked * Z::kStage, p.D))
             sh.segments[looked_in % kSegments].taint = 1;
+        __syncwarp();
         fence_async();
         ptx::mbar_arrive(&sh.kv_full[looked]);
         looked = -1;
         if (left) segment_done(sh, looked_in);
         left = false;
+        __syncwarp();
     }
     // Waits for a phase; whoever completes it may be waiting for the tile that is to be looked through.
     __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity) {
-        if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+        if (tested(bar, parity)) return true;
         look<0>();
         return wait(sh, bar, parity);
     }
 
     // kRows rows of a warp, panels of 128 bytes: lane l's row is at `from` + `mine` elements, if there is one.
-    template <int kRows, int kPanel, typename Offset>
+    template <int kRows, int kPanel, int kUnroll, typename Offset>
     __device__ __forceinline__ void copy_rows(uint32_t dst, const T *from, Offset mine, bool on, int unit) {
         const int lane = threadIdx.x % 32, column = lane % 8 * 8;
         const unsigned there = __ballot_sync(0xffffffffu, on);
+        const int D = p.D;
         const uint32_t to = dst + lane / 8 * 128 + ((lane ^ lane / 8) & 7) * 16;
         from += column;
-#pragma unroll
+#pragma unroll kUnroll
         for (int r0 = 0; r0 < kRows; r0 += 4) {
             const int r = r0 + lane / 8;
             const T *src = from + (int64_t)__shfl_sync(0xffffffffu, mine, r) * unit;
@@ -302,7 +335,7 @@ template <typename T, int DP> struct Copier {
             const uint32_t at = (to ^ (r0 % 8 ? 64 : 0)) + r0 * 128;
 #pragma unroll
             for (int panel = 0; panel < Z::kPanels; ++panel)
-                if (panel * 64 + column < p.D) copy16(at + panel * kPanel, src + panel * 64, ok);
+                if (panel * 64 + column < D) copy16(at + panel * kPanel, src + panel * 64, ok);
         }
     }
 
@@ -325,7 +358,7 @@ template <typename T, int DP> struct Copier {
             for (int t = t0; t < t1; ++t, ++tiles) {
                 const int j0 = (u.first + t) * Z::kSlots;
                 const bool edge = is_edge(u, j0, Z::kSlots);
-                const int64_t at = lane < kOwn ? cache_row(p, u, j0 + warp * kOwn + lane) : -1;
+                const int64_t at = lane < kOwn ? cache_row(p.cache, p.page_shift, u, j0 + warp * kOwn + lane) : -1;
                 const bool on = at >= 0;
                 const uint32_t mine = on ? (uint32_t)(at >> 4) : 0u;
                 const unsigned seen = __ballot_sync(0xffffffffu, on);
@@ -333,7 +366,7 @@ template <typename T, int DP> struct Copier {
                 for (int kv = 0; kv < 2; ++kv, ++items) {
                     const int stage = items % Z::kStages;
                     if (!wait_for(&sh.kv_empty[stage], (items / Z::kStages & 1) ^ 1)) return false;
-                    copy_rows<kOwn, Z::kPanel>(kv_smem + stage * Z::kStage + warp * kOwn * 128,
+                    copy_rows<kOwn, Z::kPanel, kOwn / 4>(kv_smem + stage * Z::kStage + warp * kOwn * 128,
                                                (const T *)(kv ? p.v : p.k), mine, on, 16);
                     copy_commit();
                     if (kv == 0) {
@@ -341,6 +374,7 @@ template <typename T, int DP> struct Copier {
                             if (kOwn == 32) sh.visible[tiles % kRing][warp] = seen;
                             else reinterpret_cast<uint16_t *>(sh.visible[tiles % kRing])[warp] = (uint16_t)seen;
                         }
+                        __syncwarp();
                         arrive(&sh.kv_full[stage]);
                         look<1>();
                         if (t == t0 && !queries(u, no)) return false;
@@ -360,13 +394,13 @@ template <typename T, int DP> struct Copier {
     __device__ __forceinline__ bool queries(const Segment &u, int no) {
         const int lane = threadIdx.x % 32, warp = threadIdx.x / 32 - kCopyWarp;
         if (!wait_for(&sh.q_empty, (no & 1) ^ 1)) return false;
-#pragma unroll
+#pragma unroll 1
         for (int tile = 0; tile < Z::kTiles; ++tile) {
             if (tile * 128 >= u.rows) break;
             const int r = tile * 128 + warp * 32 + lane;
             const bool on = r < u.rows;
             const int64_t mine = on ? query_offset(p, u, r) : 0;
-            copy_rows<32, Z::kQPanel>(q_smem + tile * Z::kPanels * Z::kQPanel + warp * 32 * 128, (const T *)p.q,
+            copy_rows<32, Z::kQPanel, 2>(q_smem + tile * Z::kPanels * Z::kQPanel + warp * 32 * 128, (const T *)p.q,
                                       mine, on, 1);
         }
         arrive(&sh.q_full);
@@ -385,7 +419,8 @@ template <typename T, int DP> struct Multiplier {
     __device__ __forceinline__ void scores(int tile, int buffer, int stage) {
         const uint32_t idesc = ptx::idesc_f32acc(Half<T>::kFormat, 128, Z::kSlots);
         const uint32_t q = q_smem + tile * Z::kPanels * Z::kQPanel, k = kv_smem + stage * Z::kStage;
-        for (int i = 0; i < p.D / 16; ++i) {
+        const int steps = p.D / 16;
+        for (int i = 0; i < steps; ++i) {
             const uint64_t a = ptx::sdesc_k<128>(q + i / 4 * Z::kQPanel + i % 4 * 32);
             const uint64_t b = ptx::sdesc_k<128>(k + i / 4 * Z::kPanel + i % 4 * 32);
             if (ptx::elect_one()) ptx::mma_f16(tmem + Z::kS + buffer * Z::kSlots, a, b, idesc, i > 0);
@@ -519,11 +554,11 @@ template <typename T, int DP> struct Softmax {
         const bool early = p.scale_log2 <= 0.0f;
         const float scale = early ? 1.0f : p.scale_log2;
         int tiles = 0, o_count = 0, s_count[2] = {0, 0};    // s_count: own barrier, and [2]
-        int4 head = make_int4(0, 0, 0, 0);
         bool ok;
+        if (threadIdx.x == 0 && !p.whole) p.heads[blockIdx.x] = make_int4(0, 0, 0, 0);
         for (int no = 0;; ++no) {
             const Segment *const next = next_segment(sh, no, ok);
-            if (!next) break;
+            if (!next) return ok;
             const Segment &u = *next;
             const int n = u.t1 - u.t0, from = (u.first + u.t0) * kN;
             const bool dual = u.rows > 128;
@@ -543,9 +578,6 @@ template <typename T, int DP> struct Softmax {
                 if (!wait(sh, &sh.s_full[bar], parity)) return false;
                 ptx::tc_fence_after();
                 const uint32_t at = tmem + Z::kS + buffer * kN;
-                uint32_t s[kN / 32][32];
-#pragma unroll
-                for (int w = 0; w < kN / 32; ++w) ptx::tmem_ld_32x32b_x32(at + w * 32, s[w]);
                 uint32_t seen[kN / 32], all = ~0u;
 #pragma unroll
                 for (int w = 0; w < kN / 32; ++w) {
@@ -553,76 +585,88 @@ template <typename T, int DP> struct Softmax {
                     all &= seen[w];
                 }
                 const bool masked = is_edge(u, j0, kN) || all != ~0u;
-#pragma unroll
-                for (int w = 0; w < kN / 32; ++w) ptx::tmem_wait_ld_regs(s[w]);
-                if (early) {
-#pragma unroll
-                    for (int w = 0; w < kN / 32; ++w)
+                // Scores of 32 slots as the base compares them.
+                const auto prepare = [&](uint32_t (&s)[32], int w) {
+                    if (early) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            s[w][i] = __float_as_uint(__uint_as_float(s[w][i]) * p.scale_log2);
-                }
-                if (masked) {
-#pragma unroll
-                    for (int w = 0; w < kN / 32; ++w) {
+                            s[i] = __float_as_uint(__uint_as_float(s[i]) * p.scale_log2);
+                    }
+                    if (masked) {
                         const uint32_t bits = seen[w] & range_bits(j0 + w * 32, lo, hi);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            s[w][i] = bits >> i & 1 ? s[w][i] : 0xff800000u;
+                        for (int i = 0; i < 32; ++i) s[i] = bits >> i & 1 ? s[i] : 0xff800000u;
                     }
-                }
+                };
                 float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+                const auto raise_top = [&](const uint32_t (&s)[32]) {
 #pragma unroll
-                for (int w = 0; w < kN / 32; ++w)
+                    for (int i = 0; i < 32; i += 2)
+                        top[i / 2 % 4] = max3(top[i / 2 % 4], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+                };
+                uint32_t s[kN / 32][32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) top[i % 4] = fmaxf(top[i % 4], __uint_as_float(s[w][i]));
+                for (int w = 0; w < kN / 32; ++w) ptx::tmem_ld_32x32b_x32(at + w * 32, s[w]);
+#pragma unroll
+                for (int w = 0; w < kN / 32; ++w) {
+                    ptx::tmem_wait_ld_regs(s[w]);
+                    prepare(s[w], w);
+                    raise_top(s[w]);
+                }
                 // Rounded upwards: no power of two below exceeds what the base allows it.
                 const float m = __fmul_ru(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), scale);
                 const bool raise = m > base + H::kSlack;
-                const float factor = raise && base > kNegInf ? shrink_of(base, m) : 1.0f;
                 const bool again = raise && base > kNegInf;
+                const float factor = again ? shrink_of(base, m) : 1.0f;
                 if (raise) base = m;
+                const float sub = base == kNegInf ? 0.0f : __fsub_ru(base, H::kLift);
+                const uint64_t scale2 = pair(scale, scale), sub2 = pair(-sub, -sub);
+                uint64_t sum[2] = {0, 0};
+                const auto weigh = [&](const uint32_t (&s)[32], int w) {
+                    uint32_t out[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float a, b;
+                        unpair(fma2(pair(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), scale2, sub2),
+                               a, b);
+                        a = pow2(a);
+                        b = pow2(b);
+                        sum[i % 2] = add2(sum[i % 2], pair(a, b));
+                        out[i] = H::pack(a, b);
+                    }
+                    if (!masked) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) out[i] = H::hold_up(out[i]);
+                    }
+                    tmem_st16(at + w * 16, out);
+                };
+#pragma unroll
+                for (int w = 0; w < kN / 32; ++w) weigh(s[w], w);
                 if (t > 0 && __any_sync(0xffffffffu, again)) {
                     if (!wait(sh, &sh.o_full[tile], (o_count + t - 1) & 1)) return false;
                     ptx::tc_fence_after();
                     rescale(factor);
                 }
-                const float sub = base == kNegInf ? 0.0f : __fsub_ru(base, H::kLift);
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int w = 0; w < kN / 64; ++w) {
-                    uint32_t out[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float a = pow2(fmaf(__uint_as_float(s[2 * w + i / 16][i % 16 * 2]), scale, -sub));
-                        const float b = pow2(fmaf(__uint_as_float(s[2 * w + i / 16][i % 16 * 2 + 1]), scale, -sub));
-                        sum[i % 2 * 2] += a;
-                        sum[i % 2 * 2 + 1] += b;
-                        out[i] = H::pack(a, b);
-                    }
-                    if (!masked) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) out[i] = H::hold_up(out[i]);
-                    }
-                    ptx::tmem_st_32x32b_x32(at + w * 32, out);
-                }
-                l = l * factor + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+                float even, odd;
+                unpair(add2(sum[0], sum[1]), even, odd);
+                l = l * factor + (even + odd);
                 ptx::tmem_wait_st();
                 // The product before the last has to be over before the last can be: the wait behind the
                 // loop would take the one's end for the other's.
                 if (t == n - 1 && t > 0 && !wait(sh, &sh.o_full[tile], (o_count + t - 1) & 1)) return false;
                 ptx::tc_fence_before();
-                ptx::mbar_arrive(&sh.p_full[bar]);
+                __syncwarp();
+                if (threadIdx.x % 32 == 0) ptx::mbar_arrive(&sh.p_full[bar]);
+                __syncwarp();
             }
             o_count += n;
             if (!wait(sh, &sh.o_full[tile], (o_count - 1) & 1)) return false;
             ptx::tc_fence_after();
             output(u, r, mine, lo, hi, base, l);
-            if (u.part && u.begins) head = make_int4(u.b, u.hk, u.m, u.parts);
+            if (threadIdx.x == 0 && u.part && u.begins)
+                p.heads[blockIdx.x] = make_int4(u.b, u.hk, u.m, u.parts);
             segment_done(sh, no);
         }
-        if (threadIdx.x == 0 && !p.whole) p.heads[blockIdx.x] = head;
-        return ok;
     }
 
     __device__ __forceinline__ void output(const Segment &u, int r, bool mine, int lo, int hi, float base,
@@ -663,7 +707,7 @@ template <typename T, int DP> struct Softmax {
     }
 };
 
-template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__ ChunkParams p) {
+template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(ChunkParams p) {
     typedef Sizes<DP> Z;
     extern __shared__ unsigned char dynamic[];
     __shared__ Shared sh;
@@ -683,7 +727,7 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 1) tc_
         }
         for (int i = 0; i < 3; ++i) {
             ptx::mbar_init(&sh.s_full[i], 2);
-            ptx::mbar_init(&sh.p_full[i], 128);
+            ptx::mbar_init(&sh.p_full[i], 4);
         }
         ptx::mbar_init(&sh.o_full[0], 2);
         ptx::mbar_init(&sh.o_full[1], 2);
@@ -718,7 +762,7 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 1) tc_
         } else {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
             if (warp == kMmaWarp) {
-                Multiplier<T, DP> multiplier{p, sh, q_smem, kv_smem, tmem};
+                    Multiplier<T, DP> multiplier{p, sh, q_smem, kv_smem, tmem};
                 ok = multiplier.run();
             } else if (warp == kScheduleWarp) {
                 ok = schedule<Z::kRows, Z::kSlots>(p, sh, costs);
