@@ -25,6 +25,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "chunk_device.cuh"
 #include "chunk_join.cuh"
@@ -75,7 +76,7 @@ constexpr int kThreads = 512, kCopyWarp = 8, kMmaWarp = 12, kScheduleWarp = 13;
 constexpr int kRing = 8;                                        // tiles whose visible slots are kept
 constexpr int kSegments = 8;                                    // segments that the schedule is ahead
 constexpr uint64_t kWaitLimitNs = 2000000000;                   // of a block's waits for itself
-constexpr int kSoftmaxRegs = 192, kCopyRegs = 80, kMmaRegs = 48;  // 256 * 192 + 128 (80 + 48) = 512 * 128
+constexpr int kSoftmaxRegs = 192, kCopyRegs = 72, kMmaRegs = 56;  // 256 * 192 + 128 (72 + 56) = 512 * 128
 
 // What the roles know of a segment: the unit (as in Unit) and its tiles [t0, t1); none: the end.
 struct Segment {
@@ -172,26 +173,46 @@ template <int N> __device__ __forceinline__ void copy_wait() {
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// D (+)= A[tmem] * B[smem], B column-major if the descriptor and idesc say so.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-                 "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+// Products whose operands lie `kA` and `kB` sixteen-byte units behind descriptors that differ in their lower
+// words only (the upper one: eight rows of 128 bytes a group, 128-byte swizzle): the additions belong to the
+// product, where the compiler does not keep a descriptor for each in registers.
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+template <int kA, int kB>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 a, b;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "add.u32 x, %1, %6;\n\tadd.u32 y, %2, %7;\n\t"
+                 "mov.b64 a, {x, %5};\n\tmov.b64 b, {y, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+                 "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHigh), "n"(kA), "n"(kB)
                  : "memory");
 }
-// Operand [k][n] of 128-byte swizzled panels of 64 columns, `panel` bytes apart, whose rows are k: groups of
-// eight rows are 1024 bytes apart.
-__device__ __forceinline__ uint64_t sdesc_mn(uint32_t smem_addr, uint32_t panel) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
-    d |= static_cast<uint64_t>(panel >> 4) << 16;
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;
-    return d;
+// The first operand in TMEM.
+template <int kA, int kB>
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 b;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "add.u32 x, %1, %6;\n\tadd.u32 y, %2, %7;\n\t"
+                 "mov.b64 b, {y, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, p;\n\t}" ::"r"(d_tmem),
+                 "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHigh), "n"(kA), "n"(kB)
+                 : "memory");
+}
+// The lower word for rows of K-major panels, and for a [k][n] operand of panels of 64 columns, `panel` bytes
+// apart, whose rows are k.
+__device__ __forceinline__ uint32_t desc_k(uint32_t smem_addr) { return (smem_addr >> 4 & 0x3fff) | 1u << 16; }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t smem_addr, uint32_t panel) {
+    return (smem_addr >> 4 & 0x3fff) | panel >> 4 << 16;
 }
 constexpr uint32_t kTransposeB = 1u << 16;
+
+// f(0), f(1), ... with constants.
+template <int kN, int kI = 0, typename F> __device__ __forceinline__ void each(F &&f) {
+    if constexpr (kI < kN) {
+        f(std::integral_constant<int, kI>());
+        each<kN, kI + 1>(f);
+    }
+}
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -416,26 +437,30 @@ template <typename T, int DP> struct Multiplier {
     Shared &sh;
     uint32_t q_smem, kv_smem, tmem;
 
+    // (One elected lane issues a tile's products in a row, their descriptors a constant apart.)
     __device__ __forceinline__ void scores(int tile, int buffer, int stage) {
         const uint32_t idesc = ptx::idesc_f32acc(Half<T>::kFormat, 128, Z::kSlots);
-        const uint32_t q = q_smem + tile * Z::kPanels * Z::kQPanel, k = kv_smem + stage * Z::kStage;
-        const int steps = p.D / 16;
-        for (int i = 0; i < steps; ++i) {
-            const uint64_t a = ptx::sdesc_k<128>(q + i / 4 * Z::kQPanel + i % 4 * 32);
-            const uint64_t b = ptx::sdesc_k<128>(k + i / 4 * Z::kPanel + i % 4 * 32);
-            if (ptx::elect_one()) ptx::mma_f16(tmem + Z::kS + buffer * Z::kSlots, a, b, idesc, i > 0);
-        }
+        const uint32_t q = desc_k(q_smem + tile * Z::kPanels * Z::kQPanel), k = desc_k(kv_smem + stage * Z::kStage);
+        const uint32_t s = tmem + Z::kS + buffer * Z::kSlots;
+        const int D = p.D;
+        if (ptx::elect_one())
+            each<DP / 16>([&](auto step) {
+                constexpr int i = decltype(step)::value;
+                if (i * 16 < D)
+                    mma_ss<(i / 4 * Z::kQPanel + i % 4 * 32) / 16, (i / 4 * Z::kPanel + i % 4 * 32) / 16>(
+                        s, q, k, idesc, i > 0);
+            });
     }
     __device__ __forceinline__ void values(int tile, int buffer, int stage, bool first) {
         const uint32_t idesc = ptx::idesc_f32acc(Half<T>::kFormat, 128, p.D) | kTransposeB;
-        const uint32_t v = kv_smem + stage * Z::kStage;
-#pragma unroll
-        for (int i = 0; i < Z::kSlots / 16; ++i) {
-            const uint64_t b = sdesc_mn(v + i * 2048, Z::kPanel);
-            if (ptx::elect_one())
-                mma_f16_ts(tmem + Z::kO + tile * Z::kOPitch, tmem + Z::kS + buffer * Z::kSlots + i * 8, b, idesc,
-                           i > 0 || !first);
-        }
+        const uint32_t v = desc_mn(kv_smem + stage * Z::kStage, Z::kPanel);
+        const uint32_t o = tmem + Z::kO + tile * Z::kOPitch;
+        const uint32_t w = tmem + Z::kS + buffer * Z::kSlots;
+        if (ptx::elect_one())
+            each<Z::kSlots / 16>([&](auto step) {
+                constexpr int i = decltype(step)::value;
+                mma_ts<i * 8, i * 2048 / 16>(o, w, v, idesc, i > 0 || !first);
+            });
     }
     // The barrier's phase ends when the products issued so far do; the plain arrival orders what this
     // warp has seen before it for who waits there.
@@ -535,6 +560,13 @@ template <typename T, int DP> struct Softmax {
     uint32_t tmem;           // of this warp's lanes
     int tile;                // of rows: 0 or 1
 
+    // What this warp has stored to TMEM is there.
+    __device__ __forceinline__ void pass_on(uint64_t *bar) {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (threadIdx.x % 32 == 0) ptx::mbar_arrive(bar);
+        __syncwarp();
+    }
     // Multiplies this warp's rows of O.
     __device__ __forceinline__ void rescale(float factor) {
         const uint32_t o = tmem + Z::kO + tile * Z::kOPitch;
@@ -619,6 +651,12 @@ template <typename T, int DP> struct Softmax {
                 const bool again = raise && base > kNegInf;
                 const float factor = again ? shrink_of(base, m) : 1.0f;
                 if (raise) base = m;
+                // (Before the first of this tile's weights is passed on.)
+                if (t > 0 && __any_sync(0xffffffffu, again)) {
+                    if (!wait(sh, &sh.o_full[tile], (o_count + t - 1) & 1)) return false;
+                    ptx::tc_fence_after();
+                    rescale(factor);
+                }
                 const float sub = base == kNegInf ? 0.0f : __fsub_ru(base, H::kLift);
                 const uint64_t scale2 = pair(scale, scale), sub2 = pair(-sub, -sub);
                 uint64_t sum[2] = {0, 0};
@@ -642,11 +680,6 @@ template <typename T, int DP> struct Softmax {
                 };
 #pragma unroll
                 for (int w = 0; w < kN / 32; ++w) weigh(s[w], w);
-                if (t > 0 && __any_sync(0xffffffffu, again)) {
-                    if (!wait(sh, &sh.o_full[tile], (o_count + t - 1) & 1)) return false;
-                    ptx::tc_fence_after();
-                    rescale(factor);
-                }
                 float even, odd;
                 unpair(add2(sum[0], sum[1]), even, odd);
                 l = l * factor + (even + odd);
@@ -654,10 +687,7 @@ template <typename T, int DP> struct Softmax {
                 // The product before the last has to be over before the last can be: the wait behind the
                 // loop would take the one's end for the other's.
                 if (t == n - 1 && t > 0 && !wait(sh, &sh.o_full[tile], (o_count + t - 1) & 1)) return false;
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (threadIdx.x % 32 == 0) ptx::mbar_arrive(&sh.p_full[bar]);
-                __syncwarp();
+                pass_on(&sh.p_full[bar]);
             }
             o_count += n;
             if (!wait(sh, &sh.o_full[tile], (o_count - 1) & 1)) return false;
