@@ -31,7 +31,7 @@ template <int NC> __device__ __forceinline__ int column(int tx, int c) {
     return NC % 4 == 0 ? tx * 4 + c / 4 * 64 + c % 4 : tx + 16 * c;
 }
 
-template <int NC> __global__ void __launch_bounds__(kThreads) chunk_kernel(ChunkParams p) {
+template <int NC> __global__ void __launch_bounds__(kThreads, NC <= 8 ? 2 : 1) chunk_kernel(ChunkParams p) {
     constexpr int DP = 16 * NC;
     extern __shared__ __align__(16) float smem[];
     __shared__ int64_t costs[kMaxB + 1];
@@ -105,23 +105,32 @@ template <int NC> __global__ void __launch_bounds__(kThreads) chunk_kernel(Chunk
                 }
             }
             const bool masked = __syncthreads_or(hidden) || edge;
-            float s[4][4] = {};
+            float s[4][4];
+            uint64_t s2[4][4] = {};          // sums over even and over odd columns
             for (int d = 0; d < D; d += 4) {
-                float4 a[4], b[4];
+                ulonglong2 a[4], b[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<float4 *>(sq + (ty * 4 + i) * pitch + d);
+                for (int i = 0; i < 4; ++i)
+                    a[i] = *reinterpret_cast<ulonglong2 *>(sq + (ty * 4 + i) * pitch + d);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<float4 *>(sk + (tx + 16 * j) * pitch + d);
+                for (int j = 0; j < 4; ++j)
+                    b[j] = *reinterpret_cast<ulonglong2 *>(sk + (tx + 16 * j) * pitch + d);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
-                        s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
-                        s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
-                        s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+                        s2[i][j] = fma2(a[i].x, b[j].x, s2[i][j]);
+                        s2[i][j] = fma2(a[i].y, b[j].y, s2[i][j]);
                     }
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float even, odd;
+                    unpair(s2[i][j], even, odd);
+                    s[i][j] = even + odd;
+                }
             float shrink[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -178,8 +187,16 @@ template <int NC> __global__ void __launch_bounds__(kThreads) chunk_kernel(Chunk
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float x = e == 0 ? a[i].x : e == 1 ? a[i].y : e == 2 ? a[i].z : a[i].w;
+                        if (NC % 2 == 0) {
+                            const uint64_t x2 = pair(x, x);
 #pragma unroll
-                        for (int c = 0; c < NC; ++c) o[i][c] = fmaf(x, b[c], o[i][c]);
+                            for (int c = 0; c + 1 < NC; c += 2)
+                                unpair(fma2(x2, pair(b[c], b[c + 1]), pair(o[i][c], o[i][c + 1])), o[i][c],
+                                       o[i][c + 1]);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < NC; ++c) o[i][c] = fmaf(x, b[c], o[i][c]);
+                        }
                     }
                 }
             }

@@ -34,7 +34,7 @@ struct ctr_rope_s {
 namespace ctr {
 namespace {
 
-constexpr int kThreads = 256, kMaxPairs = 256;
+constexpr int kThreads = 256, kMaxPairs = 256, kItems = 2;
 
 struct RopeParams {
     const void *q, *k, *v;
@@ -68,8 +68,8 @@ template <typename T, int N> struct __align__(sizeof(T) * N) Pack {
 
 // A block has p.tokens tokens and one in p.parts of their heads (of q, then k, then v).  An item is
 // one unit of a head: N columns and, where pairs are that far apart, their N partners.  N is one
-// 16-byte access, or 1 where strides, addresses or R allow no more.  Items are taken two at a
-// time, loads before stores, so that a thread has up to four accesses in flight.
+// 16-byte access, or 1 where strides, addresses or R allow no more.  Items are taken kItems at
+// a time, loads before stores, so that a thread has up to four accesses in flight.
 template <typename T, int N> __global__ void __launch_bounds__(kThreads) rope_kernel(RopeParams p) {
     extern __shared__ __align__(16) float2 table[];    // [tokens][R / 2] cosine and sine
     typedef Pack<T, N> P;
@@ -88,18 +88,23 @@ template <typename T, int N> __global__ void __launch_bounds__(kThreads) rope_ke
     __syncthreads();
     const bool apart = p.half || N == 1;               // partners in a pack of their own
     const int partner = p.half ? pairs : 1, turned = apart ? pairs / N : p.R / N;
-    const int units = turned + (p.D - p.R) / N, items = here * own * units;
-    for (int x0 = threadIdx.x; x0 < items; x0 += 2 * kThreads) {
-        P a[2], b[2];
-        T *to[2];
-        int angle[2];                                  // the unit's place in the table, or -1
-        bool on[2], two[2];
+    const int units = turned + (p.D - p.R) / N, rows = here * own;
+    // A thread keeps its unit and goes through the block's rows (a head of a token each).
+    const int span = min(units, kThreads), step = kThreads / span, mine = threadIdx.x / span;
+    if (mine >= step) return;
+    for (int u = threadIdx.x % span; u < units; u += span)
+    for (int y0 = mine, h_at = mine, t_at = 0; y0 < rows; y0 += kItems * step) {
+        P a[kItems], b[kItems];
+        T *to[kItems];
+        int angle[kItems];                             // the unit's place in the table, or -1
+        bool on[kItems], two[kItems];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int x = x0 + e * kThreads, u = x % units, row = x / units / own;
-            int h = h0 + x / units % own;
+        for (int e = 0; e < kItems; ++e, h_at += step) {
+            for (; h_at >= own; h_at -= own) ++t_at;
+            int h = h0 + h_at;
+            const int row = t_at;
             const int64_t t = t0 + row;
-            on[e] = x < items;
+            on[e] = y0 + e * step < rows;
             if (!on[e]) continue;
             const T *from;
             const bool is_v = h >= p.Hq + p.Hk;
@@ -116,8 +121,10 @@ template <typename T, int N> __global__ void __launch_bounds__(kThreads) rope_ke
                         if (slot >= 0) atomicOr(p.cache.status, kStatusBadPage);
                         continue;
                     }
-                    to[e] = (T *)(is_v ? p.v_pages : p.k_pages) + slot / p.cache.page * p.cache.page_stride +
-                            h * p.cache.head_stride + slot % p.cache.page * p.cache.row_stride;
+                    // (Most caches have fewer than 2^32 rows, whose division is short.)
+                    const int64_t pg = slot >> 32 ? slot / p.cache.page : (uint32_t)slot / (uint32_t)p.cache.page;
+                    to[e] = (T *)(is_v ? p.v_pages : p.k_pages) + pg * p.cache.page_stride +
+                            h * p.cache.head_stride + (slot - pg * p.cache.page) * p.cache.row_stride;
                 } else {
                     to[e] = (T *)p.k_out + t * p.ko_stride + (int64_t)h * p.D;
                 }
@@ -131,7 +138,7 @@ template <typename T, int N> __global__ void __launch_bounds__(kThreads) rope_ke
             if (two[e]) b[e] = *reinterpret_cast<const P *>(from + partner);
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < kItems; ++e) {
             if (!on[e]) continue;
             if (angle[e] >= 0) {
                 const float2 *cs = table + angle[e];

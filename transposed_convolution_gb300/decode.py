@@ -54,6 +54,16 @@ class _DecodePlan:
             raise ValueError("%s must be contiguous" % name)
         return t.data_ptr()
 
+    def _heads_at(self, t, name, T, heads, D, dtype):
+        """As _rows_at for rows of heads, [T, heads, D]: the address and row stride of what a fused
+        projection leaves, in few steps."""
+        if t.dim() == 3 and t.dtype is dtype and t.get_device() == self._index:
+            shape, stride = t.shape, t.stride()
+            if (shape[0] == T and shape[1] == heads and shape[2] == D and stride[2] == 1 and stride[1] == D
+                    and T > 1):
+                return t.data_ptr(), stride[0]
+        return self._rows_at(t, name, (T, heads, D), dtype)
+
     def _rows_at(self, t, name, shape, dtype):
         """The address and the row stride of a tensor whose rows (of all but the first dimension)
         are contiguous and lie at any distance."""
@@ -216,9 +226,8 @@ class PagedAttention(_DecodePlan):
         and dtype) turns K by positions [T] (int32) on the way, and q [T, H_q, D], which the call then
         returns turned (in q_out, which may be q).  k, v and q may be slices of a fused projection."""
         T = k.shape[0] if k.dim() else 0
-        shape = (T, self.H_kv, self.D)
-        k_ptr, kv_stride = self._rows_at(k, "k", shape, self.dtype)
-        v_ptr, v_stride = self._rows_at(v, "v", shape, self.dtype)
+        k_ptr, kv_stride = self._heads_at(k, "k", T, self.H_kv, self.D, self.dtype)
+        v_ptr, v_stride = self._heads_at(v, "v", T, self.H_kv, self.D, self.dtype)
         if v_stride != kv_stride:
             raise ValueError("k and v must have the same row stride")
         s_ptr = self._at(slots, "slots", (T,), torch.int64)
@@ -239,11 +248,11 @@ class PagedAttention(_DecodePlan):
             if rotary is None:
                 raise ValueError("q without a rotary plan")
             shape = (T, self.H_q, self.D)
-            q_ptr, q_stride = self._rows_at(q, "q", shape, self.dtype)
+            q_ptr, q_stride = self._heads_at(q, "q", T, self.H_q, self.D, self.dtype)
             if q_out is None:
                 q_out = torch.empty(shape, dtype=self.dtype, device=self.device)
                 made = (q_out,)
-            o_ptr, o_stride = self._rows_at(q_out, "q_out", shape, self.dtype)
+            o_ptr, o_stride = self._heads_at(q_out, "q_out", T, self.H_q, self.D, self.dtype)
             if not T:
                 q_ptr = o_ptr = None
         elif q_out is not None:
@@ -263,7 +272,7 @@ class PagedAttention(_DecodePlan):
         in a tensor that the call makes)."""
         T = q.shape[0] if q.dim() else 0
         shape = (T, self.H_q, self.D)
-        q_ptr, q_stride = self._rows_at(q, "q", shape, self.dtype)
+        q_ptr, q_stride = self._heads_at(q, "q", T, self.H_q, self.D, self.dtype)
         t_ptr = self._at(tables, "tables", self._table_shape, torch.int32)
         l_ptr = self._at(lens, "lens", self._lens_shape, torch.int32)
         s_ptr = self._at(starts, "starts", self._starts_shape, torch.int32)

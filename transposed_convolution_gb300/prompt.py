@@ -70,32 +70,41 @@ class Rotary(_DecodePlan):
         gradient's).  q_out may be q, and k_out k; all may be slices with any row stride."""
         T = positions.shape[0] if positions.dim() else 0
         p_ptr = self._at(positions, "positions", (T,), torch.int32)
-        args, made = [], []
-        for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
-            if x is None:
-                if out is not None:
-                    raise ValueError("%s_out without %s" % (name, name))
-                args.append((None, 0, 0, None, 0))
-                continue
-            if x.dim() != 3:
-                raise ValueError("%s must be [%d, heads, %d]" % (name, T, self.D))
-            shape = (T, x.shape[1], self.D)
-            x_ptr, x_stride = self._rows_at(x, name, shape, self.dtype)
-            if out is None:
-                out = torch.empty(shape, dtype=self.dtype, device=self.device)
-                made.append(out)
-                if name == "q":
-                    q_out = out
-                else:
-                    k_out = out
-            o_ptr, o_stride = self._rows_at(out, name + "_out", shape, self.dtype)
-            args.append((x_ptr, x_stride, shape[1], o_ptr, o_stride))
-        (qp, qs, hq, qo, qos), (kp, ks, hk, ko, kos) = args
-        st = self._forward(self.handle, qp, qs, hq, kp, ks, hk, p_ptr, T, qo, qos, ko, kos,
-                           self._stream(stream, *made))
+        made = ()
+        q_ptr = k_ptr = qo_ptr = ko_ptr = None
+        q_stride = k_stride = qo_stride = ko_stride = H_q = H_k = 0
+        if q is not None:
+            q_ptr, q_stride, H_q = self._rows_of(q, "q", T)
+            if q_out is None:
+                q_out = torch.empty((T, H_q, self.D), dtype=self.dtype, device=self.device)
+                made = (q_out,)
+                qo_ptr, qo_stride = q_out.data_ptr(), H_q * self.D
+            else:
+                qo_ptr, qo_stride = self._heads_at(q_out, "q_out", T, H_q, self.D, self.dtype)
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        if k is not None:
+            k_ptr, k_stride, H_k = self._rows_of(k, "k", T)
+            if k_out is None:
+                k_out = torch.empty((T, H_k, self.D), dtype=self.dtype, device=self.device)
+                made += (k_out,)
+                ko_ptr, ko_stride = k_out.data_ptr(), H_k * self.D
+            else:
+                ko_ptr, ko_stride = self._heads_at(k_out, "k_out", T, H_k, self.D, self.dtype)
+        elif k_out is not None:
+            raise ValueError("k_out without k")
+        st = self._forward(self.handle, q_ptr, q_stride, H_q, k_ptr, k_stride, H_k, p_ptr, T, qo_ptr,
+                           qo_stride, ko_ptr, ko_stride, self._stream(stream, *made))
         if st:
             raise _ctr.CtrError(st, "ctr_rope_forward")
         return q_out, k_out
+
+    def _rows_of(self, x, name, T):
+        if x.dim() != 3:
+            raise ValueError("%s must be [%d, heads, %d]" % (name, T, self.D))
+        heads = x.shape[1]
+        ptr, stride = self._heads_at(x, name, T, heads, self.D, self.dtype)
+        return ptr, stride, heads
 
     def describe(self) -> str:
         return _ctr.ctr_rope_describe(self.handle)
