@@ -160,6 +160,7 @@ class PagePool(_DecodePlan):
         if t is None:
             t = torch.empty(shape, dtype=dtype, device=self.device)
             made.append(t)
+            return t, t.data_ptr()
         return t, self._at(t, name, shape, dtype)
 
     def reserve(self, tables, lens, counts, rows, granted=None, starts=None, slots=None,
