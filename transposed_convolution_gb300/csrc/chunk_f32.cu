@@ -227,10 +227,11 @@ template <int NC> __global__ void __launch_bounds__(kThreads, NC <= 8 ? 2 : 1) c
             for (int i = 0; i < 4; ++i) {
                 if (ty * 4 + i >= u.rows) continue;
                 float *to = (float *)p.out + output_offset(p, u, ty * 4 + i);
+                // (A row without weight is 0 whatever V holds: 0 times an infinity would be NaN.)
                 const float inv = l[i] == 0.0f ? 0.0f : 1.0f / l[i];
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
-                    if (column<NC>(tx, c) < D) to[column<NC>(tx, c)] = o[i][c] * inv;
+                    if (column<NC>(tx, c) < D) to[column<NC>(tx, c)] = l[i] == 0.0f ? 0.0f : o[i][c] * inv;
             }
         }
     }
