@@ -242,6 +242,9 @@ class PagedAttention(_DecodePlan):
                                  % (rotary.D, rotary.dtype, self.D, self.dtype))
             p_ptr = self._at(positions, "positions", (T,), torch.int32)
             r_ptr = rotary.handle
+            if not r_ptr:
+                # (The C call takes no plan for no rotation.)
+                raise ValueError("the rotary plan is closed")
         elif positions is not None:
             raise ValueError("positions without a rotary plan")
         if q is not None:
