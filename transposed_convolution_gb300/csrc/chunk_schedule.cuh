@@ -34,7 +34,8 @@ __device__ __forceinline__ Sequence sequence_of(const ChunkParams &p, int b, boo
         if (report && blockIdx.x == 0) atomicOr(p.cache.status, kStatusBadLength);
         s.row0 = s.n = 0;
     }
-    if (s.len > p.cache.cap - s.n) {
+    // (An idle sequence asks for no slots, whatever its rows.)
+    if (s.len >= 0 && s.len > p.cache.cap - s.n) {
         if (report && blockIdx.x == 0) atomicOr(p.cache.status, kStatusBadLength);
         s.len = min(s.len, p.cache.cap);
     }
