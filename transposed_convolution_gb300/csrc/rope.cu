@@ -176,9 +176,11 @@ void set_turns(const ctr_rope_s *pl, RopeParams *p) {
     double f[kMaxPairs];
     frequencies(pl, f);
     for (int64_t i = 0; i < pl->R / 2; ++i) {
-        double x = f[i] / 6.283185307179586476925;
-        x -= std::floor(x);
-        p->turns[i] = x < 1.0 ? (uint64_t)(x * 18446744073709551616.0) : 0;
+        // (The fraction of the absolute value is exact; that of a small negative one, close to 1, would not be.)
+        const double x = std::fabs(f[i] / 6.283185307179586476925);
+        const double part = x - std::floor(x);             // (NaN where a tiny factor makes f infinite)
+        const uint64_t turn = part < 1.0 ? (uint64_t)(part * 18446744073709551616.0) : 0;
+        p->turns[i] = f[i] < 0.0 ? 0 - turn : turn;
     }
     p->magnitude = pl->magnitude;
     p->R = (int)pl->R;
