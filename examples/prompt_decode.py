@@ -4,7 +4,8 @@ B streams of different lengths: ``PagePool.reserve`` takes pages for the new tok
 says where each goes; ``PagedAttention.put`` turns the keys by their positions (``Rotary``) on
 their way there, and the queries beside them; ``PagedAttention.forward_chunk`` attends, prompts of any lengths
 at once, and ``PagedAttention.forward`` does for one token a stream.  A step may be taken back
-(``PagePool.release``), as drafted codes are that turn out wrong.  The weights are random: the example shows
+(``PagePool.release``), as drafted codes are that turn out wrong.  Streams that the pool refuses, or that are
+idle, stay as they are beside the others (``rows_as_asked``).  The weights are random: the example shows
 the calls, not a model.
 
     python examples/prompt_decode.py
@@ -19,6 +20,20 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import torch  # noqa: E402
 
 import transposed_convolution_gb300 as ctr  # noqa: E402
+
+
+def rows_as_asked(counts, granted, first, slots, positions):
+    """Starts [B + 1], slots and positions of rows that lie as ``counts`` asked for them, from what
+    ``PagePool.reserve`` says of the rows that it granted, which follow one another without those that it
+    refused.  Refused rows get slot -1 and position 0.  On the GPU, as only it knows who was refused."""
+    T = len(slots)
+    ends = counts.clamp(min=0).cumsum(0).clamp(max=T)
+    starts = torch.cat([torch.zeros_like(ends[:1]), ends])
+    row = torch.arange(T, device=slots.device)
+    stream = torch.searchsorted(ends, row, right=True).clamp(max=len(counts) - 1)
+    has = (granted[stream] > 0) & (row < ends[-1])
+    at = (first[stream] + row - starts[stream]).clamp(0, max(T - 1, 0))
+    return starts.to(torch.int32), torch.where(has, slots[at], -1), torch.where(has, positions[at], 0)
 
 
 class PromptDecoder:
@@ -45,6 +60,7 @@ class PromptDecoder:
         self.pool = ctr.PagePool(B, page, pages, num_pages)
         self.tables = torch.full((B, pages), -1, dtype=torch.int32, device="cuda")
         self.lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+        self.granted = None                 # of the last call
 
     def qkv(self, codes):
         x = self.embed[codes]
@@ -56,25 +72,28 @@ class PromptDecoder:
 
     def extend(self, codes, counts):
         """codes [T] (int64), of which each stream has the next ``counts`` [B] (int32), to the logits
-        [T, vocab] after each of them, and the counts that were granted.  (The pool serves the streams in
-        order; rows follow the granted counts, so a caller whose request was refused, other than the last
-        ones, sends the others again.)"""
-        granted, starts, slots, positions, lens = self.pool.reserve(self.tables, self.lens, counts,
-                                                                    len(codes))
+        [T, vocab] after each of them, and the counts that were granted: all of a stream's, or 0 where the pool
+        has no room or the stream is idle.  A refused stream is as it was; its rows are codes that saw nothing."""
+        T = len(codes)
+        granted, first, slots, positions, lens = self.pool.reserve(self.tables, self.lens, counts, T)
+        starts, slots, positions = rows_as_asked(counts, granted, first, slots, positions)
         x, q, k, v = self.qkv(codes)
         q = self.attention.put(k, v, slots, q=q, positions=positions, rotary=self.rotary)
-        seen = self.attention.forward_chunk(q, self.tables, self.lens, starts)
-        self.lens = lens
+        seen = self.attention.forward_chunk(q, self.tables, torch.where(granted == counts, self.lens, -1),
+                                            starts)
+        self.lens, self.granted = lens, granted
         return self.logits(x, seen), granted
 
     def step(self, codes):
-        """codes [B], one more for each stream, to the logits [B, vocab], by the decode step's attention."""
+        """codes [B], one more for each stream, to the logits [B, vocab], by the decode step's attention.
+        ``granted`` [B] then says 0 for a stream that is idle or was refused, as ``extend`` does."""
         ones = torch.ones_like(self.lens)
-        _, _, slots, positions, lens = self.pool.reserve(self.tables, self.lens, ones, self.B)
+        granted, first, slots, positions, lens = self.pool.reserve(self.tables, self.lens, ones, self.B)
+        _, slots, positions = rows_as_asked(ones, granted, first, slots, positions)
         x, q, k, v = self.qkv(codes)
         q = self.attention.put(k, v, slots, q=q, positions=positions, rotary=self.rotary)
-        seen = self.attention.forward(q, self.tables, lens)
-        self.lens = lens
+        seen = self.attention.forward(q, self.tables, torch.where(granted > 0, lens, -1))
+        self.lens, self.granted = lens, granted
         return self.logits(x, seen)
 
     def take_back(self, counts):

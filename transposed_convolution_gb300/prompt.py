@@ -169,7 +169,11 @@ class PagePool(_DecodePlan):
         tables [B, max_pages].  Returns (granted [B], the counts, or 0 for requests that do not fit
         behind the earlier ones; starts [B + 1], each sequence's first row; slots [rows] int64 and
         positions [rows], of the new tokens, -1 and 0 behind the last; lens_out [B], the lengths with
-        them).  All int32 but the slots; lens is not changed, and lens[b] < 0 marks an idle one."""
+        them).  All int32 but the slots; lens is not changed, and lens[b] < 0 marks an idle one.
+
+        The rows are those of the granted requests, one after the other: where one is refused, those behind it
+        come earlier than in rows laid out by ``counts``, and the caller brings the two together (as
+        ``rows_as_asked`` in examples/prompt_decode.py does, on the GPU) before ``put``."""
         rows, made = int(rows), []
         t_ptr = self._at(tables, "tables", self._table_shape, torch.int32)
         l_ptr = self._at(lens, "lens", self._row_shape, torch.int32)
