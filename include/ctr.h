@@ -582,6 +582,9 @@ ctr_status ctr_attn_set_weights(ctr_attn_t plan, int enable);
 /* Allow ctr_attn_forward_chunk (default 0): the workspace then also holds its partial results.
  * Unbinds the workspace. */
 ctr_status ctr_attn_set_chunks(ctr_attn_t plan, int enable);
+/* Limit, in nanoseconds, of the waits of a 16-bit chunk's kernel for its own copies and products (default
+ * 1e10).  A test hook, as ctr_plan_set_wait_limit_ns: any other limit runs a kernel that polls, and is slower. */
+ctr_status ctr_attn_set_wait_limit_ns(ctr_attn_t plan, uint64_t limit_ns);
 size_t ctr_attn_workspace_bytes(ctr_attn_t plan);
 /* Bind a caller-owned workspace (256-byte aligned), as ctr_plan_bind_workspace. */
 ctr_status ctr_attn_bind_workspace(ctr_attn_t plan, void *dev_ptr, size_t bytes);

@@ -29,10 +29,10 @@ Decode step of the model that writes a codec's frames (same names as the C ABI):
 ``ctr_sampler_forward``, ``ctr_sampler_describe``, ``ctr_sampler_destroy``.
 
 Chunks of new tokens (prompts, drafted tokens) on the same cache: ``ctr_attn_set_chunks``,
-``ctr_attn_forward_chunk``, ``ctr_attn_put``, ``ctr_rope_create``, ``ctr_rope_set_layout``,
-``ctr_rope_set_base``, ``ctr_rope_set_scaling``, ``ctr_rope_set_magnitude``, ``ctr_rope_set_frequencies``,
-``ctr_rope_frequencies``, ``ctr_rope_forward``, ``ctr_rope_describe``, ``ctr_rope_destroy``,
-``ctr_pages_create``, ``ctr_pages_bind_list``, ``ctr_pages_workspace_bytes``,
+``ctr_attn_set_wait_limit_ns``, ``ctr_attn_forward_chunk``, ``ctr_attn_put``, ``ctr_rope_create``,
+``ctr_rope_set_layout``, ``ctr_rope_set_base``, ``ctr_rope_set_scaling``, ``ctr_rope_set_magnitude``,
+``ctr_rope_set_frequencies``, ``ctr_rope_frequencies``, ``ctr_rope_forward``, ``ctr_rope_describe``,
+``ctr_rope_destroy``, ``ctr_pages_create``, ``ctr_pages_bind_list``, ``ctr_pages_workspace_bytes``,
 ``ctr_pages_bind_workspace``, ``ctr_pages_reset``, ``ctr_pages_reserve``, ``ctr_pages_release``,
 ``ctr_pages_check``, ``ctr_pages_describe``, ``ctr_pages_destroy``.
 
@@ -151,6 +151,7 @@ SIGNATURES = {
     "ctr_attn_describe": (ctypes.c_int, [_vp, ctypes.c_char_p, ctypes.c_size_t]),
     "ctr_attn_destroy": (None, [_vp]),
     "ctr_attn_set_chunks": (ctypes.c_int, [_vp, ctypes.c_int]),
+    "ctr_attn_set_wait_limit_ns": (ctypes.c_int, [_vp, ctypes.c_uint64]),
     "ctr_attn_forward_chunk": (ctypes.c_int, [_vp, _vp, ctypes.c_int64, ctypes.c_int64, _vp, _vp, _vp, _vp,
                                               _vp]),
     "ctr_attn_put": (ctypes.c_int, [_vp, _vp, _vp, ctypes.c_int64, _vp, _vp, ctypes.c_int64, _vp, _vp,
@@ -447,6 +448,10 @@ def ctr_attn_set_weights(plan, enable):
 
 def ctr_attn_set_chunks(plan, enable):
     _check(lib.ctr_attn_set_chunks(plan, int(enable)), "ctr_attn_set_chunks")
+
+
+def ctr_attn_set_wait_limit_ns(plan, limit_ns):
+    _check(lib.ctr_attn_set_wait_limit_ns(plan, int(limit_ns)), "ctr_attn_set_wait_limit_ns")
 
 
 def ctr_attn_workspace_bytes(plan) -> int:

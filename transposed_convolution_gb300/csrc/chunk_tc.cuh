@@ -81,8 +81,6 @@ template <int DP> struct Sizes {
 constexpr int kThreads = 512, kCopyWarp = 8, kMmaWarp = 12, kScheduleWarp = 13;
 constexpr int kRing = 8;                                        // tiles whose visible slots are kept
 constexpr int kSegments = 8;                                    // segments that the schedule is ahead
-constexpr uint64_t kWaitLimitNs = 10000000000;                  // of a block's waits for itself (a unit of
-                                                                // 2^28 slots takes 6 s)
 constexpr int kSoftmaxRegs = 192, kCopyRegs = 72, kMmaRegs = 56;  // 256 * 192 + 128 (72 + 56) = 512 * 128
 
 // What the roles know of a segment: the unit (as in Unit) and its tiles [t0, t1); none: the end.
@@ -94,7 +92,7 @@ struct Segment {
     int taint;               // values that are no numbers were taken out of V
 };
 
-struct Shared {
+template <bool kPolled> struct Shared {
     // Whoever waits at a barrier waits for each of its phases in turn, or knows by what it has seen
     // that the earlier ones are over: a wait tells only odd phases from even ones.  So where one tile of
     // rows uses both S buffers, the second has barriers of its own ([2]).
@@ -104,42 +102,58 @@ struct Shared {
     uint32_t visible[kRing][4];
     uint32_t tmem;
     volatile int abort;
+    uint64_t copied;
 };
 
 // Bounded; every lane asks, and the answer is a vote: behind a branch the compiler takes the warp for
 // divided, and its products and TMEM accesses for many (which took twice the time).
-__device__ __forceinline__ bool tested(uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity));
+// try_wait sleeps for longer than any healthy wait takes, so that another limit than the default is kept by asking
+// test_wait instead: by a kernel of its own (kPolled), because a choice at every wait took 5 to 12% of the time and
+// a limit that is no constant 2.
+template <bool kPolled>
+__device__ __forceinline__ bool tested(const ChunkParams &p, Shared<kPolled> &sh, uint64_t *bar, uint32_t parity) {
+    if constexpr (kPolled) {
+        const uint64_t start = ptx::globaltimer_ns();
+        bool there;
+        while (!(there = ptx::mbar_test_wait(bar, parity)) && !sh.abort &&
+               ptx::globaltimer_ns() - start < p.wait_limit_ns) {
+        }
+        return __all_sync(0xffffffffu, there);
+    } else {
+        return __all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity));
+    }
 }
-__device__ __forceinline__ bool wait(Shared &sh, uint64_t *bar, uint32_t parity) {
-    if (tested(bar, parity)) return true;
-    return ptx::mbar_wait_warp(bar, parity, kWaitLimitNs, &sh.abort);
+template <bool kPolled>
+__device__ __forceinline__ bool wait(const ChunkParams &p, Shared<kPolled> &sh, uint64_t *bar, uint32_t parity) {
+    if (tested(p, sh, bar, parity)) return true;
+    return !kPolled && ptx::mbar_wait_warp(bar, parity, kChunkWaitLimitNs, &sh.abort);
 }
-__device__ __forceinline__ void give_up(Shared &sh, const ChunkParams &p) {
+template <bool kPolled> __device__ __forceinline__ void give_up(Shared<kPolled> &sh, const ChunkParams &p) {
     sh.abort = 1;
     if (threadIdx.x % 32 == 0) atomicOr(p.cache.status, kStatusTimeout);
 }
 
 // The next segment's description, or null at the end (ok stays) or when a wait fails; and done with one.
-__device__ __forceinline__ Segment *next_segment(Shared &sh, int no, bool &ok) {
-    ok = wait(sh, &sh.segment_full[no % kSegments], no / kSegments & 1);
+template <bool kPolled>
+__device__ __forceinline__ Segment *next_segment(const ChunkParams &p, Shared<kPolled> &sh, int no, bool &ok) {
+    ok = wait(p, sh, &sh.segment_full[no % kSegments], no / kSegments & 1);
     Segment *s = &sh.segments[no % kSegments];
     return ok && s->t1 > s->t0 ? s : nullptr;
 }
-__device__ __forceinline__ void segment_done(Shared &sh, int no) {
+template <bool kPolled> __device__ __forceinline__ void segment_done(Shared<kPolled> &sh, int no) {
     __syncwarp();
     if (threadIdx.x % 32 == 0) ptx::mbar_arrive(&sh.segment_empty[no % kSegments]);
     __syncwarp();
 }
 
 // Describes the block's segments, ahead of the roles that work on them.
-template <int MT, int NT>
-__device__ __forceinline__ bool schedule(const ChunkParams &p, Shared &sh, const int64_t *costs) {
+template <int MT, int NT, bool kPolled>
+__device__ __forceinline__ bool schedule(const ChunkParams &p, Shared<kPolled> &sh, const int64_t *costs) {
     Walk<MT, NT> walk;
     walk.start(p, find_start<MT, NT>(p, costs));
     for (int no = 0;; ++no) {
         const bool more = walk.next(p);
-        if (!wait(sh, &sh.segment_empty[no % kSegments], (no / kSegments & 1) ^ 1)) return false;
+        if (!wait(p, sh, &sh.segment_empty[no % kSegments], (no / kSegments & 1) ^ 1)) return false;
         if (threadIdx.x % 32 == 0) {
             const Unit<MT, NT> &u = walk.u;
             Segment &s = sh.segments[no % kSegments];
@@ -298,10 +312,10 @@ template <typename T, int DP> __device__ __noinline__ bool take_out(uint32_t sta
 // ------------------------------------------------------------------------------------------------
 // Copies.  Each of the four warps has a quarter of a tile's slots: a lane looks one up, then eight
 // lanes copy 128 bytes of one.
-template <typename T, int DP> struct Copier {
+template <typename T, int DP, bool kPolled> struct Copier {
     typedef Sizes<DP> Z;
     const ChunkParams &p;
-    Shared &sh;
+    Shared<kPolled> &sh;
     uint32_t q_smem, kv_smem;
     int items;
     int looked;              // the stage of a V tile that is still to be looked through, or -1,
@@ -328,9 +342,9 @@ template <typename T, int DP> struct Copier {
     }
     // Waits for a phase; whoever completes it may be waiting for the tile that is to be looked through.
     __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity) {
-        if (tested(bar, parity)) return true;
+        if (tested(p, sh, bar, parity)) return true;
         look<0>();
-        return wait(sh, bar, parity);
+        return wait(p, sh, bar, parity);
     }
 
     // kRows rows of a warp, panels of 128 bytes: lane l's row is at `from` + `mine` elements, if there is one.
@@ -363,7 +377,7 @@ template <typename T, int DP> struct Copier {
         looked = -1;
         left = false;
         for (int no = 0;; ++no) {
-            const Segment *const next = next_segment(sh, no, ok);
+            const Segment *const next = next_segment(p, sh, no, ok);
             if (!next) {
                 look<0>();
                 return ok;
@@ -426,10 +440,10 @@ template <typename T, int DP> struct Copier {
 
 // ------------------------------------------------------------------------------------------------
 // Products.
-template <typename T, int DP> struct Multiplier {
+template <typename T, int DP, bool kPolled> struct Multiplier {
     typedef Sizes<DP> Z;
     const ChunkParams &p;
-    Shared &sh;
+    Shared<kPolled> &sh;
     uint32_t q_smem, kv_smem, tmem;
 
     // (One elected lane issues a tile's products in a row, their descriptors a constant apart.)
@@ -470,7 +484,7 @@ template <typename T, int DP> struct Multiplier {
     }
     // Waits for copies, whose writes the products then see.
     __device__ __forceinline__ bool arrived(uint64_t *bar, uint32_t parity) {
-        const bool ok = wait(sh, bar, parity);
+        const bool ok = wait(p, sh, bar, parity);
         fence_async();
         return ok;
     }
@@ -482,7 +496,7 @@ template <typename T, int DP> struct Multiplier {
         int items = 0, p_count[3] = {0, 0, 0};
         bool ok;
         for (int no = 0;; ++no) {
-            const Segment *const u = next_segment(sh, no, ok);
+            const Segment *const u = next_segment(p, sh, no, ok);
             if (!u) return ok;
             const int n = u->t1 - u->t0;
             const bool dual = u->rows > 128;
@@ -501,7 +515,7 @@ template <typename T, int DP> struct Multiplier {
                 const int v = (items + 1) % Z::kStages, k = (items + 2) % Z::kStages;
                 const bool more = t + 1 < n;
                 if (dual) {
-                    if (!arrived(items + 1) || !wait(sh, &sh.p_full[0], p_count[0]++ & 1)) return false;
+                    if (!arrived(items + 1) || !wait(p, sh, &sh.p_full[0], p_count[0]++ & 1)) return false;
                     ptx::tc_fence_after();
                     values(0, 0, v, t == 0);
                     commit(&sh.o_full[0]);
@@ -511,7 +525,7 @@ template <typename T, int DP> struct Multiplier {
                         scores(0, 0, k);
                         commit(&sh.s_full[0]);
                     }
-                    if (!wait(sh, &sh.p_full[1], p_count[1]++ & 1)) return false;
+                    if (!wait(p, sh, &sh.p_full[1], p_count[1]++ & 1)) return false;
                     ptx::tc_fence_after();
                     values(1, 1, v, t == 0);
                     commit(&sh.o_full[1]);
@@ -533,7 +547,7 @@ template <typename T, int DP> struct Multiplier {
                         if (t + 2 == n) release(&sh.q_empty);
                     }
                     const uint32_t parity = (now ? p_count[2]++ : p_count[0]++) & 1;
-                    if (!arrived(items + 1) || !wait(sh, &sh.p_full[now ? 2 : 0], parity)) return false;
+                    if (!arrived(items + 1) || !wait(p, sh, &sh.p_full[now ? 2 : 0], parity)) return false;
                     ptx::tc_fence_after();
                     values(0, now, v, t == 0);
                     commit(&sh.o_full[0]);
@@ -546,12 +560,12 @@ template <typename T, int DP> struct Multiplier {
 
 // ------------------------------------------------------------------------------------------------
 // Softmax of one tile of rows, and its output.
-template <typename T, int DP> struct Softmax {
+template <typename T, int DP, bool kPolled> struct Softmax {
     typedef Sizes<DP> Z;
     typedef Half<T> H;
     static constexpr int kN = Z::kSlots;
     const ChunkParams &p;
-    Shared &sh;
+    Shared<kPolled> &sh;
     uint32_t tmem;           // of this warp's lanes
     int tile;                // of rows: 0 or 1
 
@@ -584,7 +598,7 @@ template <typename T, int DP> struct Softmax {
         bool ok;
         if (threadIdx.x == 0 && !p.whole) p.heads[blockIdx.x] = make_int4(0, 0, 0, 0);
         for (int no = 0;; ++no) {
-            const Segment *const next = next_segment(sh, no, ok);
+            const Segment *const next = next_segment(p, sh, no, ok);
             if (!next) return ok;
             const Segment &u = *next;
             const int n = u.t1 - u.t0, from = (u.first + u.t0) * kN;
@@ -602,7 +616,7 @@ template <typename T, int DP> struct Softmax {
                 const int buffer = dual ? tile : t & 1, bar = second ? 2 : tile;
                 const int j0 = from + t * kN;
                 const uint32_t parity = (second ? s_count[1]++ : s_count[0]++) & 1;
-                if (!wait(sh, &sh.s_full[bar], parity)) return false;
+                if (!wait(p, sh, &sh.s_full[bar], parity)) return false;
                 ptx::tc_fence_after();
                 const uint32_t at = tmem + Z::kS + buffer * kN;
                 uint32_t seen[kN / 32], all = ~0u;
@@ -648,7 +662,7 @@ template <typename T, int DP> struct Softmax {
                 if (raise) base = m;
                 // (Before the first of this tile's weights is passed on.)
                 if (t > 0 && __any_sync(0xffffffffu, again)) {
-                    if (!wait(sh, &sh.o_full[tile], (o_count + t - 1) & 1)) return false;
+                    if (!wait(p, sh, &sh.o_full[tile], (o_count + t - 1) & 1)) return false;
                     ptx::tc_fence_after();
                     rescale(factor);
                 }
@@ -681,11 +695,11 @@ template <typename T, int DP> struct Softmax {
                 ptx::tmem_wait_st();
                 // The product before the last has to be over before the last can be: the wait behind the
                 // loop would take the one's end for the other's.
-                if (t == n - 1 && t > 0 && !wait(sh, &sh.o_full[tile], (o_count + t - 1) & 1)) return false;
+                if (t == n - 1 && t > 0 && !wait(p, sh, &sh.o_full[tile], (o_count + t - 1) & 1)) return false;
                 pass_on(&sh.p_full[bar]);
             }
             o_count += n;
-            if (!wait(sh, &sh.o_full[tile], (o_count - 1) & 1)) return false;
+            if (!wait(p, sh, &sh.o_full[tile], (o_count - 1) & 1)) return false;
             ptx::tc_fence_after();
             output(u, r, mine, lo, hi, base, l);
             if (threadIdx.x == 0 && u.part && u.begins)
@@ -732,10 +746,10 @@ template <typename T, int DP> struct Softmax {
     }
 };
 
-template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(ChunkParams p) {
+template <typename T, int DP, bool kPolled> __global__ void __launch_bounds__(kThreads, 1) tc_kernel(ChunkParams p) {
     typedef Sizes<DP> Z;
     extern __shared__ unsigned char dynamic[];
-    __shared__ Shared sh;
+    __shared__ Shared<kPolled> sh;
     const uint32_t raw = ptx::smem_u32(dynamic), smem = (raw + 1023) & ~1023u;
     const int warp = threadIdx.x / 32;
     if (threadIdx.x == 0) {
@@ -746,6 +760,7 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 1) tc_
         ptx::mbar_init(&sh.q_full, 128);
         ptx::mbar_init(&sh.q_empty, 1);
         ptx::mbar_init(&sh.drained, 1);
+        ptx::mbar_init(&sh.copied, 128);
         for (int i = 0; i < kSegments; ++i) {
             ptx::mbar_init(&sh.segment_full[i], 1);
             ptx::mbar_init(&sh.segment_empty[i], 4 * Z::kTiles + 5);     // warps
@@ -775,19 +790,21 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 1) tc_
     if (warp < kCopyWarp) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         if (warp / 4 < Z::kTiles) {
-            Softmax<T, DP> softmax{p, sh, tmem + ((uint32_t)(warp % 4 * 32) << 16), warp / 4};
+            Softmax<T, DP, kPolled> softmax{p, sh, tmem + ((uint32_t)(warp % 4 * 32) << 16), warp / 4};
             ok = softmax.run();
         }
     } else {
         if (warp < kMmaWarp) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
-            Copier<T, DP> copier{p, sh, q_smem, kv_smem};
+            Copier<T, DP, kPolled> copier{p, sh, q_smem, kv_smem};
             ok = copier.run();
-            copy_wait<0>();
+            // Copies that nobody waits for any more: all that this thread began, and their arrivals.
+            copier.arrive(&sh.copied);
+            ok &= ptx::mbar_wait_warp(&sh.copied, 0, kChunkWaitLimitNs, nullptr);
         } else {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
             if (warp == kMmaWarp) {
-                    Multiplier<T, DP> multiplier{p, sh, q_smem, kv_smem, tmem};
+                Multiplier<T, DP, kPolled> multiplier{p, sh, q_smem, kv_smem, tmem};
                 ok = multiplier.run();
             } else if (warp == kScheduleWarp) {
                 ok = schedule<Z::kRows, Z::kSlots>(p, sh, costs);
@@ -798,7 +815,7 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 1) tc_
     if (warp == kMmaWarp) {
         // Products that nobody waits for any more.
         if (ptx::elect_one()) ptx::mma_commit(&sh.drained);
-        ptx::mbar_wait_warp(&sh.drained, 0, kWaitLimitNs, nullptr);
+        if (!ptx::mbar_wait_warp(&sh.drained, 0, kChunkWaitLimitNs, nullptr)) give_up(sh, p);
     }
     ptx::tc_fence_before();
     __syncthreads();
@@ -806,12 +823,13 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 1) tc_
     if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, 512);
 }
 
-template <typename T, int DP> cudaError_t launch_tc(const ctr_attn_s *pl, const ChunkParams &p, cudaStream_t st) {
+template <typename T, int DP, bool kPolled>
+cudaError_t launch_tc(const ctr_attn_s *pl, const ChunkParams &p, cudaStream_t st) {
     typedef Sizes<DP> Z;
-    static_assert(Z::kSmem + sizeof(Shared) <= 227 * 1024, "shared memory");
+    static_assert(Z::kSmem + sizeof(Shared<kPolled>) <= 227 * 1024, "shared memory");
     static_assert(kMaxB * sizeof(int64_t) <= Z::kQ, "costs");
     static PerDeviceOnce once;
-    const auto kernel = tc_kernel<T, DP>;
+    const auto kernel = tc_kernel<T, DP, kPolled>;
     cudaError_t e = once.run(current_device(), cudaSuccess, [&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::kSmem);
     });
@@ -822,9 +840,14 @@ template <typename T, int DP> cudaError_t launch_tc(const ctr_attn_s *pl, const 
     return launch_join<T, Z::kRows>(p, pl->num_sms, st);
 }
 
+template <typename T, bool kPolled>
+cudaError_t launch_by_size(const ctr_attn_s *pl, const ChunkParams &p, cudaStream_t st) {
+    return p.D <= 64 ? launch_tc<T, 64, kPolled>(pl, p, st) : p.D <= 128 ? launch_tc<T, 128, kPolled>(pl, p, st)
+                                                                         : launch_tc<T, 256, kPolled>(pl, p, st);
+}
 template <typename T> cudaError_t launch_16(const ctr_attn_s *pl, const ChunkParams &p, cudaStream_t st) {
-    return p.D <= 64 ? launch_tc<T, 64>(pl, p, st) : p.D <= 128 ? launch_tc<T, 128>(pl, p, st)
-                                                                : launch_tc<T, 256>(pl, p, st);
+    return p.wait_limit_ns == kChunkWaitLimitNs ? launch_by_size<T, false>(pl, p, st)
+                                                : launch_by_size<T, true>(pl, p, st);
 }
 
 }  // namespace chunk

@@ -72,6 +72,7 @@ ctr_status ctr_attn_create(ctr_attn_t *out, int64_t B, int64_t H_q, int64_t H_kv
     pl->layout = CTR_CACHE_HEAD_MAJOR;
     pl->scale = (float)(1.0 / std::sqrt((double)D));
     pl->num_sms = ctr::device_sms();
+    pl->wait_limit_ns = ctr::kChunkWaitLimitNs;
     layout_workspace(pl);
     *out = pl;
     return CTR_OK;
@@ -107,6 +108,12 @@ ctr_status ctr_attn_set_chunks(ctr_attn_t pl, int enable) {
     if (!pl || (enable != 0 && enable != 1)) return CTR_ERR_INVALID_ARG;
     pl->chunks = enable;
     layout_workspace(pl);
+    return CTR_OK;
+}
+
+ctr_status ctr_attn_set_wait_limit_ns(ctr_attn_t pl, uint64_t limit_ns) {
+    if (!pl) return CTR_ERR_INVALID_ARG;
+    pl->wait_limit_ns = limit_ns;
     return CTR_OK;
 }
 
@@ -228,6 +235,7 @@ ctr_status ctr_attn_forward_chunk(ctr_attn_t pl, const void *q, int64_t q_stride
     p.scale_log2 = (float)((double)pl->scale * 1.4426950408889634);
     p.page_shift = ctr::page_shift(pl->page);
     p.whole = pl->max_pages * pl->page <= ctr::kWholeSlots;
+    p.wait_limit_ns = pl->wait_limit_ns;
     return ctr::launch_chunk(pl, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? CTR_OK : CTR_ERR_CUDA;
 }
 

@@ -17,6 +17,7 @@ struct ctr_attn_s {
     void *ws;
     size_t ws_bytes;
     int ready;               // ctr_attn_reset ran on the bound workspace
+    uint64_t wait_limit_ns;
 };
 
 namespace ctr {
@@ -88,6 +89,7 @@ struct ChunkParams {
     float scale_log2;
     int page_shift;          // log2 of the page size, or -1
     int whole;               // units are not cut
+    uint64_t wait_limit_ns;  // of a role's wait for another
 };
 
 // A chunk attention's launch: rows of a tile, and blocks an SM.
@@ -95,6 +97,9 @@ struct ChunkShape {
     int rows, per_sm;
 };
 ChunkShape chunk_shape(int dtype, int64_t D);
+
+// Default limit of a role's wait for another in the chunk attention: a unit of 2^28 slots takes 6 s.
+constexpr uint64_t kChunkWaitLimitNs = 10000000000;
 
 // Most blocks an SM that an attention launch has; the workspace holds two parts for each.
 constexpr int kMaxPerSm = 4;

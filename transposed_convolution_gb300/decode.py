@@ -333,9 +333,12 @@ class PagedAttention(_DecodePlan):
             raise _ctr.CtrError(st, "ctr_attn_evict")
         return slots, lens_out, weights_out
 
+    def set_wait_limit_ns(self, ns):
+        _ctr.ctr_attn_set_wait_limit_ns(self.handle, ns)
+
     def check(self, stream=None):
         """Wait for ``stream`` and raise CtrError when a call met a page number, a slot, a length or
-        a start out of range."""
+        a start out of range, or a kernel gave up waiting for its own copies or products."""
         _ctr.ctr_attn_check(self.handle, self._stream(stream))
 
     def describe(self) -> str:
