@@ -622,9 +622,10 @@ ctr_status ctr_attn_forward(ctr_attn_t plan, const void *q, int64_t q_stride, co
  * with weights accumulates none here.
  *
  * Scores, softmax statistics and sums are fp32; the probabilities of 16-bit caches are rounded once to the
- * dtype for the product with V (fp16: down to 2^-37 of the largest); out is rounded once.  The result does
- * not depend on timing.  What a row does not attend to never reaches it, infinities and NaN in V and
- * stale rows included; an infinite V that a row attends to makes that output infinite (a weight below
+ * dtype for the product with V (8 bits in bf16, 11 in fp16, where ctr_attn_forward keeps 15; fp16: to multiples of
+ * 2^-37 of the largest, and to one at least where all rows of a tile attend to the slot); out is rounded
+ * once.  The result does not depend on timing.  What a row does not attend to never reaches it, infinities and
+ * NaN in V and stale rows included; an infinite V that a row attends to makes that output infinite (a weight below
  * 2^-126 of the row's largest counts as 0 and gives NaN), a NaN or +inf score makes the head's outputs NaN, and
  * a row without slots or whose scores are all -inf gives 0.  Page numbers out of range hide their slots.
  * starts out of order or range make their sequence empty, and tokens past the table's capacity
@@ -677,8 +678,9 @@ void ctr_attn_destroy(ctr_attn_t plan);
  *                             at least 0 and at most 1: pairs that turn fewer than `low` times over
  *                             `original` positions are scaled, those of more than `high` turns are not
  *
- * or frequencies of the caller's own.  Angles are exact to 2^-32 turn plus the position times the 53-bit
- * rounding of f_i; the products are fp32, rounded once to the dtype.  Positions are int32; a
+ * or frequencies of the caller's own (a ramp over the pair's number instead of its turns, for one).  Angles are
+ * reduced to at most half a turn, to 2^-32 turn plus the position times the 53-bit rounding of f_i, and then rounded to
+ * fp32, which is 2^-26 turn at most; the products are fp32, rounded once to the dtype.  Positions are int32; a
  * negative one turns backwards, so that a call with the negated positions is the transpose
  * (the gradient of a call with respect to its input, from the gradient of its output).
  * ------------------------------------------------------------------------------------ */

@@ -3,8 +3,11 @@
 // Two products of 64 rows by 64 slots by D a tile, as fp32 multiply-adds on the CUDA cores, which bound
 // it: a thread has 4 x 4 scores and 4 x D / 16 outputs, so that 64 multiply-adds go to eight 16-byte
 // loads from shared memory, two an instruction.  6 sequences of 100 to 311 tokens with a window of 750, 16/8
-// heads of 80: 164 us (24 TFLOP/s); 512 tokens on 4096, 32/8 heads of 128: 986 us (37).  (The tensor pipe's accumulation, even of tf32 terms that add up to fp32,
-// truncates, which would cost the result digits.)
+// heads of 80: 164 us (24 TFLOP/s); 512 tokens on 4096, 32/8 heads of 128: 986 us (37).  What keeps it from the
+// multiply-adds' rate: one buffer of K and V, so that copies and products take turns; at two blocks an SM
+// (128 registers) a few spills (12 to 104 bytes a thread; none where D > 128); and 80 columns are five a thread, an odd
+// number, whose second product goes one multiply-add an instruction.  (The tensor pipe's accumulation, even of tf32
+// terms that add up to fp32, truncates, which would cost the result digits.)
 #include <algorithm>
 
 #include "chunk_device.cuh"

@@ -15,10 +15,12 @@
 // and V is read as it lies, [slots][columns], as a column-major operand.  With one tile of rows the
 // two S buffers alternate instead.
 //
-// 512 tokens on 65531 cached ones, 32/8 heads of 128, bf16: 433 us (1275 TFLOP/s, 64% of cuBLAS's measured
-// rate); without the softmax 343, the products alone 307.  8192 tokens: 489 us.  2048 tokens on 16384: 407 us for
-// heads of 64 (the softmax bounds it), 453 for 128, 988 for 256.  16 single tokens on 8192 slots each: 97 us (5.5
-// TB/s).  4 tokens on 125: 9.8 us.
+// 512 tokens on 65531 cached ones, 32/8 heads of 128, bf16: 485 to 494 us (1.13 PFLOP/s, 57% of cuBLAS's measured
+// rate) through the API with inputs in turn, 433 to 447 in a captured graph of one call again and again.  Its K and V,
+// 270 MB, do not fit the L2, and the row tiles of a head walk them at different times: 2.16 GB come from memory.  Of
+// the 433, without the softmax 343, the products alone 307.  8192 tokens: 493 us.  In graphs, 2048 tokens on
+// 16384: 409 us for heads of 64 (the softmax bounds it), 453 for 128, 985 for 256.  16 single tokens on 8192 slots
+// each: 98 us (5.5 TB/s).  4 tokens on 125: 10 to 11 us.
 //
 // Softmax: powers of two of a score's distance to the row's base, which follows the running maximum only when
 // that exceeds it by kSlack, because then O has to be rescaled in TMEM, which the tensor pipe waits

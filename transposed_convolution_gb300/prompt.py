@@ -24,8 +24,10 @@ class Rotary(_DecodePlan):
 
     Pair i turns by base ** (-2i / rotary_dim) radians a position.  ``scaling`` "linear" divides that
     by ``factor``; "parts" divides it for pairs that turn fewer than ``low`` times over ``original``
-    positions, leaves those of more than ``high`` turns, and blends between; ``frequencies`` gives
-    all of them instead.  ``magnitude`` multiplies what is turned."""
+    positions, leaves those of more than ``high`` turns, and blends between, in proportion to the turns;
+    ``frequencies`` gives all of them instead (for a blend in proportion to the pair's number, as many models
+    were trained with: such a model's come out otherwise with "parts").  ``magnitude`` multiplies what is
+    turned."""
 
     def __init__(self, D, rotary_dim=None, layout="half", base=10000.0, scaling=None, factor=1.0,
                  original=None, low=1.0, high=32.0, magnitude=1.0, frequencies=None, dtype=None,
