@@ -847,6 +847,8 @@ __global__ void __launch_bounds__(32 * C::Shape::kWarps, C::Shape::kPerSm) atten
             }
             if (whole) {
                 const float r = sum > 0.0f ? 1.0f / sum : 0.0f;
+                // (A head without weight is 0 whatever V holds: 0 times an infinity would be NaN.)
+                if (sum == 0.0f) v = make_float4(0.f, 0.f, 0.f, 0.f);
                 store4(static_cast<T *>(p.out) + (h0 + head) * D + d, v.x * r, v.y * r, v.z * r, v.w * r);
                 if (p.scores && d == 0) p.stats[h0 + head] = make_float2(top, sum);
             } else {
@@ -981,10 +983,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(AttnParams p, int
     }
     const float r = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+    for (int i = 0; i < N; ++i) {
+        if (sum == 0.0f) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (d + i * 128 < p.D)
             store4(static_cast<T *>(p.out) + row_no * p.D + d + i * 128, v[i].x * r, v[i].y * r, v[i].z * r,
                    v[i].w * r);
+    }
     if (p.scores && lane == 0) p.stats[row_no] = make_float2(top, sum);
 }
 
